@@ -297,6 +297,198 @@ int moonep_swiglu_backward(const moonep_shape* shape, const void* h_saved, const
                            void* dh, void* stream);
 
 /*
+ * ---- Router ------------------------------------------------------------------
+ * From a router's logits to the plan's input: the experts and gates of every token,
+ * and from the gates' gradient back to the logits'.
+ */
+enum { MOONEP_SOFTMAX = 0, MOONEP_SIGMOID = 1 };
+typedef struct moonep_router {
+  int32_t score;      /* MOONEP_SOFTMAX (over the experts) or MOONEP_SIGMOID */
+  int32_t dtype;      /* of the logits and their gradient: MOONEP_BF16 or MOONEP_FP32 */
+  int32_t groups;     /* the E experts form this many groups of consecutive ids (1: no groups) */
+  int32_t top_groups; /* groups whose experts may be chosen, 1 .. groups */
+  int32_t group_top;  /* a group's score: the sum of its 1 or 2 best experts' scores */
+  int32_t renorm;     /* 1: a token's gates are divided by their sum */
+  float scale;        /* positive factor of every gate */
+} moonep_router;
+
+/*
+ * Choose every token's K experts.
+ *   logits    in   router->dtype [N, E]
+ *   bias      in   NULL, or float32 [E]: added to the scores for the choice alone (the
+ *                  gates do not see it); -inf switches an expert off
+ *   topk_idx  out  int32 [N, K]: best first, moonep_plan's input
+ *   gates     out  float32 [N, K]
+ * The rule, for one token with logits l:
+ *   An expert is masked where its logit or its bias is -inf. s = sigmoid(l), or the
+ *   softmax of l over the experts whose bias is not -inf. Experts are ranked by s + bias
+ *   (without a bias by l itself, whose order s keeps), compared in float64, ties to the
+ *   lower id. With groups, a group's score is the best value of that ranking in it
+ *   (group_top 1), or the sum of the two largest s + bias of its unmasked experts
+ *   (group_top 2; of the one there is, if it has one); the top_groups best groups stay, ties to
+ *   the lower group, and the experts of the others rank as masked. Masked experts, and
+ *   any whose rank is not a number, come last in ascending id: they are chosen only
+ *   where fewer than K others are left, and get the gate 0.
+ *   gate = scale * s, divided (renorm) by the sum of s over the chosen experts that are
+ *   not masked. Float32; with renorm it is formed relative to the largest chosen score,
+ *   so that very low logits do not give 0 / 0. A token with nothing left to choose gets
+ *   K distinct valid ids and gates of 0.
+ *   A NaN among the logits (or biases, -inf bias excepted: a switched-off expert's logit
+ *   is not read as a number), or with SOFTMAX a +inf, makes all gates of the token NaN;
+ *   its ids are still distinct and valid.
+ * Requires K <= top_groups * (E / groups), group_top <= E / groups where groups > 1, and
+ * a finite scale > 0 (MOONEP_EINVAL); groups <= 64 (MOONEP_ELIMIT).
+ */
+int moonep_route(const moonep_shape* shape, const moonep_router* router, const void* logits,
+                 const float* bias, int32_t* topk_idx, float* gates, void* stream);
+
+/*
+ * Gradient of the logits from the gates' gradient; the choice itself is a constant.
+ * With g the gates, q = g / scale and dg their gradient (sums over the token's choices):
+ *   SOFTMAX, renorm     dl_e = g_e (dg_e - sum q dg)             for chosen e, else 0
+ *   SIGMOID, renorm     dl_e = g_e (dg_e - sum q dg) (1 - s_e)   for chosen e, else 0
+ *   SIGMOID             dl_e = g_e dg_e (1 - s_e)                for chosen e, else 0
+ *   SOFTMAX             dl_e = g_e dg_e - s_e sum g dg           for every e
+ * in float32, rounded once to router->dtype.
+ *   logits, bias, topk_idx, gates  in   as moonep_route took and gave them
+ *   dgates                         in   float32 [N, K]
+ *   dlogits                        out  router->dtype [N, E], every element written
+ * A choice whose gate is 0 (a masked one) has no gradient, and its dgates is not used. A
+ * topk_idx entry outside [0, E) is skipped; an id named twice adds both. Training layers
+ * only.
+ */
+int moonep_route_backward(const moonep_shape* shape, const moonep_router* router,
+                          const void* logits, const float* bias, const int32_t* topk_idx,
+                          const float* gates, const float* dgates, void* dlogits, void* stream);
+
+/*
+ * Gradient of the gates of moonep_combine: dgates[g][k] = <dy[g], src[slot_map[g*K+k]]>,
+ * float32, in a fixed order.
+ *   width   H or Hp
+ *   src     in   float32 [R*SK, width]: what moonep_combine read
+ *   dy      in   dtype [N, width]: the gradient of its output
+ *   dgates  out  float32 [N, K]; 0 where slot_map is negative
+ * Training layers only.
+ */
+int moonep_gate_grad(const moonep_shape* shape, int32_t width, const float* src,
+                     const int32_t* slot_map, const void* dy, float* dgates, void* stream);
+
+/*
+ * ---- 8-bit activation checkpoints -----------------------------------------------
+ * What a training layer keeps from its forward to its backward pass, in 8 bits: the
+ * input x (one row per token, not per slot) and the gate/up pre-activation h. The
+ * backward pass permutes x again from its checkpoint and forms the activation again
+ * from h's, so the slot buffers xp and act need not be kept.
+ * Format: a checkpoint of rows of `width` values is
+ *   q       uint8 [rows, width]: OCP e4m3 values
+ *   scales  uint8 [rows, 4*ceil(width/128)]: one E8M0 scale (2^(byte-127), 255 = NaN) per
+ *           32 consecutive columns, the last block possibly shorter; bytes past
+ *           ceil(width/32) are written 0.
+ * The scale of a block is the smallest power of two (at least 2^-127) that clips none of
+ * its values, and values are rounded to nearest even: off by at most 2^-4 of the value,
+ * or 2^-10 of the scale where that is more. A block that holds an Inf or a NaN becomes NaN.
+ */
+
+/* Checkpoint of token rows: src dtype [N, width], width H or Hp. */
+int moonep_checkpoint_quantize(const moonep_shape* shape, int32_t width, const void* src,
+                               uint8_t* q, uint8_t* scales, void* stream);
+
+/*
+ * moonep_dispatch (without gates) from a checkpoint of the tokens: dst[slot_map[u]] =
+ * the values of row u / K, rounded to dtype (exact but for bfloat16 subnormals).
+ * Slots whose slot_map entry is negative are skipped.
+ */
+int moonep_checkpoint_dispatch(const moonep_shape* shape, int32_t width, const uint8_t* q,
+                               const uint8_t* scales, const int32_t* slot_map, void* dst,
+                               void* stream);
+
+/*
+ * moonep_swiglu whose saved pre-activation is a checkpoint: act as there; q and scales
+ * hold h, [R*SK, 2*Hp] wide (interleaved, so every block is 32 gate or 32 up columns).
+ * Requires Hp a multiple of 32.
+ */
+int moonep_swiglu_checkpoint(const moonep_shape* shape, const float* h, void* act, uint8_t* q,
+                             uint8_t* scales, void* stream);
+
+/*
+ * moonep_grouped_gemm_swiglu whose saved pre-activation is a checkpoint, without the
+ * float32 h in memory: the same bits as moonep_grouped_gemm(FWD, up shape) followed by
+ * moonep_swiglu_checkpoint. bfloat16 layers only (MOONEP_EINVAL otherwise). Requires H a
+ * multiple of 64 and Hp a multiple of 64.
+ */
+int moonep_grouped_gemm_swiglu_checkpoint(const moonep_shape* shape, const void* xp,
+                                          const void* w1_all, const int32_t* cu_seqlens, void* act,
+                                          uint8_t* q, uint8_t* scales, void* ws, size_t ws_bytes,
+                                          void* stream);
+
+/*
+ * SwiGLU backward from a checkpoint. With gate and up the checkpoint's values,
+ *   a = silu(gate) * up,   dh as moonep_swiglu_backward, both in float32.
+ * Without gates (NULL; src_index and dgates must then be NULL too), da is the gradient of
+ * act and
+ *   act  out  dtype [R*SK, Hp]: a, the operand of WGRAD(W2)
+ *   dh   out  dtype [R*SK, 2*Hp]
+ * With gates (float32 [N, K]), da is the DGRAD of dY permuted without gates, and the call
+ * also gives the gates' gradient, which then needs no float32 expert output:
+ *   dgates[u] = <a, da> of the slot u at each position (src_index from moonep_plan);
+ *   act  = gate_u * a   (WGRAD(W2) with the dY permuted without gates: the same product)
+ *   dh   = gate_u * dh
+ * A position whose src_index is not in [0, N*K) gets act = dh = 0 and writes no dgates.
+ *   da  in  float32 [R*SK, Hp]
+ * Requires Hp a multiple of 32. Training layers only.
+ */
+int moonep_swiglu_backward_checkpoint(const moonep_shape* shape, const uint8_t* q,
+                                      const uint8_t* scales, const float* da,
+                                      const int32_t* src_index, const float* gates, void* act,
+                                      void* dh, float* dgates, void* stream);
+
+/*
+ * ---- Experts in 4 bits -----------------------------------------------------------
+ * MXFP4 operands for serving: OCP e2m1 values with one E8M0 scale per 32 consecutive
+ * values along the reduction (H), chosen and rounded as in the checkpoints above (off by
+ * at most 2^-2 of the value, or 2^-2 of the scale where that is more). With T = ceil(H/128) k-tiles and
+ * C = ceil(H/512) k-chunks (padding is zero):
+ *   token rows   q       uint8 [rows, 64*T]: value k is nibble k % 2 (0 = low) of byte k / 2
+ *                scales  uint8 [rows, 16*C]: the scale of block b = k / 32 is byte
+ *                        16*(b/16) + 4*(b%4) + (b/4)%4
+ *   weights      q       uint8 [E+R*B, Hp/16, T, 64, 16]: value (k, n) is nibble k % 2 of
+ *                        byte (k%32)/2 of lane 16*((k/32)%4) + n%16 of tile (n/16, k/128)
+ *                scales  uint8 [E+R*B, Hp/16, C, 64, 4]: of block k / 32 of column n, byte
+ *                        (k/128)%4 of that lane of (n/16, k/512)
+ * rows as in W_all: E home experts, then every rank's prefetch slots.
+ */
+
+/* Quantise `rows` rows of `width` values (dtype) to token rows; width a multiple of 32. */
+int moonep_mx_quantize(const moonep_shape* shape, int64_t rows, int32_t width, const void* src,
+                       uint8_t* q, uint8_t* scales, void* stream);
+
+/* Quantise the E home experts of w, dtype [E, H, Hp], to weights' rows 0..E-1 (a set-up
+ * call). Requires Hp a multiple of 16 and H of 32. */
+int moonep_mx_quantize_weight(const moonep_shape* shape, const void* w, uint8_t* wq,
+                              uint8_t* wscales, void* stream);
+
+/* moonep_prefetch_weight on 4-bit weights. Requires Hp a multiple of 16. */
+int moonep_mx_prefetch_weight(const moonep_shape* shape, const int32_t* replica_expert,
+                              uint8_t* wq, uint8_t* wscales, void* stream);
+
+/*
+ * Grouped GEMM (forward) on 4-bit operands with float32 accumulation:
+ *   c[position of (q,i)] = x[row of the position] @ view_q(i)
+ *   xq, xscales  in   token rows of width H: with src_index (from moonep_plan) one row per
+ *                     token, [N, ..], and position p reads row src_index[p] / K (no permute
+ *                     is needed); with src_index NULL one row per position, [R*SK, ..]
+ *   wq, wscales  in   weights
+ *   c            out  float32 [R*SK, Hp]
+ * A position whose src_index is not in [0, N*K) gives a row of zeros. Requires H and Hp
+ * multiples of 64. shape->dtype plays no part. The workspace is shared with the layer's
+ * other calls.
+ */
+int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* xq, const uint8_t* xscales,
+                           const int32_t* src_index, const uint8_t* wq, const uint8_t* wscales,
+                           const int32_t* cu_seqlens, float* c, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/*
  * ---- Process-global prefetch-slot pool ----------------------------------------
  * The prefetch slots of every layer come from one process-global pool, so the
  * extra memory is R*B expert weights per projection in total, not per layer,

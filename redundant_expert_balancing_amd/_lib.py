@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(_HERE, "libmoonep.so")
 TRAIN, INFER = 0, 1
 BF16, FP32 = 0, 1
 FWD, DGRAD, WGRAD = 0, 1, 2
+SOFTMAX, SIGMOID = 0, 1
 ERR_ID_RANGE, ERR_ID_DUP = 1, 2
 OK, EINVAL, EWORKSPACE, EHIP, EMODE, ELIMIT = 0, -1, -2, -3, -4, -5
 
@@ -25,6 +26,11 @@ EXPORTS = (
     "moonep_workspace_init", "moonep_plan", "moonep_prefetch_weight", "moonep_dispatch",
     "moonep_grouped_gemm", "moonep_grouped_gemm_noalloc", "moonep_combine", "moonep_reduce_grad", "moonep_get_error",
     "moonep_swiglu", "moonep_grouped_gemm_swiglu", "moonep_swiglu_backward",
+    "moonep_route", "moonep_route_backward", "moonep_gate_grad",
+    "moonep_checkpoint_quantize", "moonep_checkpoint_dispatch", "moonep_swiglu_checkpoint",
+    "moonep_grouped_gemm_swiglu_checkpoint", "moonep_swiglu_backward_checkpoint",
+    "moonep_mx_quantize", "moonep_mx_quantize_weight", "moonep_mx_prefetch_weight",
+    "moonep_mx_grouped_gemm",
     "moonep_vm_granularity", "moonep_pool_create", "moonep_pool_bytes", "moonep_pool_destroy",
     "moonep_view_create", "moonep_view_destroy",
 )
@@ -43,6 +49,12 @@ class Shape(ctypes.Structure):
                    BF16 if cfg.dtype == "bf16" else FP32)
 
 
+class Router(ctypes.Structure):
+    """moonep_router."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "dtype", "groups", "top_groups",
+                                              "group_top", "renorm")] + [("scale", ctypes.c_float)]
+
+
 class MoonepError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} failed: {status} ({strerror(status)})")
@@ -52,6 +64,7 @@ class MoonepError(RuntimeError):
 _lib = None
 _vp = ctypes.c_void_p
 _sp = ctypes.POINTER(Shape)
+_rp = ctypes.POINTER(Router)
 
 
 def lib() -> ctypes.CDLL:
@@ -83,6 +96,21 @@ def lib() -> ctypes.CDLL:
             "moonep_grouped_gemm_swiglu": ([_sp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                                             _vp], ctypes.c_int),
             "moonep_swiglu_backward": ([_sp, _vp, _vp, _vp, _vp], ctypes.c_int),
+            "moonep_route": ([_sp, _rp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+            "moonep_route_backward": ([_sp, _rp] + [_vp] * 7, ctypes.c_int),
+            "moonep_gate_grad": ([_sp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+            "moonep_checkpoint_quantize": ([_sp, ctypes.c_int32, _vp, _vp, _vp, _vp], ctypes.c_int),
+            "moonep_checkpoint_dispatch": ([_sp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp],
+                                           ctypes.c_int),
+            "moonep_swiglu_checkpoint": ([_sp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+            "moonep_grouped_gemm_swiglu_checkpoint": ([_sp] + [_vp] * 7 + [ctypes.c_size_t, _vp],
+                                                      ctypes.c_int),
+            "moonep_swiglu_backward_checkpoint": ([_sp] + [_vp] * 9, ctypes.c_int),
+            "moonep_mx_quantize": ([_sp, ctypes.c_int64, ctypes.c_int32, _vp, _vp, _vp, _vp],
+                                   ctypes.c_int),
+            "moonep_mx_quantize_weight": ([_sp, _vp, _vp, _vp, _vp], ctypes.c_int),
+            "moonep_mx_prefetch_weight": ([_sp, _vp, _vp, _vp, _vp], ctypes.c_int),
+            "moonep_mx_grouped_gemm": ([_sp] + [_vp] * 8 + [ctypes.c_size_t, _vp], ctypes.c_int),
             "moonep_vm_granularity": ([], ctypes.c_size_t),
             "moonep_pool_create": ([_sp, ctypes.c_int32, ctypes.POINTER(_vp)], ctypes.c_int),
             "moonep_pool_bytes": ([_vp], ctypes.c_size_t),
@@ -287,6 +315,175 @@ def moonep_swiglu_backward(shape, h_saved, da, dh, stream=None):
     _check("moonep_swiglu_backward", lib().moonep_swiglu_backward(
         ctypes.byref(shape), _p(h_saved, NK * 2 * Hp * eb, "h_saved", a),
         _p(da, 4 * NK * Hp, "da", _f32()), _p(dh, NK * 2 * Hp * eb, "dh", a), _s(stream)))
+
+
+# ---- router, gates' gradient, 8-bit checkpoints, 4-bit experts
+def _q(t, nbytes, name, dtype):
+    """_p for the calls below, which also refuse a missing tensor and one that is not on
+    the current device (whose stream the call goes to)."""
+    if t is None:
+        raise ValueError(f"{name}: a tensor is required")
+    p = _p(t, nbytes, name, dtype)
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return p
+
+
+def _u8():
+    import torch
+    return torch.uint8
+
+
+def _logit(router: Router):
+    import torch
+    return (torch.bfloat16, 2) if router.dtype == BF16 else (torch.float32, 4)
+
+
+def moonep_route(shape, router, logits, bias, topk_idx, gates, stream=None):
+    N, NK, _, _ = _dims(shape)
+    dt, lb = _logit(router)
+    _check("moonep_route", lib().moonep_route(
+        ctypes.byref(shape), ctypes.byref(router), _q(logits, N * shape.E * lb, "logits", dt),
+        None if bias is None else _q(bias, 4 * shape.E, "bias", _f32()),
+        _q(topk_idx, 4 * NK, "topk_idx", _i32()), _q(gates, 4 * NK, "gates", _f32()), _s(stream)))
+
+
+def moonep_route_backward(shape, router, logits, bias, topk_idx, gates, dgates, dlogits,
+                          stream=None):
+    N, NK, _, _ = _dims(shape)
+    dt, lb = _logit(router)
+    _check("moonep_route_backward", lib().moonep_route_backward(
+        ctypes.byref(shape), ctypes.byref(router), _q(logits, N * shape.E * lb, "logits", dt),
+        None if bias is None else _q(bias, 4 * shape.E, "bias", _f32()),
+        _q(topk_idx, 4 * NK, "topk_idx", _i32()), _q(gates, 4 * NK, "gates", _f32()),
+        _q(dgates, 4 * NK, "dgates", _f32()), _q(dlogits, N * shape.E * lb, "dlogits", dt),
+        _s(stream)))
+
+
+def moonep_gate_grad(shape, width, src, slot_map, dy, dgates, stream=None):
+    N, NK, _, eb = _dims(shape)
+    w = int(width)
+    _check("moonep_gate_grad", lib().moonep_gate_grad(
+        ctypes.byref(shape), w, _q(src, 4 * NK * w, "src", _f32()),
+        _q(slot_map, 4 * NK, "slot_map", _i32()), _q(dy, N * w * eb, "dy", _act(shape)),
+        _q(dgates, 4 * NK, "dgates", _f32()), _s(stream)))
+
+
+def checkpoint_scale_bytes(width: int) -> int:
+    """Bytes of a checkpoint row's scales."""
+    return 4 * -(-width // 128)
+
+
+def moonep_checkpoint_quantize(shape, width, src, q, scales, stream=None):
+    N, _, _, eb = _dims(shape)
+    w = int(width)
+    _check("moonep_checkpoint_quantize", lib().moonep_checkpoint_quantize(
+        ctypes.byref(shape), w, _q(src, N * w * eb, "src", _act(shape)), _q(q, N * w, "q", _u8()),
+        _q(scales, N * checkpoint_scale_bytes(w), "scales", _u8()), _s(stream)))
+
+
+def moonep_checkpoint_dispatch(shape, width, q, scales, slot_map, dst, stream=None):
+    N, NK, _, eb = _dims(shape)
+    w = int(width)
+    _check("moonep_checkpoint_dispatch", lib().moonep_checkpoint_dispatch(
+        ctypes.byref(shape), w, _q(q, N * w, "q", _u8()),
+        _q(scales, N * checkpoint_scale_bytes(w), "scales", _u8()),
+        _q(slot_map, 4 * NK, "slot_map", _i32()), _q(dst, NK * w * eb, "dst", _act(shape)),
+        _s(stream)))
+
+
+def _checkpoint_h(shape, q, scales):
+    _, NK, _, _ = _dims(shape)
+    w = 2 * shape.Hp
+    return (_q(q, NK * w, "q", _u8()),
+            _q(scales, NK * checkpoint_scale_bytes(w), "scales", _u8()))
+
+
+def moonep_swiglu_checkpoint(shape, h, act, q, scales, stream=None):
+    _, NK, _, eb = _dims(shape)
+    Hp = shape.Hp
+    _check("moonep_swiglu_checkpoint", lib().moonep_swiglu_checkpoint(
+        ctypes.byref(shape), _q(h, 4 * NK * 2 * Hp, "h", _f32()),
+        _q(act, NK * Hp * eb, "act", _act(shape)), *_checkpoint_h(shape, q, scales), _s(stream)))
+
+
+def moonep_grouped_gemm_swiglu_checkpoint(shape, xp, w1_all, cu_seqlens, act, q, scales, ws,
+                                          stream=None):
+    _, NK, _, eb = _dims(shape)
+    H, Hp, a = shape.H, shape.Hp, _act(shape)
+    _check("moonep_grouped_gemm_swiglu_checkpoint", lib().moonep_grouped_gemm_swiglu_checkpoint(
+        ctypes.byref(shape), _q(xp, NK * H * eb, "xp", a),
+        _q(w1_all, (shape.E + shape.R * shape.B) * H * 2 * Hp * eb, "w1_all", a),
+        _q(cu_seqlens, 4 * shape.R * (shape.E + shape.B + 1), "cu_seqlens", _i32()),
+        _q(act, NK * Hp * eb, "act", a), *_checkpoint_h(shape, q, scales),
+        _q(ws, moonep_workspace_bytes(shape), "ws", None), _nbytes(ws), _s(stream)))
+
+
+def moonep_swiglu_backward_checkpoint(shape, q, scales, da, src_index, gates, act, dh, dgates,
+                                      stream=None):
+    _, NK, _, eb = _dims(shape)
+    Hp, a = shape.Hp, _act(shape)
+    opt = [None if t is None else _q(t, 4 * NK, name, dt) for t, name, dt in
+           ((src_index, "src_index", _i32()), (gates, "gates", _f32()), (dgates, "dgates", _f32()))]
+    _check("moonep_swiglu_backward_checkpoint", lib().moonep_swiglu_backward_checkpoint(
+        ctypes.byref(shape), *_checkpoint_h(shape, q, scales), _q(da, 4 * NK * Hp, "da", _f32()),
+        opt[0], opt[1], _q(act, NK * Hp * eb, "act", a), _q(dh, NK * 2 * Hp * eb, "dh", a), opt[2],
+        _s(stream)))
+
+
+def mx_row_bytes(width: int):
+    """Bytes of one token row's values and of its scales."""
+    return 64 * -(-width // 128), 16 * -(-width // 512)
+
+
+def mx_weight_bytes(H: int, Hp: int):
+    """Bytes of one expert's values and of its scales."""
+    q, s = mx_row_bytes(H)
+    return Hp * q, Hp * s
+
+
+def moonep_mx_quantize(shape, rows, width, src, q, scales, stream=None):
+    eb = _dims(shape)[3]
+    rows, w = int(rows), int(width)
+    qb, sb = mx_row_bytes(w)
+    _check("moonep_mx_quantize", lib().moonep_mx_quantize(
+        ctypes.byref(shape), rows, w, _q(src, rows * w * eb, "src", _act(shape)),
+        _q(q, rows * qb, "q", _u8()), _q(scales, rows * sb, "scales", _u8()), _s(stream)))
+
+
+def moonep_mx_quantize_weight(shape, w, wq, wscales, stream=None):
+    E, eb = shape.E, _dims(shape)[3]
+    qb, sb = mx_weight_bytes(shape.H, shape.Hp)
+    _check("moonep_mx_quantize_weight", lib().moonep_mx_quantize_weight(
+        ctypes.byref(shape), _q(w, E * shape.H * shape.Hp * eb, "w", _act(shape)),
+        _q(wq, E * qb, "wq", _u8()), _q(wscales, E * sb, "wscales", _u8()), _s(stream)))
+
+
+def _mx_weights(shape, wq, wscales):
+    rows = shape.E + shape.R * shape.B
+    qb, sb = mx_weight_bytes(shape.H, shape.Hp)
+    return _q(wq, rows * qb, "wq", _u8()), _q(wscales, rows * sb, "wscales", _u8())
+
+
+def moonep_mx_prefetch_weight(shape, replica_expert, wq, wscales, stream=None):
+    _check("moonep_mx_prefetch_weight", lib().moonep_mx_prefetch_weight(
+        ctypes.byref(shape), _q(replica_expert, 4 * shape.R * shape.B, "replica_expert", _i32()),
+        *_mx_weights(shape, wq, wscales), _s(stream)))
+
+
+def moonep_mx_grouped_gemm(shape, xq, xscales, src_index, wq, wscales, cu_seqlens, c, ws,
+                           stream=None):
+    N, NK, _, _ = _dims(shape)
+    rows = NK if src_index is None else N
+    qb, sb = mx_row_bytes(shape.H)
+    _check("moonep_mx_grouped_gemm", lib().moonep_mx_grouped_gemm(
+        ctypes.byref(shape), _q(xq, rows * qb, "xq", _u8()), _q(xscales, rows * sb, "xscales", _u8()),
+        None if src_index is None else _q(src_index, 4 * NK, "src_index", _i32()),
+        *_mx_weights(shape, wq, wscales),
+        _q(cu_seqlens, 4 * shape.R * (shape.E + shape.B + 1), "cu_seqlens", _i32()),
+        _q(c, 4 * NK * shape.Hp, "c", _f32()), _q(ws, moonep_workspace_bytes(shape), "ws", None),
+        _nbytes(ws), _s(stream)))
 
 
 def moonep_vm_granularity() -> int:

@@ -77,6 +77,33 @@ __device__ inline uint32_t bf16_rne_bits(float f) {
   return b >> 16;
 }
 
+// The same for any input: a NaN stays one (rounding up its mantissa could carry out of it).
+__device__ inline uint32_t bf16_rne_any(float f) {
+  return f == f ? bf16_rne_bits(f) : 0x7FC0u;
+}
+
+// Block scales (E8M0: the byte is the exponent plus 127, 255 is NaN) of small float types.
+// The scale of a block is the smallest power of two 2^e, e >= -127, with
+// amax <= top * 2^e, so that no value is clipped; top is 448 (e4m3) or 6 (e2m1), given by
+// its exponent and mantissa bits. amax_bits: the largest |value| of the block as bits;
+// integer order ranks Inf and NaN above every number, and either makes the scale NaN.
+struct E4M3 { static constexpr int kTopExp = 8; static constexpr uint32_t kTopMant = 0x600000u; };
+struct E2M1 { static constexpr int kTopExp = 2; static constexpr uint32_t kTopMant = 0x400000u; };
+
+template <typename T>
+__device__ inline uint32_t scale_byte(uint32_t amax_bits) {
+  const int e = int(amax_bits >> 23);
+  if (e == 255) return 255;
+  const int b = e - T::kTopExp + ((amax_bits & 0x7FFFFFu) > T::kTopMant ? 1 : 0);
+  return uint32_t(b < 0 ? 0 : b);
+}
+// 2^-e of a scale byte (at most 254 for a finite block), exact
+__device__ inline float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^e of a scale byte: byte 0 is the subnormal 2^-127
+__device__ inline float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 255 ? 0x7FC00000u : byte ? byte << 23 : 0x400000u);
+}
+
 // SwiGLU in float32: silu(g) * u with silu(g) = g / (1 + e^-g). Every kernel that
 // produces the activation calls this one function, so all of them agree bit for bit.
 __device__ inline float swiglu_f32(float g, float u) { return g / (1.0f + expf(-g)) * u; }
@@ -86,9 +113,29 @@ __device__ inline float swiglu_f32(float g, float u) { return g / (1.0f + expf(-
 // + p % kSwigluBlock and its up projection kSwigluBlock further.
 constexpr int kSwigluBlock = MOONEP_SWIGLU_BLOCK;
 
+// Layouts of the 4-bit expert operands (moonep.h, "Experts in 4 bits"): tiles of 128 and
+// chunks of 512 along the reduction.
+constexpr int kScaleBlock = 32;
+inline int64_t k_tiles(int width) { return (int64_t(width) + 127) / 128; }
+inline int64_t k_chunks(int width) { return (int64_t(width) + 511) / 512; }
+
 // Host-side validation shared by all entry points (defined in api.hip).
 int validate(const moonep_shape* s);
 int elem_bytes(const moonep_shape& s);
 int launch_status();  // MOONEP_OK or MOONEP_EHIP after the last launch
+
+// One work entry of the grouped GEMMs' tile lists (gemm.hip).
+struct TileEntry {
+  int32_t rowbase;  // global buffer row of the segment's first slot: q*SK + cu[q][i]
+  int32_t wrow;     // W_all row (FWD/DGRAD) / grad row (WGRAD: < E grad_home, else reduce_buf+E)
+  int32_t m0;       // first segment row of this entry (FWD/DGRAD), 0 for WGRAD
+  int32_t n;        // segment length
+};
+
+// Enqueues the tile list of `s` and cu_seqlens, M-tiles of bm rows (bm >= kMinTileM), into
+// the workspace (gemm.hip); *tiles and *ntiles receive its device addresses.
+int launch_tile_list(const moonep_shape& s, const int32_t* cu_seqlens, int bm, void* ws,
+                     hipStream_t strm, const TileEntry** tiles, const int32_t** ntiles);
+int device_cus();   // compute units of the current device, 0 on failure
 
 }  // namespace moonep

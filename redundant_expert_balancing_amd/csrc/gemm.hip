@@ -48,13 +48,6 @@ namespace moonep {
 typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8_t;
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float floatx4_t;
 
-struct TileEntry {
-  int32_t rowbase;  // global buffer row of the segment's first slot: q*SK + cu[q][i]
-  int32_t wrow;     // W_all row (FWD/DGRAD) / grad row (WGRAD: < E grad_home, else reduce_buf+E)
-  int32_t m0;       // first segment row of this entry (FWD/DGRAD), 0 for WGRAD
-  int32_t n;        // segment length
-};
-
 // ------------------------------------------------------------------ tile list
 __device__ inline int wave_scan_incl(int v) {
   const int lane = threadIdx.x & 63;
@@ -407,10 +400,21 @@ struct GemmArgs {
   uint16_t* act;      // SwiGLU epilogue: bf16 [rows, Hp/2]
   uint16_t* h_saved;  // SwiGLU epilogue: NULL or bf16 [rows, Hp]
   int32_t* qcnt;      // 8 per-XCD tile-queue counters, zero at launch (NULL: static order)
+  uint8_t* h_q;       // checkpointing SwiGLU epilogue: e4m3 [rows, Hp] and its block scales
+  uint8_t* h_scales;  // [rows, Hp/32]
 };
 
+// The largest of a 16-lane row's values, in every lane of the row.
+__device__ inline uint32_t row16_max(uint32_t v) {
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false)));   // quad_perm 1,0,3,2
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, false)));   // quad_perm 2,3,0,1
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, false)));  // row_half_mirror
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x140, 0xF, 0xF, false)));  // row_mirror
+  return v;
+}
+
 template <int OP, int BM, int BN, int WAVES_M, int WAVES_N, bool SWIGLU = false,
-          bool STREAM_OUT = false, int STAGES = 2, bool HALFN = false>
+          bool STREAM_OUT = false, int STAGES = 2, bool HALFN = false, bool CKPT = false>
 __global__ __launch_bounds__(WAVES_M * WAVES_N * 64) void gemm_bf16_kernel(GemmArgs g) {
   constexpr int NW = WAVES_M * WAVES_N;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
@@ -817,7 +821,43 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64) void gemm_bf16_kernel(GemmA
                                                       la[jp] + rowoff + h * 32, 0, 0);
               }
           }
-        if (g.h_saved) {
+        if constexpr (CKPT) {
+          // e4m3 checkpoint of the pre-activation: blocks 2b, 2b+1 of 16 columns are one
+          // block of 32 (gate or up) columns, whose scale comes from the 16 lanes of a row
+          const __amdgpu_buffer_rsrc_t qrs =
+              make_rsrc(g.h_q + row0 * g.Hp + n0, clamp_bytes(int64_t(rows_valid) * g.Hp));
+          const int srow = g.Hp / 32;
+          const __amdgpu_buffer_rsrc_t srs =
+              make_rsrc(g.h_scales + row0 * srow + n0 / 32, clamp_bytes(int64_t(rows_valid) * srow));
+          uint32_t lq[FN / 2];
+#pragma unroll
+          for (int b = 0; b < FN / 2; ++b)
+            lq[b] = col0 + (b / 2) * 64 < cols_valid
+                        ? lane_rows * g.Hp + uint32_t(col0 + b * 32 + r16) : kOffNone;
+          // lane b of a row stores the scale of block b
+          const uint32_t ls = r16 < FN / 2 && col0 + (r16 / 2) * 64 < cols_valid
+                                  ? lane_rows * srow + uint32_t(col0 / 32 + r16) : kOffNone;
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              uint32_t mine = 0;
+#pragma unroll
+              for (int b = 0; b < FN / 2; ++b) {
+                const float v0 = acc[i][2 * b][r], v1 = acc[i][2 * b + 1][r];
+                const uint32_t sb = scale_byte<E4M3>(row16_max(
+                    max(__float_as_uint(v0) & 0x7FFFFFFFu, __float_as_uint(v1) & 0x7FFFFFFFu)));
+                const float inv = scale_inverse(sb);
+                const int w = sb == 255 ? 0 : __builtin_amdgcn_cvt_pk_fp8_f32(v0 * inv, v1 * inv, 0, false);
+                const uint32_t off = lq[b] + uint32_t(i * 16 + r) * g.Hp;
+                __builtin_amdgcn_raw_buffer_store_b8((unsigned char)w, qrs, off, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b8((unsigned char)(w >> 8), qrs, off + 16, 0, 0);
+                if (r16 == b) mine = sb;
+              }
+              __builtin_amdgcn_raw_buffer_store_b8((unsigned char)mine, srs,
+                                                   ls + uint32_t(i * 16 + r) * srow, 0, 0);
+            }
+        } else if (g.h_saved) {
           const __amdgpu_buffer_rsrc_t hrs = make_rsrc(
               g.h_saved + row0 * g.Hp + n0, clamp_bytes(int64_t(rows_valid) * g.Hp * 2));
           const uint32_t hrow = lane_rows * g.Hp * 2;
@@ -1045,7 +1085,7 @@ __global__ __launch_bounds__(256) void gemm_fp32_swiglu_kernel(
 // ------------------------------------------------------------------ host
 // Compute units of the current device, cached per device. Host threads may call
 // concurrently: every store of an entry writes the same value.
-static int device_cus() {
+int device_cus() {
   constexpr int kMaxDevices = 64;
   static std::atomic<int> cache[kMaxDevices];
   int dev = 0;
@@ -1109,10 +1149,11 @@ static bool split_tails(const moonep_shape& s, int ncols, int cus) {
   return full_tiles(s, ncols) >= 4 * int64_t(cus);
 }
 
-template <int OP, bool SWIGLU, typename C, bool STREAM_OUT = false, bool HALFN = false>
+template <int OP, bool SWIGLU, typename C, bool STREAM_OUT = false, bool HALFN = false,
+          bool CKPT = false>
 static void launch_cfg(const GemmArgs& g, int cus, hipStream_t strm) {
   gemm_bf16_kernel<OP, C::BM, C::BN, C::WAVES_M, C::WAVES_N, SWIGLU, STREAM_OUT, C::STAGES,
-                   HALFN><<<cus, C::WAVES_M * C::WAVES_N * 64, 0, strm>>>(g);
+                   HALFN, CKPT><<<cus, C::WAVES_M * C::WAVES_N * 64, 0, strm>>>(g);
 }
 
 // The full-tile list (on the small-tile kernel for a small call), then (FWD and DGRAD,
@@ -1122,7 +1163,7 @@ static void launch_cfg(const GemmArgs& g, int cus, hipStream_t strm) {
 template <int OP, bool SWIGLU>
 constexpr bool kHalfnOp = OP == MOONEP_FWD && !SWIGLU;
 
-template <int OP, bool SWIGLU = false, bool STREAM_OUT = false>
+template <int OP, bool SWIGLU = false, bool STREAM_OUT = false, bool CKPT = false>
 static void launch_bf16(GemmArgs g, const TileEntry* tails, const int32_t* ntails,
                         bool tails_apart, bool small, int ncols, int cus, hipStream_t strm) {
   if constexpr (OP != MOONEP_WGRAD && !SWIGLU) {
@@ -1135,12 +1176,12 @@ static void launch_bf16(GemmArgs g, const TileEntry* tails, const int32_t* ntail
   if (kHalfnOp<OP, SWIGLU> && last > 0 && last <= TileCfg::BN / 2)
     launch_cfg<OP, SWIGLU, TileCfg, STREAM_OUT, kHalfnOp<OP, SWIGLU>>(g, cus, strm);
   else
-    launch_cfg<OP, SWIGLU, TileCfg, STREAM_OUT>(g, cus, strm);
+    launch_cfg<OP, SWIGLU, TileCfg, STREAM_OUT, false, CKPT>(g, cus, strm);
   if (OP != MOONEP_WGRAD && tails_apart) {
     g.tiles = tails;
     g.ntiles = ntails;
     if (g.qcnt) g.qcnt += kQueueWords;
-    launch_cfg<OP, SWIGLU, TailCfg, STREAM_OUT>(g, cus, strm);
+    launch_cfg<OP, SWIGLU, TailCfg, STREAM_OUT, false, CKPT>(g, cus, strm);
   }
 }
 
@@ -1207,7 +1248,8 @@ static int gemm_launch(const moonep_shape& s, int32_t op, const void* a, const v
 
   if (bf16) {
     GemmArgs g{static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(b), c, grad_home,
-               reduce_buf, w.tiles, w.ntiles, s.H, s.Hp, s.E, nullptr, nullptr, w.qcnt};
+               reduce_buf, w.tiles, w.ntiles, s.H, s.Hp, s.E, nullptr, nullptr, w.qcnt,
+               nullptr, nullptr};
     if (op == MOONEP_FWD)
       launch_bf16<MOONEP_FWD>(g, w.tails, w.ntails, tails_apart, small, ncols, cus, strm);
     else if (op == MOONEP_DGRAD && s.Hp <= kStreamOutMaxK)
@@ -1235,6 +1277,18 @@ static GemmLists ws_lists(void* ws, const WsLayout& w) {
                    ws_ptr<int32_t>(ws, w.flags) + kFlagTileCount,
                    ws_ptr<int32_t>(ws, w.flags) + kFlagTileCountTail, w.max_tiles, w.max_tail,
                    ws_ptr<int32_t>(ws, w.flags) + kFlagQueue};
+}
+
+int launch_tile_list(const moonep_shape& s, const int32_t* cu_seqlens, int bm, void* ws,
+                     hipStream_t strm, const TileEntry** tiles, const int32_t** ntiles) {
+  const WsLayout l = ws_layout(s);
+  const GemmLists w = ws_lists(ws, l);
+  gemm_tiles_kernel<<<1, 1024, 0, strm>>>(cu_seqlens, s.R, s.E, s.B, s.S * s.K, bm, 0, false,
+                                          w.tiles, w.ntiles, int(w.max_tiles), w.tails, w.ntails,
+                                          int(w.max_tail), w.qcnt, 0);
+  *tiles = w.tiles;
+  *ntiles = w.ntiles;
+  return launch_status();
 }
 
 // ------------------------------------------------------------------ no-alloc scratch
@@ -1311,19 +1365,26 @@ extern "C" int moonep_grouped_gemm_noalloc(const moonep_shape* shape, int32_t op
                      as_stream(stream));
 }
 
-extern "C" int moonep_grouped_gemm_swiglu(const moonep_shape* shape, const void* xp,
-                                          const void* w1_all, const int32_t* cu_seqlens, void* act,
-                                          void* h_saved, void* ws, size_t ws_bytes, void* stream) {
+namespace moonep {
+
+// The gate/up GEMM with its SwiGLU epilogue; the pre-activation is saved in dtype
+// (h_saved), as a checkpoint (q and scales, checkpoint = true), or not at all.
+static int gemm_swiglu(const moonep_shape* shape, const void* xp, const void* w1_all,
+                       const int32_t* cu_seqlens, void* act, void* h_saved, bool checkpoint,
+                       uint8_t* q, uint8_t* scales, void* ws, size_t ws_bytes, void* stream) {
   int st = validate(shape);
   if (st) return st;
   const moonep_shape& s = *shape;
-  if (s.H % 64 || s.Hp % kSwigluBlock) return MOONEP_EINVAL;
+  if (checkpoint && s.mode != MOONEP_TRAIN) return MOONEP_EMODE;
+  if (s.H % 64 || s.Hp % (checkpoint ? 64 : kSwigluBlock)) return MOONEP_EINVAL;
+  if (checkpoint && s.dtype != MOONEP_BF16) return MOONEP_EINVAL;
   if (!aligned16(cu_seqlens) || !aligned16(ws)) return MOONEP_EINVAL;
   const WsLayout w = ws_layout(s);
   if (ws_bytes < w.total) return MOONEP_EWORKSPACE;
   if (s.S == 0) return MOONEP_OK;
   if (!aligned16(xp) || !aligned16(w1_all) || !aligned16(act)) return MOONEP_EINVAL;
   if (h_saved && !aligned16(h_saved)) return MOONEP_EINVAL;
+  if (checkpoint && (!aligned16(q) || !aligned16(scales))) return MOONEP_EINVAL;
   hipStream_t strm = as_stream(stream);
   TileEntry* tiles = ws_ptr<TileEntry>(ws, w.tiles);
   TileEntry* tails = ws_ptr<TileEntry>(ws, w.tiles_tail);
@@ -1342,12 +1403,34 @@ extern "C" int moonep_grouped_gemm_swiglu(const moonep_shape* shape, const void*
   if (bf16) {
     GemmArgs g{static_cast<const uint16_t*>(xp), static_cast<const uint16_t*>(w1_all), nullptr,
                nullptr, nullptr, tiles, ntiles, s.H, 2 * s.Hp, s.E,
-               static_cast<uint16_t*>(act), static_cast<uint16_t*>(h_saved), qcnt};
-    launch_bf16<MOONEP_FWD, true>(g, tails, ntails, tails_apart, false, 2 * s.Hp, cus, strm);
+               static_cast<uint16_t*>(act), static_cast<uint16_t*>(h_saved), qcnt, q, scales};
+    if (checkpoint)
+      launch_bf16<MOONEP_FWD, true, false, true>(g, tails, ntails, tails_apart, false, 2 * s.Hp,
+                                                 cus, strm);
+    else
+      launch_bf16<MOONEP_FWD, true>(g, tails, ntails, tails_apart, false, 2 * s.Hp, cus, strm);
   } else {
     gemm_fp32_swiglu_kernel<<<dim3(64, 256), 256, 0, strm>>>(
         static_cast<const float*>(xp), static_cast<const float*>(w1_all),
         static_cast<float*>(act), static_cast<float*>(h_saved), tiles, ntiles, s.H, s.Hp);
   }
   return launch_status();
+}
+
+}  // namespace moonep
+
+extern "C" int moonep_grouped_gemm_swiglu(const moonep_shape* shape, const void* xp,
+                                          const void* w1_all, const int32_t* cu_seqlens, void* act,
+                                          void* h_saved, void* ws, size_t ws_bytes, void* stream) {
+  return gemm_swiglu(shape, xp, w1_all, cu_seqlens, act, h_saved, false, nullptr, nullptr, ws,
+                     ws_bytes, stream);
+}
+
+extern "C" int moonep_grouped_gemm_swiglu_checkpoint(const moonep_shape* shape, const void* xp,
+                                                     const void* w1_all,
+                                                     const int32_t* cu_seqlens, void* act,
+                                                     uint8_t* q, uint8_t* scales, void* ws,
+                                                     size_t ws_bytes, void* stream) {
+  return gemm_swiglu(shape, xp, w1_all, cu_seqlens, act, nullptr, true, q, scales, ws, ws_bytes,
+                     stream);
 }

@@ -1,6 +1,6 @@
 // HBM-bound data movement of the balanced MoE layer on gfx950: fused permute
-// (dispatch), fused unpermute (combine), prefetch of replica weights and the
-// fold of replica gradients (reduce_grad). All moves are 16-byte vectors with
+// (dispatch), fused unpermute (combine), the gates' gradient, prefetch of replica
+// weights and the fold of replica gradients (reduce_grad). All moves are 16-byte vectors with
 // consecutive lanes on consecutive addresses of a row; per-token slot indices
 // and gates are uniform across a workgroup, staged once in LDS.
 //
@@ -141,6 +141,63 @@ __global__ __launch_bounds__(kMoveThreads) void combine_kernel(
       }
     }
     __syncthreads();
+  }
+}
+
+// Gates' gradient: one workgroup per token; each thread multiplies its columns of dy with
+// kGateK expert output rows at a time and the workgroup sums them in a fixed order
+// (columns of a thread ascending, lanes by butterfly, wavefronts ascending).
+constexpr int kGateK = 8;
+template <bool BF16>
+__global__ __launch_bounds__(kMoveThreads) void gate_grad_kernel(
+    const v4f_t* __restrict__ src, int nvec, int N, int K, const int32_t* __restrict__ slot_map,
+    const void* __restrict__ dy, float* __restrict__ dgates, int64_t nsrc) {
+  constexpr int kWaves = kMoveThreads / 64;
+  __shared__ float s_part[kWaves][kGateK];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int64_t g = blockIdx.x; g < N; g += gridDim.x) {
+    for (int k0 = 0; k0 < K; k0 += kGateK) {
+      int64_t at[kGateK];
+      float acc[kGateK];
+#pragma unroll
+      for (int k = 0; k < kGateK; ++k) {
+        const int d = k0 + k < K ? slot_map[g * K + k0 + k] : -1;
+        at[k] = (d >= 0 && d < nsrc) ? int64_t(d) * nvec : -1;
+        acc[k] = 0.f;
+      }
+      for (int v = threadIdx.x; v < nvec; v += kMoveThreads) {
+        v4f_t d;
+        if (BF16) {
+          const uint2 u = static_cast<const uint2*>(dy)[g * nvec + v];
+          d = v4f_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                    __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
+        } else {
+          d = static_cast<const v4f_t*>(dy)[g * nvec + v];
+        }
+        v4f_t x[kGateK];
+#pragma unroll
+        for (int k = 0; k < kGateK; ++k)
+          x[k] = at[k] >= 0 ? __builtin_nontemporal_load(src + at[k] + v) : v4f_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kGateK; ++k)
+          if (at[k] >= 0)
+            acc[k] = fmaf(x[k].w, d.w, fmaf(x[k].z, d.z, fmaf(x[k].y, d.y, fmaf(x[k].x, d.x, acc[k]))));
+      }
+#pragma unroll
+      for (int k = 0; k < kGateK; ++k) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) acc[k] += __shfl_xor(acc[k], o, 64);
+        if (lane == 0) s_part[w][k] = acc[k];
+      }
+      __syncthreads();
+      if (threadIdx.x < kGateK && k0 + threadIdx.x < K) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) t += s_part[i][threadIdx.x];
+        dgates[g * K + k0 + threadIdx.x] = t;
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -290,6 +347,31 @@ extern "C" int moonep_combine(const moonep_shape* shape, int32_t width, const fl
     if (two) launch_combine<false, 2>(grid, strm, sv, nvec, N, s.K, slot_map, nullptr, dv, nsrc);
     else launch_combine<false, 1>(grid, strm, sv, nvec, N, s.K, slot_map, nullptr, dv, nsrc);
   }
+  return launch_status();
+}
+
+extern "C" int moonep_gate_grad(const moonep_shape* shape, int32_t width, const float* src,
+                                const int32_t* slot_map, const void* dy, float* dgates,
+                                void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (s.mode != MOONEP_TRAIN) return MOONEP_EMODE;
+  if (width != s.H && width != s.Hp) return MOONEP_EINVAL;
+  const int N = s.R * s.S;
+  if (N == 0) return MOONEP_OK;
+  if (!aligned16(src) || !aligned16(slot_map) || !aligned16(dy) || !aligned16(dgates))
+    return MOONEP_EINVAL;
+  const int nvec = width / 4;
+  const int grid = grid_for(N, 1 << 20);
+  const v4f_t* sv = reinterpret_cast<const v4f_t*>(src);
+  const int64_t nsrc = int64_t(N) * s.K;
+  if (s.dtype == MOONEP_BF16)
+    gate_grad_kernel<true><<<grid, kMoveThreads, 0, as_stream(stream)>>>(sv, nvec, N, s.K, slot_map,
+                                                                         dy, dgates, nsrc);
+  else
+    gate_grad_kernel<false><<<grid, kMoveThreads, 0, as_stream(stream)>>>(sv, nvec, N, s.K, slot_map,
+                                                                          dy, dgates, nsrc);
   return launch_status();
 }
 

@@ -9,6 +9,17 @@ Forward  : plan -> prefetch(W1, W2) -> dispatch(x) -> gate/up GEMM with SwiGLU
            -> down GEMM -> combine(z, gates)
 Backward : dispatch(dy, gates) -> dgrad(W2) -> wgrad(W2) -> SwiGLU backward
            -> dgrad(W1) -> wgrad(W1) -> combine(dxp, no gates) -> reduce_grad(W1, W2)
+           gate_grad(dy) -> dgates, the router's upstream gradient
+
+With checkpoint=True the forward keeps x and the gate/up pre-activation in 8 bits
+(xq, xs; hq, hscales) instead of xp, act and hs, and the backward is
+  dispatch(dy, no gates) -> dgrad(W2) -> SwiGLU backward from the checkpoint (act
+  and dh times the gates, and dgates) -> wgrad(W2) -> dgrad(W1) -> permute of x
+  from its checkpoint -> wgrad(W1) -> combine -> reduce_grad.
+The slot buffers then hold nothing between the two passes, so the layers of a
+model can share one set of them (scratch=another layer of the same shape): what
+each keeps per slot falls from 2H + 6H' bytes (bfloat16 xp, act, hs) to 2.0625 H'
+bytes, plus 1.03 H bytes per token.
 
 Shapes passed to the library (H' = cfg.Hp, the intermediate size):
   ffn  (H, H')    SwiGLU calls        up  (H, 2H')   everything on W1, x, dX
@@ -27,6 +38,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from .checkpoint import buffers as checkpoint_buffers
 
 
 def _shape(cfg, H, Hp):
@@ -37,10 +49,16 @@ def _shape(cfg, H, Hp):
 
 class MoEFFN:
     def __init__(self, cfg, device="cuda", backward: bool = False, w1_all=None, w2_all=None,
-                 fused: bool = True):
+                 fused: bool = True, checkpoint: bool = False, scratch: "MoEFFN | None" = None):
         c = cfg
+        if checkpoint and not backward:
+            raise ValueError("checkpoint: needs backward=True")
+        if scratch is not None and not (checkpoint and scratch.checkpoint):
+            raise ValueError("scratch: only layers with checkpoints can share slot buffers")
         self.cfg = c
-        self.fused = fused
+        self.checkpoint = checkpoint
+        # the float32 gate/up GEMM has no checkpointing epilogue
+        self.fused = fused = fused and not (checkpoint and c.dtype == "fp32")
         self.shape = _shape(c, c.H, c.Hp)
         self.up = _shape(c, c.H, 2 * c.Hp)
         self.down = _shape(c, c.Hp, c.H)
@@ -66,18 +84,31 @@ class MoEFFN:
         W = c.E + c.R * c.B
         self.w1_all = w1_all if w1_all is not None else torch.empty((W, c.H, 2 * c.Hp), **dtd)
         self.w2_all = w2_all if w2_all is not None else torch.empty((W, c.Hp, c.H), **dtd)
-        self.xp = torch.empty((rows, c.H), **dtd)
-        self.act = torch.empty((rows, c.Hp), **dtd)
-        self.h = None if fused else torch.empty((rows, 2 * c.Hp), **f32)
-        self.hs = torch.empty((rows, 2 * c.Hp), **dtd) if backward else None
-        self.z = torch.empty((rows, c.H), **f32)
+        if scratch is None:
+            self.xp = torch.empty((rows, c.H), **dtd)
+            self.act = torch.empty((rows, c.Hp), **dtd)
+            self.h = None if fused else torch.empty((rows, 2 * c.Hp), **f32)
+            self.z = torch.empty((rows, c.H), **f32)
+        else:
+            mine = (c.R, c.S, c.K, c.H, c.Hp, c.dtype, fused, self.device.type)
+            o = scratch.cfg
+            if mine != (o.R, o.S, o.K, o.H, o.Hp, o.dtype, scratch.fused, scratch.device.type):
+                raise ValueError("scratch: a layer of another shape")
+            for name in ("xp", "act", "h", "z", "dyp", "da", "dh", "dxp"):
+                setattr(self, name, getattr(scratch, name))
+        self.hs = torch.empty((rows, 2 * c.Hp), **dtd) if backward and not checkpoint else None
         self.y = torch.empty((max(N, 1), c.H), **f32)
+        if checkpoint:
+            self.xq, self.xs = checkpoint_buffers(N, c.H, self.device)
+            self.hq, self.hscales = checkpoint_buffers(rows, 2 * c.Hp, self.device)
         if backward:
-            self.dyp = torch.empty((rows, c.H), **dtd)
-            self.da = torch.empty((rows, c.Hp), **f32)
-            self.dh = torch.empty((rows, 2 * c.Hp), **dtd)
-            self.dxp = torch.empty((rows, c.H), **f32)
+            if scratch is None:
+                self.dyp = torch.empty((rows, c.H), **dtd)
+                self.da = torch.empty((rows, c.Hp), **f32)
+                self.dh = torch.empty((rows, 2 * c.Hp), **dtd)
+                self.dxp = torch.empty((rows, c.H), **f32)
             self.dx = torch.empty((max(N, 1), c.H), **f32)
+            self.dgates = torch.empty((max(N, 1), c.K), **f32)
             B = max(c.B, 1)
             self.grad1 = torch.zeros((c.E, c.H, 2 * c.Hp), **f32)
             self.red1 = torch.zeros((c.R, B, c.H, 2 * c.Hp), **f32)
@@ -96,14 +127,26 @@ class MoEFFN:
     def dispatch(self, x, stream=None):
         L.moonep_dispatch(self.up, self.cfg.H, x, self.slot_map, None, self.xp, stream)
 
+    def save_input(self, x, stream=None):
+        """x in 8 bits, for the backward pass (checkpoint=True)."""
+        L.moonep_checkpoint_quantize(self.up, self.cfg.H, x, self.xq, self.xs, stream)
+
     def gate_up(self, stream=None):
-        if self.fused:
+        if self.fused and self.checkpoint:
+            L.moonep_grouped_gemm_swiglu_checkpoint(self.shape, self.xp, self.w1_all,
+                                                    self.cu_seqlens, self.act, self.hq,
+                                                    self.hscales, self.ws, stream)
+        elif self.fused:
             L.moonep_grouped_gemm_swiglu(self.shape, self.xp, self.w1_all, self.cu_seqlens,
                                          self.act, self.hs, self.ws, stream)
         else:
             L.moonep_grouped_gemm(self.up, L.FWD, self.xp, self.w1_all, self.cu_seqlens, self.h,
                                   None, None, self.ws, stream)
-            L.moonep_swiglu(self.shape, self.h, self.act, self.hs, stream)
+            if self.checkpoint:
+                L.moonep_swiglu_checkpoint(self.shape, self.h, self.act, self.hq, self.hscales,
+                                           stream)
+            else:
+                L.moonep_swiglu(self.shape, self.h, self.act, self.hs, stream)
 
     def down_proj(self, stream=None):
         L.moonep_grouped_gemm(self.down, L.FWD, self.act, self.w2_all, self.cu_seqlens, self.z,
@@ -116,14 +159,40 @@ class MoEFFN:
         self.plan(topk_idx, stream)
         self.prefetch(stream)
         self.dispatch(x, stream)
+        if self.checkpoint:
+            self.save_input(x, stream)
         self.gate_up(stream)
         self.down_proj(stream)
         self.combine(gates, stream)
         return self.y
 
     # ---- backward
+    def gate_grad(self, dy, stream=None):
+        """Gradient of the gates [N,K]. With checkpoints, the one that the last backward
+        formed (the expert outputs are not kept); else from the forward's outputs and dy."""
+        if not self.checkpoint:
+            L.moonep_gate_grad(self.up, self.cfg.H, self.z, self.slot_map, dy, self.dgates, stream)
+        return self.dgates
+
+    def _backward_checkpoint(self, dy, gates, stream):
+        c = self.cfg
+        L.moonep_dispatch(self.up, c.H, dy, self.slot_map, None, self.dyp, stream)
+        L.moonep_grouped_gemm(self.down, L.DGRAD, self.dyp, self.w2_all, self.cu_seqlens, self.da,
+                              None, None, self.ws, stream)
+        L.moonep_swiglu_backward_checkpoint(self.shape, self.hq, self.hscales, self.da,
+                                            self.src_index, gates, self.act, self.dh, self.dgates,
+                                            stream)
+        L.moonep_grouped_gemm(self.down, L.WGRAD, self.act, self.dyp, self.cu_seqlens, None,
+                              self.grad2, self.red2, self.ws, stream)
+        L.moonep_grouped_gemm(self.up, L.DGRAD, self.dh, self.w1_all, self.cu_seqlens, self.dxp,
+                              None, None, self.ws, stream)
+        L.moonep_checkpoint_dispatch(self.up, c.H, self.xq, self.xs, self.slot_map, self.xp, stream)
+
     def backward(self, dy, gates, stream=None):
         c = self.cfg
+        if self.checkpoint:
+            self._backward_checkpoint(dy, gates, stream)
+            return self._backward_tail(stream)
         L.moonep_dispatch(self.up, c.H, dy, self.slot_map, gates, self.dyp, stream)
         L.moonep_grouped_gemm(self.down, L.DGRAD, self.dyp, self.w2_all, self.cu_seqlens, self.da,
                               None, None, self.ws, stream)
@@ -132,6 +201,10 @@ class MoEFFN:
         L.moonep_swiglu_backward(self.shape, self.hs, self.da, self.dh, stream)
         L.moonep_grouped_gemm(self.up, L.DGRAD, self.dh, self.w1_all, self.cu_seqlens, self.dxp,
                               None, None, self.ws, stream)
+        return self._backward_tail(stream)
+
+    def _backward_tail(self, stream):
+        c = self.cfg
         L.moonep_grouped_gemm(self.up, L.WGRAD, self.xp, self.dh, self.cu_seqlens, None,
                               self.grad1, self.red1, self.ws, stream)
         L.moonep_combine(self.up, c.H, self.dxp, self.slot_map, None, self.dx, stream)

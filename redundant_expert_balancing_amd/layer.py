@@ -4,6 +4,7 @@ and the hot path as a sequence of library calls (no computation here).
 Forward  : plan -> prefetch_weight -> dispatch(x) -> grouped_gemm(FWD) -> combine(out, gates)
 Backward : dispatch(dy, gates) -> grouped_gemm(DGRAD) -> grouped_gemm(WGRAD)
            -> combine(dxp, no gates) -> reduce_grad
+           gate_grad(dy) -> dgates fp32 [N,K], the router's upstream gradient
 Buffer layout (row-major, one allocation per array):
   topk_idx int32 [N,K]; gates fp32 [N,K]; cu_seqlens int32 [R,E+B+1];
   replica_expert int32 [R,B]; slot_map, src_index int32 [N*K];
@@ -51,6 +52,7 @@ class MoEProjection:
             self.grad_home = torch.zeros((c.E, c.H, c.Hp), dtype=torch.float32, device=self.device)
             self.reduce_buf = torch.zeros((c.R, max(c.B, 1), c.H, c.Hp), dtype=torch.float32,
                                           device=self.device)
+            self.dgates = torch.empty((max(N, 1), c.K), dtype=torch.float32, device=self.device)
 
     # ---- stages
     def plan(self, topk_idx, stream=None):
@@ -89,6 +91,12 @@ class MoEProjection:
         L.moonep_reduce_grad(self.shape, self.replica_expert, self.reduce_buf, self.grad_home,
                              stream)
         return self.dx
+
+    def gate_grad(self, dy, stream=None):
+        """Gradient of the gates [N,K], from the forward's expert outputs and dy."""
+        c = self.cfg
+        L.moonep_gate_grad(self.shape, c.Hp, self.out, self.slot_map, dy, self.dgates, stream)
+        return self.dgates
 
     def error_flags(self, clear=False) -> int:
         return L.moonep_get_error(self.shape, self.ws, clear)

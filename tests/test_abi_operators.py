@@ -1,0 +1,143 @@
+"""Argument checks of the router, the gates' gradient, the 8-bit checkpoints and the 4-bit
+experts: every refusal comes back before a launch (no GPU call is made here)."""
+import ctypes
+
+import pytest
+import torch
+
+from redundant_expert_balancing_amd import _lib as L
+
+P = ctypes.c_void_p(0x1000)       # aligned, never dereferenced
+BAD = ctypes.c_void_p(0x1008)
+BIG = 1 << 30
+
+
+def S(**kw):
+    base = dict(R=4, S=64, E=16, K=2, B=4, H=128, Hp=64, mode=L.TRAIN, dtype=L.BF16)
+    base.update(kw)
+    return L.Shape(*[base[k] for k in ("R", "S", "E", "K", "B", "H", "Hp", "mode", "dtype")])
+
+
+def RT(**kw):
+    base = dict(score=L.SOFTMAX, dtype=L.FP32, groups=1, top_groups=1, group_top=1, renorm=1,
+                scale=1.0)
+    base.update(kw)
+    return L.Router(*[base[k] for k in ("score", "dtype", "groups", "top_groups", "group_top",
+                                        "renorm", "scale")])
+
+
+def route(sh, r, *p):
+    p = p or (P, None, P, P)
+    return L.lib().moonep_route(ctypes.byref(sh), ctypes.byref(r), *p, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(score=2), dict(dtype=2), dict(groups=0), dict(groups=3), dict(top_groups=0),
+    dict(top_groups=2), dict(group_top=0), dict(group_top=3), dict(renorm=2), dict(scale=0.0),
+    dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")),
+    dict(groups=16, top_groups=16, group_top=2),      # one expert per group
+    dict(groups=16, top_groups=1),                    # K = 2 > the one expert that stays
+])
+def test_router_rules(kw):
+    assert route(S(), RT(**kw)) == L.EINVAL
+    sh, r = S(), RT(**kw)
+    assert L.lib().moonep_route_backward(ctypes.byref(sh), ctypes.byref(r), P, None, P, P, P, P,
+                                         None) == L.EINVAL
+
+
+def test_router_limits_modes_and_pointers():
+    assert route(S(R=1, E=128, B=128), RT(groups=128, top_groups=128)) == L.ELIMIT
+    assert route(S(E=18), RT()) == L.EINVAL
+    assert L.lib().moonep_route(ctypes.byref(S()), None, P, None, P, P, None) == L.EINVAL
+    for p in ((BAD, None, P, P), (P, BAD, P, P), (P, None, None, P), (P, None, P, BAD)):
+        assert route(S(), RT(), *p) == L.EINVAL
+    assert route(S(S=0), RT(), None, None, None, None) == L.OK
+    inf = S(mode=L.INFER, B=2)
+    assert L.lib().moonep_route_backward(ctypes.byref(inf), ctypes.byref(RT()), P, None, P, P, P, P,
+                                         None) == L.EMODE
+    assert L.lib().moonep_route_backward(ctypes.byref(S()), ctypes.byref(RT()), P, None, P, P, None,
+                                         P, None) == L.EINVAL
+
+
+def test_gate_grad_and_checkpoint_rules():
+    lib = L.lib()
+    sh, inf, empty = S(), S(mode=L.INFER, B=2), S(S=0)
+    assert lib.moonep_gate_grad(ctypes.byref(sh), 100, P, P, P, P, None) == L.EINVAL
+    assert lib.moonep_gate_grad(ctypes.byref(sh), 64, P, P, BAD, P, None) == L.EINVAL
+    assert lib.moonep_gate_grad(ctypes.byref(inf), 64, P, P, P, P, None) == L.EMODE
+    assert lib.moonep_gate_grad(ctypes.byref(empty), 64, None, None, None, None, None) == L.OK
+    assert lib.moonep_checkpoint_quantize(ctypes.byref(sh), 100, P, P, P, None) == L.EINVAL
+    assert lib.moonep_checkpoint_quantize(ctypes.byref(sh), 128, P, BAD, P, None) == L.EINVAL
+    assert lib.moonep_checkpoint_quantize(ctypes.byref(inf), 128, P, P, P, None) == L.EMODE
+    assert lib.moonep_checkpoint_dispatch(ctypes.byref(sh), 96, P, P, P, P, None) == L.EINVAL
+    assert lib.moonep_checkpoint_dispatch(ctypes.byref(sh), 128, P, P, None, P, None) == L.EINVAL
+    assert lib.moonep_checkpoint_dispatch(ctypes.byref(empty), 128, None, None, None, None, None) == L.OK
+    assert lib.moonep_swiglu_checkpoint(ctypes.byref(S(Hp=48)), P, P, P, P, None) == L.EINVAL
+    assert lib.moonep_swiglu_checkpoint(ctypes.byref(sh), P, P, P, BAD, None) == L.EINVAL
+    assert lib.moonep_swiglu_checkpoint(ctypes.byref(inf), P, P, P, P, None) == L.EMODE
+    back = lib.moonep_swiglu_backward_checkpoint
+    assert back(ctypes.byref(sh), P, P, P, None, P, P, P, P, None) == L.EINVAL   # gates, no src_index
+    assert back(ctypes.byref(sh), P, P, P, P, P, P, P, None, None) == L.EINVAL   # gates, no dgates
+    assert back(ctypes.byref(sh), P, P, P, P, None, P, P, None, None) == L.EINVAL  # src_index alone
+    assert back(ctypes.byref(sh), P, P, P, None, None, P, P, P, None) == L.EINVAL  # dgates alone
+    assert back(ctypes.byref(inf), P, P, P, P, P, P, P, P, None) == L.EMODE
+    assert back(ctypes.byref(empty), *[None] * 9) == L.OK
+    fused = lib.moonep_grouped_gemm_swiglu_checkpoint
+    assert fused(ctypes.byref(S(dtype=L.FP32)), P, P, P, P, P, P, P, BIG, None) == L.EINVAL
+    assert fused(ctypes.byref(S(Hp=32)), P, P, P, P, P, P, P, BIG, None) == L.EINVAL
+    assert fused(ctypes.byref(sh), P, P, P, P, None, P, P, BIG, None) == L.EINVAL
+    assert fused(ctypes.byref(sh), P, P, P, P, P, P, P, 16, None) == L.EWORKSPACE
+    assert fused(ctypes.byref(inf), P, P, P, P, P, P, P, BIG, None) == L.EMODE
+
+
+def test_mx_rules():
+    lib = L.lib()
+    sh, empty = S(), S(S=0)
+    q = lib.moonep_mx_quantize
+    assert q(ctypes.byref(sh), -1, 128, P, P, P, None) == L.EINVAL
+    assert q(ctypes.byref(sh), 1 << 31, 128, P, P, P, None) == L.EINVAL
+    assert q(ctypes.byref(sh), 4, 48, P, P, P, None) == L.EINVAL
+    assert q(ctypes.byref(sh), 4, 0, P, P, P, None) == L.EINVAL
+    assert q(ctypes.byref(sh), 4, 128, BAD, P, P, None) == L.EINVAL
+    assert q(ctypes.byref(sh), 0, 128, None, None, None, None) == L.OK
+    assert lib.moonep_mx_quantize_weight(ctypes.byref(S(H=72)), P, P, P, None) == L.EINVAL
+    assert lib.moonep_mx_quantize_weight(ctypes.byref(S(Hp=72)), P, P, P, None) == L.EINVAL
+    assert lib.moonep_mx_quantize_weight(ctypes.byref(sh), P, P, None, None) == L.EINVAL
+    assert lib.moonep_mx_prefetch_weight(ctypes.byref(sh), P, BAD, P, None) == L.EINVAL
+    none = S(mode=L.INFER, B=0)
+    assert lib.moonep_mx_prefetch_weight(ctypes.byref(none), None, None, None, None) == L.OK
+    g = lib.moonep_mx_grouped_gemm
+    assert g(ctypes.byref(S(H=96)), P, P, P, P, P, P, P, P, BIG, None) == L.EINVAL
+    assert g(ctypes.byref(S(Hp=96)), P, P, P, P, P, P, P, P, BIG, None) == L.EINVAL
+    assert g(ctypes.byref(sh), P, P, BAD, P, P, P, P, P, BIG, None) == L.EINVAL
+    assert g(ctypes.byref(sh), P, P, None, P, P, P, None, P, BIG, None) == L.EINVAL
+    assert g(ctypes.byref(sh), P, P, None, P, P, P, P, P, 16, None) == L.EWORKSPACE
+    assert g(ctypes.byref(empty), None, None, None, None, None, P, None, P, BIG, None) == L.OK
+
+
+def test_binding_refuses_host_and_missing_tensors():
+    sh, r = S(), RT()
+    f = torch.zeros((256, 16))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        L.moonep_route(sh, r, f, None, f, f)
+    with pytest.raises(ValueError, match="required"):
+        L.moonep_route(sh, r, None, None, f, f)
+    with pytest.raises(ValueError, match="required"):
+        L.moonep_mx_grouped_gemm(sh, None, f, None, f, f, f, f, f)
+
+
+def test_layer_arguments():
+    from redundant_expert_balancing_amd.ffn import MoEFFN
+    from redundant_expert_balancing_amd.mx import MXProjection
+    from redundant_expert_balancing_amd.router import MoERouter
+    from redundant_expert_balancing_amd.synth import CONFIGS
+    cfg = CONFIGS["tiny_fp32_train"]
+    with pytest.raises(ValueError, match="score"):
+        MoERouter(cfg, score="tanh", device="cpu")
+    with pytest.raises(ValueError, match="dtype"):
+        MoERouter(cfg, dtype="fp16", device="cpu")
+    with pytest.raises(ValueError, match="checkpoint"):
+        MoEFFN(cfg, device="cpu", checkpoint=True)
+    import dataclasses
+    with pytest.raises(L.MoonepError):
+        MXProjection(dataclasses.replace(cfg, H=96), device="cpu")

@@ -1,0 +1,318 @@
+"""8-bit activation checkpoints on the GPU: stored bytes equal the oracle's, everything
+computed from them within its rounding of the float64 value, and the FFN that runs on them."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ffn as FF
+from oracle import formats as F
+from redundant_expert_balancing_amd import _lib as L
+from redundant_expert_balancing_amd import checkpoint as C
+from redundant_expert_balancing_amd.ffn import MoEFFN
+from redundant_expert_balancing_amd.synth import make_dense, make_routing
+
+from gpu_helpers import say, small_cfg
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def _dt(dtype):
+    return torch.bfloat16 if dtype == "bf16" else torch.float32
+
+
+def _shape(N, K, H, Hp, dtype, R=1, E=8):
+    return L.Shape(R, N // R, E, K, E // R, H, Hp, L.TRAIN, L.BF16 if dtype == "bf16" else L.FP32)
+
+
+def _wide(rng, shape):
+    """Values over many magnitudes, zeros, whole zero blocks and exact borders among them."""
+    x = rng.standard_normal(shape) * 2.0 ** rng.integers(-6, 7, shape)
+    x *= 2.0 ** rng.integers(-30, 30, (shape[0], 1))
+    x[rng.random(shape) < 0.05] = 0.0
+    x[0] = 0.0
+    if shape[0] > 3:
+        x[1] = 2.0 ** -140                  # float32 subnormals: below every scale
+        x[2, ::2] = 448.0
+        x[3, ::3] = -448.0 * (1 + 2.0 ** -7)
+    return x.astype(np.float32)
+
+
+def _assert_bytes(q, s, x, width):
+    want_q, want_s = F.checkpoint(x)
+    nb = want_s.shape[1]
+    s = s.cpu().numpy()
+    assert np.array_equal(s[:, :nb], want_s)
+    assert (s[:, nb:] == 0).all()
+    assert np.array_equal(q.cpu().numpy(), want_q)
+
+
+@pytest.mark.parametrize("dtype,width,N,K", [("bf16", 8, 1, 1), ("bf16", 64, 5, 2), ("bf16", 200, 67, 3),
+                                             ("fp32", 4, 3, 1), ("fp32", 76, 33, 8), ("fp32", 512, 9, 2),
+                                             ("bf16", 1408, 21, 8), ("fp32", 132, 40, 32)])
+def test_rows_and_dispatch(dtype, width, N, K):
+    say("checkpoint rows", dtype, width, N, K)
+    sh = _shape(N, K, width, 64, dtype, E=64)
+    rng = np.random.default_rng(width)
+    x = torch.from_numpy(_wide(rng, (N, width))).cuda().to(_dt(dtype))
+    q, s = C.buffers(N, width)
+    q.fill_(0xAA), s.fill_(0xAA)
+    L.moonep_checkpoint_quantize(sh, width, x, q, s)
+    torch.cuda.synchronize()
+    _assert_bytes(q, s, x.double().cpu().numpy(), width)
+    sm = rng.permutation(N * K).astype(np.int32)
+    skip = sm.copy()
+    if N * K > 2:
+        skip[1], skip[2] = -1, N * K
+    dst = torch.full((N * K, width), 3.0, dtype=_dt(dtype), device="cuda")
+    L.moonep_checkpoint_dispatch(sh, width, q, s, torch.from_numpy(skip).cuda(), dst)
+    torch.cuda.synchronize()
+    val = F.checkpoint_values(q.cpu().numpy(), s.cpu().numpy()[:, :-(-width // 32)])
+    want = torch.full((N * K, width), 3.0, dtype=torch.float64)
+    for u in range(N * K):
+        if 0 <= skip[u] < N * K:
+            want[skip[u]] = torch.from_numpy(val[u // K])
+    # e4m3 times a power of two is exact in both types (bfloat16 subnormals apart)
+    assert torch.equal(dst.cpu(), want.float().to(_dt(dtype)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_inf_and_nan_stay_in_their_block(dtype):
+    say("checkpoint nan", dtype)
+    N, width = 6, 96
+    x = torch.ones((N, width), dtype=_dt(dtype), device="cuda")
+    x[0, 40], x[1, 0], x[2, 95] = float("nan"), float("inf"), float("-inf")
+    sh = _shape(N, 1, width, 64, dtype)
+    q, s = C.buffers(N, width)
+    L.moonep_checkpoint_quantize(sh, width, x, q, s)
+    dst = torch.zeros_like(x)
+    L.moonep_checkpoint_dispatch(sh, width, q, s, torch.arange(N, dtype=torch.int32, device="cuda"), dst)
+    torch.cuda.synchronize()
+    want = torch.ones((N, width))
+    want[0, 32:64] = want[1, :32] = want[2, 64:] = float("nan")
+    assert torch.equal(torch.isnan(dst).cpu(), torch.isnan(want))
+    assert bool((dst[~torch.isnan(dst)] == 1).all())
+
+
+def _h(rng, rows, Hp):
+    h = rng.standard_normal((rows, 2 * Hp)) * 3.0
+    h[0, :32] = np.linspace(-30, 30, 32)
+    if rows > 2:
+        h[1] = 0.0
+        h[2] *= 1e-6
+    return h.astype(np.float32)
+
+
+@pytest.mark.parametrize("dtype,N,K,Hp", [("bf16", 1, 1, 32), ("bf16", 33, 2, 96), ("fp32", 7, 3, 64),
+                                          ("bf16", 40, 8, 1408), ("fp32", 65, 1, 160), ("fp32", 5, 2, 2048)])
+@pytest.mark.parametrize("gated", [True, False])
+def test_swiglu_forward_and_backward(dtype, N, K, Hp, gated):
+    say("checkpoint swiglu", dtype, N, K, Hp, gated)
+    rows = N * K
+    sh = _shape(N, K, 64, Hp, dtype)
+    rng = np.random.default_rng(Hp + N)
+    hn = _h(rng, rows, Hp)
+    h = torch.from_numpy(hn).cuda()
+    q, s = C.buffers(rows, 2 * Hp)
+    q.fill_(0xAA), s.fill_(0xAA)
+    act = torch.full((rows, Hp), float("nan"), dtype=_dt(dtype), device="cuda")
+    L.moonep_swiglu_checkpoint(sh, h, act, q, s)
+    plain = torch.empty_like(act)
+    L.moonep_swiglu(sh, h, plain, None)
+    torch.cuda.synchronize()
+    assert torch.equal(act, plain)
+    _assert_bytes(q, s, hn.astype(np.float64), 2 * Hp)
+    hv = F.checkpoint_values(q.cpu().numpy(), s.cpu().numpy()[:, :2 * Hp // 32])
+    gate, up = FF.gate_up_columns(Hp)
+    gv, uv = hv[:, gate], hv[:, up]
+    dan = rng.standard_normal((rows, Hp)).astype(np.float32)
+    gates = rng.random((N, K)).astype(np.float32)
+    src = rng.permutation(rows).astype(np.int32)
+    if rows > 4:
+        src[4] = -1
+        gates.reshape(-1)[src[3]] = 0.0
+    ok = src >= 0
+    w = np.where(ok, gates.reshape(-1)[np.where(ok, src, 0)], 0.0)[:, None] if gated else np.ones((rows, 1))
+    a_out, dh = torch.empty_like(act), torch.empty((rows, 2 * Hp), dtype=_dt(dtype), device="cuda")
+    dg = torch.full((N, K), 9.0, device="cuda")
+    L.moonep_swiglu_backward_checkpoint(
+        sh, q, s, torch.from_numpy(dan).cuda(), torch.from_numpy(src).cuda() if gated else None,
+        torch.from_numpy(gates).cuda() if gated else None, a_out, dh, dg if gated else None)
+    torch.cuda.synchronize()
+    sg = FF.sigmoid(gv)
+    a_ref = gv * sg * uv
+    # half a step of the stored type, and float32 evaluation: expf within 2 ulp of a rounded
+    # argument (|g| <= 30 + half a step), 6 products and sums -> 2^-18 of the terms' magnitude
+    step = 2.0 ** -8 * (1 + 2.0 ** -7) if dtype == "bf16" else 0.0
+    ev = 2.0 ** -18
+    got = a_out.double().cpu().numpy()
+    assert (np.abs(got - w * a_ref) <= (step + ev) * np.abs(w * a_ref) + 1e-37).all()
+    ref, terms = np.zeros((rows, 2 * Hp)), np.zeros((rows, 2 * Hp))
+    ref[:, gate] = w * dan * uv * (sg + gv * sg * FF.sigmoid(-gv))
+    terms[:, gate] = np.abs(w * dan * uv) * (sg + np.abs(gv) * sg * (1 - sg) + np.abs(gv) * sg * 2.0 ** -6)
+    ref[:, up] = w * dan * gv * sg
+    terms[:, up] = np.abs(ref[:, up])
+    assert (np.abs(dh.double().cpu().numpy() - ref) <= step * np.abs(ref) + ev * terms + 1e-37).all()
+    if gated:
+        d = dg.cpu().numpy().reshape(-1).astype(np.float64)
+        want = (a_ref * dan).sum(1)
+        mag = np.abs(a_ref * dan).sum(1)
+        assert (np.abs(d[src[ok]] - want[ok]) <= (ev + Hp * U) * mag[ok] + 1e-37).all()
+        untouched = np.setdiff1d(np.arange(rows), src[ok])
+        assert (d[untouched] == 9.0).all()
+
+
+def test_backward_of_an_empty_plan_writes_zeros():
+    say("checkpoint empty plan")
+    N, K, Hp = 5, 2, 64
+    sh = _shape(N, K, 64, Hp, "bf16")
+    q, s = C.buffers(N * K, 2 * Hp)
+    q.fill_(0x7F), s.fill_(0xFF)            # stale NaN bytes
+    act = torch.ones((N * K, Hp), dtype=torch.bfloat16, device="cuda")
+    dh = torch.ones((N * K, 2 * Hp), dtype=torch.bfloat16, device="cuda")
+    dg = torch.full((N, K), 9.0, device="cuda")
+    L.moonep_swiglu_backward_checkpoint(
+        sh, q, s, torch.full((N * K, Hp), float("nan"), device="cuda"),
+        torch.full((N * K,), -1, dtype=torch.int32, device="cuda"), torch.ones((N, K), device="cuda"),
+        act, dh, dg)
+    torch.cuda.synchronize()
+    assert not act.any() and not dh.any() and bool((dg == 9.0).all())
+
+
+def _ffn(cfg, checkpoint, d, **kw):
+    return MoEFFN(cfg, backward=True, w1_all=d["W1"], w2_all=d["W2"], checkpoint=checkpoint, **kw)
+
+
+def _data(cfg, alpha=2.0, seed=0):
+    r = make_routing(cfg, 3.0, seed=seed, alpha=alpha)
+    d = make_dense(cfg, "cuda", seed, which=("x", "W1", "W2", "dyH"), w_rows=cfg.E + cfg.R * cfg.B)
+    return r, d, torch.from_numpy(r.topk_idx).cuda(), torch.from_numpy(r.gates).cuda()
+
+
+# the first layer has segments beyond one tile and short tails, the second splits its tails
+# into their own launch (four rounds of full tiles)
+@pytest.mark.parametrize("kw,alpha", [
+    (dict(R=4, S=200, E=16, K=4, H=128, Hp=192), 2.5),
+    (dict(R=8, S=4096, E=64, K=8, H=64, Hp=320), 1.0),
+    (dict(R=1, S=1, E=4, K=1, H=64, Hp=64), 1.0),
+])
+def test_fused_gemm_gives_the_same_bytes(kw, alpha):
+    cfg = small_cfg(name="ck_fused", **kw)
+    say("checkpoint fused gemm", kw)
+    r, d, topk, gates = _data(cfg, alpha)
+    a, b = _ffn(cfg, True, d), _ffn(cfg, True, d, fused=False)
+    for l in (a, b):
+        l.hq.fill_(0xAA), l.hscales.fill_(0xAA)
+        l.act.view(torch.int16).fill_(-1)
+        l.forward(topk, d["x"], gates)
+    torch.cuda.synchronize()
+    for name in ("act", "hq", "hscales", "y"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+    hb = b.h.cpu().numpy()[:64].astype(np.float64)
+    _assert_bytes(a.hq[:64], a.hscales[:64], hb, 2 * cfg.Hp)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_ffn_on_checkpoints(dtype):
+    """The forward is the plain layer's, bit for bit; the gradients are those of the formula
+    at the checkpointed x and h (oracle in float64), and near the plain layer's."""
+    cfg = small_cfg(name="ck_ffn", R=4, S=40, E=8, K=2, H=128, Hp=64, dtype=dtype)
+    say("checkpoint ffn", dtype)
+    r, d, topk, gates = _data(cfg)
+    plain, ck = _ffn(cfg, False, d), _ffn(cfg, True, d)
+    y0, y1 = plain.forward(topk, d["x"], gates).clone(), ck.forward(topk, d["x"], gates)
+    assert torch.equal(y0, y1)
+    dx0, dx1 = plain.backward(d["dyH"], gates), ck.backward(d["dyH"], gates)
+    dg0, dg1 = plain.gate_grad(d["dyH"]), ck.gate_grad(d["dyH"])
+    torch.cuda.synchronize()
+    # the formula at the checkpointed values
+    xv = F.checkpoint_values(*F.checkpoint(d["x"].double().cpu().numpy()))
+    K, Hp = cfg.K, cfg.Hp
+    sm = ck.slot_map.cpu().numpy()
+    hv = F.checkpoint_values(ck.hq.cpu().numpy(), ck.hscales.cpu().numpy()[:, :2 * Hp // 32])[sm]
+    W1, W2 = d["W1"].double().cpu().numpy(), d["W2"].double().cpu().numpy()
+    dy, g = d["dyH"].double().cpu().numpy(), r.gates.astype(np.float64)
+    gc, uc = FF.gate_up_columns(Hp)
+    dx, dW1, dW2 = np.zeros((cfg.N, cfg.H)), np.zeros((cfg.E, cfg.H, 2 * Hp)), np.zeros((cfg.E, Hp, cfg.H))
+    dgr = np.zeros((cfg.N, K))
+    for t in range(cfg.N):
+        for k in range(K):
+            u, e = t * K + k, int(r.topk_idx[t, k])
+            gv, uv = hv[u, gc], hv[u, uc]
+            s = FF.sigmoid(gv)
+            a = gv * s * uv
+            da = dy[t] @ W2[e].T
+            dgr[t, k] = a @ da
+            dh = np.zeros(2 * Hp)
+            dh[gc] = g[t, k] * da * uv * (s + gv * s * (1 - s))
+            dh[uc] = g[t, k] * da * gv * s
+            # the two operands that the layer stores in its dtype, rounded once as it rounds them
+            dh = FF.round_to(dh, dtype)
+            dx[t] += dh @ W1[e].T
+            dW1[e] += np.outer(xv[t], dh)
+            dW2[e] += np.outer(FF.round_to(g[t, k] * a, dtype), dy[t])
+    tol = 1e-2 if dtype == "bf16" else 1e-5     # the layer's bar, of the RMS
+    for got, want in ((dx1, dx), (ck.grad1, dW1), (ck.grad2, dW2), (dg1, dgr)):
+        err = np.abs(got.double().cpu().numpy() - want).max() / np.sqrt((want ** 2).mean())
+        assert err <= tol, err
+    # 8-bit values are off by 2^-4 at most, a few per cent on average
+    for a, b in ((dx0, dx1), (plain.grad1, ck.grad1), (plain.grad2, ck.grad2), (dg0, dg1)):
+        a, b = a.double(), b.double()
+        assert float((a - b).norm() / a.norm()) < 2.0 ** -4
+    assert not ck.red1.any() and not ck.red2.any()
+
+
+def test_layers_share_their_slot_buffers():
+    """Two layers on one set of slot buffers: forward 0, forward 1, backward 1, backward 0
+    gives each layer the gradients it has alone."""
+    cfg = small_cfg(name="ck_share", R=2, S=50, E=8, K=2, H=64, Hp=128)
+    say("checkpoint shared buffers")
+    r, d0, topk, gates = _data(cfg)
+    _, d1, _, _ = _data(cfg, seed=1)
+    alone = [_ffn(cfg, True, d) for d in (d0, d1)]
+    first = _ffn(cfg, True, d0)
+    both = [first, _ffn(cfg, True, d1, scratch=first)]
+    assert both[1].xp is first.xp and both[1].act is first.act
+    for l, d in zip(alone, (d0, d1)):
+        l.forward(topk, d["x"], gates)
+        l.backward(d["dyH"], gates)
+    for l, d in zip(both, (d0, d1)):
+        l.forward(topk, d["x"], gates)
+    for l, d in reversed(list(zip(both, (d0, d1)))):
+        l.backward(d["dyH"], gates)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        for name in ("y", "dx", "grad1", "grad2", "dgates"):
+            assert torch.equal(getattr(a, name), getattr(b, name)), name
+    with pytest.raises(ValueError, match="shape"):
+        _ffn(small_cfg(name="ck_other", R=2, S=51, E=8, K=2, H=64, Hp=128), True, d0, scratch=first)
+    with pytest.raises(ValueError, match="checkpoints"):
+        _ffn(cfg, False, d0, scratch=first)
+
+
+def test_checkpoint_ffn_graph_replays_match_eager():
+    cfg = small_cfg(name="ck_graph", R=4, S=64, E=16, K=4, H=128, Hp=192)
+    say("checkpoint graph")
+    r, d, topk, gates = _data(cfg)
+    l = _ffn(cfg, True, d)
+
+    def run():
+        l.forward(topk, d["x"], gates)
+        l.backward(d["dyH"], gates)
+
+    keys = ("y", "dx", "grad1", "grad2", "dgates", "hq", "xq")
+    run()
+    torch.cuda.synchronize()
+    want = {k: getattr(l, k).clone() for k in keys}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for rep in range(3):
+        l.grad1.zero_(), l.grad2.zero_()
+        for k in ("y", "dx", "dgates"):
+            getattr(l, k).fill_(float("nan"))
+        _ = torch.randn(4096, device="cuda").sum().item()
+        g.replay()
+        torch.cuda.synchronize()
+        for k, v in want.items():
+            assert torch.equal(getattr(l, k), v), (rep, k)

@@ -1,0 +1,308 @@
+"""Router and gates' gradient on the GPU against the float64 oracle: choices equal, gates
+and gradients within their float32 error bounds."""
+import dataclasses
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe as M
+from oracle import route as RT
+from redundant_expert_balancing_amd import _lib as L
+from redundant_expert_balancing_amd.layer import MoEProjection
+from redundant_expert_balancing_amd.router import MoERouter
+from redundant_expert_balancing_amd.synth import LayerConfig, make_dense
+
+from gpu_helpers import say, small_cfg
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def cfg_of(N, E, K, mode="train"):
+    return LayerConfig("route", 1, N, E, K, E, 64, 64, "bf16", mode, (1.0,))
+
+
+def to(logits, dtype):
+    return torch.from_numpy(np.asarray(logits, np.float32)).cuda().to(
+        torch.bfloat16 if dtype == "bf16" else torch.float32)
+
+
+def check(cfg, logits, bias, dtype="fp32", **kw):
+    """One route and one backward against the oracle."""
+    rt = MoERouter(cfg, dtype=dtype, backward=True, **kw)
+    t = to(logits, dtype)
+    b = None if bias is None else torch.from_numpy(np.asarray(bias, np.float32)).cuda()
+    rt.topk_idx.fill_(-7)
+    rt.gates.fill_(-7.0)
+    ids, gates = rt.forward(t, b)
+    torch.cuda.synchronize()
+    lh = t.double().cpu().numpy()
+    bh = None if b is None else b.double().cpu().numpy()
+    want_ids, want = RT.route(lh, bh, cfg.K, **kw)
+    got = gates.double().cpu().numpy()
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    # exp of a rounded argument x: relative error (|x| + 2) u; sums of at most E positive
+    # terms add E u at most, two divisions, a product and the sigmoid's own sum 8 u
+    with np.errstate(invalid="ignore"):
+        x = np.nan_to_num(np.abs(np.where(np.isfinite(lh), lh, 0)).clip(max=200).max(), nan=0)
+    tol = (2 * x + cfg.E + 16) * U
+    ok = ~np.isnan(want)
+    assert (np.abs(got - want)[ok] <= tol * np.abs(want)[ok] + 1e-37).all()
+    if cfg.N == 0:
+        return
+    rng = np.random.default_rng(5)
+    dg = rng.standard_normal((cfg.N, cfg.K)).astype(np.float32)
+    rt.dlogits.fill_(float("nan"))
+    d = rt.backward(t, torch.from_numpy(dg).cuda(), b)
+    torch.cuda.synchronize()
+    bk = dict(score=kw.get("score", "softmax"), renorm=kw.get("renorm", True),
+              scale=kw.get("scale", 1.0))
+    ref = RT.route_backward(lh, bh, want_ids, got, dg, **bk)
+    d = d.double().cpu().numpy()
+    rows = ~np.isnan(got).any(1)
+    # terms summed: |g| (|dg| + sum |q dg|) at the chosen, |p| sum |g dg| everywhere else
+    ga = np.abs(np.nan_to_num(got))
+    terms = (ga * np.abs(dg)).sum(1, keepdims=True) * (1 + 1 / bk["scale"]) + 1e-30
+    bound = (2 * x + cfg.E + 2 * cfg.K + 16) * U * terms
+    if dtype == "bf16":
+        bound = bound + np.abs(ref) * 2.0 ** -8 * (1 + 2.0 ** -7)
+    assert (np.abs(d - ref)[rows] <= bound[rows]).all()
+    return ids, gates
+
+
+GROUPS = [dict(), dict(groups=4, top_groups=2, group_top=2), dict(groups=4, top_groups=3, group_top=1)]
+
+
+@pytest.mark.parametrize("score,renorm,dtype", list(itertools.product(
+    ["softmax", "sigmoid"], [True, False], ["fp32", "bf16"])))
+@pytest.mark.parametrize("bias", [False, True])
+def test_choice_gates_and_gradient(score, renorm, dtype, bias):
+    say("route", score, renorm, dtype, bias)
+    for N, E, K in ((1, 8, 1), (3, 64, 8), (67, 60, 7), (33, 384, 8), (5, 1024, 32), (130, 100, 3),
+                    (9, 264, 6), (1, 256, 8)):
+        for g in GROUPS:
+            if K > E // 4 * g.get("top_groups", 4):
+                continue
+            rng = np.random.default_rng(N * E + K)
+            b = 0.05 * rng.standard_normal(E) if bias else None
+            check(cfg_of(N, E, K), rng.standard_normal((N, E)), b, dtype, score=score,
+                  renorm=renorm, scale=2.5, **g)
+
+
+@pytest.mark.parametrize("E", [1, 2, 63, 65, 97])
+def test_odd_expert_counts(E):
+    say("route odd", E)
+    rng = np.random.default_rng(E)
+    for dtype in ("fp32", "bf16"):
+        for score in ("softmax", "sigmoid"):
+            check(cfg_of(37, E, min(E, 5)), rng.standard_normal((37, E)), None, dtype, score=score,
+                  renorm=False)
+
+
+def test_empty_layer():
+    say("route empty")
+    rt = MoERouter(cfg_of(0, 16, 2), backward=True)
+    t = torch.zeros((1, 16), device="cuda")
+    rt.gates.fill_(7.0)
+    rt.forward(t)
+    rt.backward(t, torch.zeros((1, 2), device="cuda"))
+    torch.cuda.synchronize()
+    assert bool((rt.gates == 7.0).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", GROUPS)
+def test_ties_go_to_the_lower_id(score, groups):
+    """Few distinct logits: equal scores everywhere, with and without an all-zero bias."""
+    say("route ties", score, groups)
+    rng = np.random.default_rng(3)
+    l = rng.integers(-1, 2, (65, 64)).astype(float)
+    for b in (None, np.zeros(64)):
+        for renorm in (True, False):
+            check(cfg_of(65, 64, 6), l, b, "bf16", score=score, renorm=renorm, **groups)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_values_next_to_a_border(score):
+    """Biased scores that differ by far less than float32 resolves keep their order: logits
+    one float32 step apart, and biases that almost cancel the difference of two scores."""
+    say("route border", score)
+    rng = np.random.default_rng(4)
+    N, E = 64, 32
+    base = np.float32(1.5)
+    l = np.full((N, E), base)
+    for g in range(N):
+        l[g] = base + np.float32(2.0 ** -23) * rng.integers(0, 4, E).astype(np.float32)
+    check(cfg_of(N, E, 8), l, np.full(E, 0.25), score=score)
+    check(cfg_of(N, E, 8), l, None, score=score)
+    l = rng.standard_normal((N, E)).astype(np.float32)
+    s = 1 / (1 + np.exp(-l[0].astype(np.float64)))
+    if score == "softmax":
+        s = np.exp(l[0].astype(np.float64)) / np.exp(l[0].astype(np.float64)).sum()
+    check(cfg_of(N, E, 8), np.repeat(l[:1], N, 0), (1.0 - s).astype(np.float32), score=score)
+    check(cfg_of(N, E, 8), np.repeat(l[:1], N, 0), (1.0 - s).astype(np.float32), score=score,
+          groups=4, top_groups=2, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_masks_infinities_and_nan(score, dtype):
+    say("route masks", score, dtype)
+    rng = np.random.default_rng(6)
+    E, K = 48, 4
+    lowest = float(torch.finfo(torch.bfloat16).min)
+    l = rng.standard_normal((40, E))
+    l[0] = -np.inf                       # nothing left
+    l[1, 2:] = -np.inf                   # fewer than K left
+    l[2] = lowest                        # masks of the type's lowest value
+    l[3, 1:] = lowest
+    l[4, :] = -1000.0
+    l[5, 7] = np.nan
+    l[6, 3] = np.inf
+    l[7, :3] = np.inf
+    l[8, 0] = 1000.0
+    l[9] = -90.0 + rng.standard_normal(E)
+    l[10, ::2] = -np.inf
+    b = 0.1 * rng.standard_normal(E)
+    off = b.copy()
+    off[5] = off[11] = -np.inf           # switched off ...
+    l[11, 5] = np.nan                    # ... whatever their logits hold
+    l[12, 11] = np.inf
+    high = b.copy()
+    high[9] = np.inf
+    for renorm in (True, False):
+        for g in GROUPS:
+            for bias in (None, off, high):
+                check(cfg_of(40, E, K), l, bias, dtype, score=score, renorm=renorm, **g)
+    most = np.full(E, -np.inf)
+    most[[3, 40]] = 0.0
+    check(cfg_of(40, E, K), l, most, dtype, score=score)
+    bad = b.copy()
+    bad[4] = np.nan
+    check(cfg_of(40, E, K), l, bad, dtype, score=score)
+
+
+def test_backward_skips_bad_ids_and_adds_repeated_ones():
+    say("route backward ids")
+    cfg = cfg_of(2, 8, 3)
+    rt = MoERouter(cfg, score="sigmoid", renorm=False, backward=True)
+    l = torch.zeros((2, 8), device="cuda")
+    rt.topk_idx.copy_(torch.tensor([[1, 1, 9], [-1, 2, 3]], dtype=torch.int32))
+    rt.gates.fill_(0.5)
+    d = rt.backward(l, torch.ones((2, 3), device="cuda"))
+    torch.cuda.synchronize()
+    want = torch.zeros((2, 8))
+    want[0, 1], want[1, 2], want[1, 3] = 0.5, 0.25, 0.25
+    assert torch.equal(d.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype,width,K", [("fp32", 64, 1), ("fp32", 76, 3), ("bf16", 8, 2),
+                                           ("bf16", 1408, 8), ("fp32", 1028, 9), ("bf16", 7168, 8),
+                                           ("bf16", 264, 32)])
+def test_gate_grad(dtype, width, K):
+    say("gate grad", dtype, width, K)
+    N, E = 53, 64
+    other = 64
+    sh = L.Shape(1, N, E, K, E, width, other, L.TRAIN, L.BF16 if dtype == "bf16" else L.FP32)
+    rng = np.random.default_rng(width)
+    src = torch.from_numpy(rng.standard_normal((N * K, width)).astype(np.float32)).cuda()
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    dy = torch.from_numpy(rng.standard_normal((N, width)).astype(np.float32)).cuda().to(dt)
+    perm = rng.permutation(N * K).astype(np.int32)
+    perm[3], perm[N * K - 1] = -1, N * K + 5          # slots without a row
+    out = torch.full((N, K), float("nan"), device="cuda")
+    src[torch.from_numpy(np.setdiff1d(np.arange(N * K), perm)).cuda()] = float("nan")
+    L.moonep_gate_grad(sh, width, src, torch.from_numpy(perm).cuda(), dy, out)
+    torch.cuda.synchronize()
+    ok = (perm >= 0) & (perm < N * K)
+    a = src.double().cpu().numpy()[np.where(ok, perm, 0)]
+    b = np.repeat(dy.double().cpu().numpy(), K, 0)
+    want = np.where(ok, (a * b).sum(1), 0.0)
+    mag = np.where(ok, (np.abs(a) * np.abs(b)).sum(1), 0.0)
+    got = out.double().cpu().numpy().reshape(-1)
+    assert (got[~ok] == 0).all()
+    # a sum of `width` products in any order: at most width roundings of the magnitude sum
+    assert (np.abs(got - want) <= width * U * mag)[ok].all()
+
+
+def test_router_and_layer_together():
+    """logits -> route -> plan .. combine, then dy -> gates' gradient -> dlogits, against the
+    dense oracle's differences through the gates."""
+    cfg = small_cfg(name="route_layer", R=4, S=24, E=16, K=3, H=64, Hp=64, dtype="fp32")
+    say("router and layer", cfg.name)
+    d = make_dense(cfg, "cuda", 0, which=("x", "W", "dy"), w_rows=cfg.E + cfg.R * cfg.B)
+    rng = np.random.default_rng(0)
+    logits = torch.from_numpy(rng.standard_normal((cfg.N, cfg.E)).astype(np.float32)).cuda()
+    rt = MoERouter(cfg, score="sigmoid", backward=True, scale=1.5, groups=4, top_groups=2, group_top=2)
+    layer = MoEProjection(cfg, backward=True, w_all=d["W"])
+    ids, gates = rt.forward(logits)
+    y = layer.forward(ids, d["x"], gates)
+    dl = rt.backward(logits, layer.gate_grad(d["dy"]))
+    torch.cuda.synchronize()
+    kw = dict(score="sigmoid", scale=1.5, groups=4, top_groups=2, group_top=2)
+    lh = logits.double().cpu().numpy()
+    want_ids, want_g = RT.route(lh, None, cfg.K, **kw)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    W = d["W"][:cfg.E].cpu().numpy()
+    x, dy = d["x"].cpu().numpy(), d["dy"].cpu().numpy()
+    outs = M.dense_expert_outputs(x, W, want_ids).reshape(cfg.N, cfg.K, cfg.Hp)
+    ref = (outs * want_g[..., None]).sum(1)
+    assert np.abs(y.cpu().numpy() - ref).max() <= 1e-5 * np.sqrt((ref ** 2).mean())
+    # the loss <y, dy> as a function of the logits, by central differences
+    dgates = (outs * dy[:, None, :].astype(np.float64)).sum(-1)
+    got = dl.double().cpu().numpy()
+    h = 1e-5
+    for g in range(0, cfg.N, 7):
+        for e in range(cfg.E):
+            f = []
+            for s in (1, -1):
+                row = lh[g:g + 1].copy()
+                row[0, e] += s * h
+                i, v = RT.route(row, None, cfg.K, **kw)
+                assert np.array_equal(i[0], want_ids[g])
+                f.append((v * dgates[g]).sum())
+            diff = (f[0] - f[1]) / (2 * h)
+            scale = np.abs(dgates[g]).max()
+            assert abs(got[g, e] - diff) <= 1e-5 * scale + 1e-6
+
+
+def test_router_graph_capture_and_stream():
+    """Route, gates' gradient and backward captured in one graph and replayed after eager
+    work; and issued on a side stream."""
+    cfg = small_cfg(name="route_graph", R=2, S=40, E=32, K=4, H=64, Hp=128)
+    say("route graph")
+    g0 = torch.Generator(device="cuda").manual_seed(0)
+    logits = torch.randn((cfg.N, cfg.E), generator=g0, device="cuda")
+    d = make_dense(cfg, "cuda", 0, which=("x", "W", "dy"), w_rows=cfg.E + cfg.R * cfg.B)
+    rt = MoERouter(cfg, score="sigmoid", backward=True)
+    layer = MoEProjection(cfg, backward=True, w_all=d["W"])
+
+    def run():
+        ids, gates = rt.forward(logits)
+        layer.forward(ids, d["x"], gates)
+        rt.backward(logits, layer.gate_grad(d["dy"]))
+
+    run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (rt.topk_idx, rt.gates, rt.dlogits, layer.dgates)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, (rt.topk_idx, rt.gates, rt.dlogits, layer.dgates)))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for rep in range(3):
+        for t in (rt.topk_idx, rt.gates, rt.dlogits, layer.dgates):
+            t.fill_(0)
+        _ = torch.randn(4096, device="cuda").sum().item()
+        g.replay()
+        torch.cuda.synchronize()
+        got = (rt.topk_idx, rt.gates, rt.dlogits, layer.dgates)
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), rep
