@@ -42,6 +42,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "lds_dma.h"
 
 namespace moonep {
 
@@ -247,10 +248,7 @@ __global__ __launch_bounds__(1024) void gemm_tiles_kernel(const int32_t* __restr
 //   m/n-contiguous operand [64][COLS]: one row per k, chunk c of row k at c ^ swz_mn(k);
 //     read with ds_read_b64_tr_b16, which hands each lane 4 consecutive k of one
 //     column, the MFMA operand layout, without a transpose anywhere else.
-typedef int v4i_t __attribute__((ext_vector_type(4)));
 typedef short v4s_t __attribute__((ext_vector_type(4)));
-constexpr int kRsrcFlags = 0x00020000;      // raw (unswizzled) 32-bit data, gfx9 family
-constexpr uint32_t kOffNone = 0x80000000u;  // an offset past every range used here
 constexpr int kBK = 64;                     // k per pipeline step
 constexpr int kBlockE = 4, kBlockN = 8;     // FWD/DGRAD tile order block
 constexpr int kTailGroup = 8;               // entries per tile-order block of queued FWD calls
@@ -265,50 +263,11 @@ constexpr int kEpiAhead = 4;                // WGRAD epilogue: row blocks read a
 constexpr int kStreamStore = 18;
 constexpr int kStreamOutMaxK = 1536;
 
-__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  // the range is uniform; readfirstlane keeps it (and the descriptor) in scalar
-  // registers even where it was computed with 64-bit vector compares
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0,
-                                           __builtin_amdgcn_readfirstlane((int)bytes), kRsrcFlags);
-}
-
-__device__ inline uint32_t clamp_bytes(int64_t b) {
-  return b <= 0 ? 0u : (b >= int64_t(kOffNone) ? kOffNone : uint32_t(b));
-}
-
-// One 16-byte-per-lane DMA into LDS at byte address lds (uniform). Issued as
-// inline assembly so that the compiler's wait-count pass does not wait for all
-// outstanding DMAs at every LDS read; the k-loop waits for exactly the steps it
-// needs (wait_vm).
-__device__ inline void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(r), "s"(__builtin_amdgcn_readfirstlane(lds))
-               : "memory");
-}
-
-// Wait until at most n of this wavefront's vector memory operations are pending.
-template <int n>
-__device__ inline void wait_vm() {
-  static_assert(n >= 0 && n < 64, "vmcnt range");
-  // s_waitcnt simm16: vmcnt[3:0] in bits 3:0, vmcnt[5:4] in bits 15:14, expcnt and
-  // lgkmcnt left at their maxima (no wait)
-  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
-__device__ inline int swz_k(int r) { return (r >> 1) & 7; }
 // the 4 k-rows one 16-lane group reads take disjoint 32-byte column slots of a
 // 256-byte bank window (k & 3), and the group 8 rows further on, which shares the
 // half-wavefront's pass, takes the 8 slots left free (k & 8)
 __device__ inline int swz_mn(int k) {
   return ((k & 1) ? 6 : 0) ^ ((k & 2) ? 10 : 0) ^ ((k & 8) ? 2 : 0);
-}
-
-typedef __attribute__((address_space(3))) char lds_char;
-
-// LDS byte address of a pointer into __shared__ memory (address-space cast).
-__device__ inline uint32_t lds_addr(const void* p) {
-  return uint32_t(reinterpret_cast<uintptr_t>((const lds_char*)p));
 }
 
 // k-contiguous operand tile: ROWS rows x 64 k.

@@ -3,13 +3,15 @@
 // takes e2m1 operands and one scale byte per 32 values). Layouts: moonep.h, "Experts in 4
 // bits"; the weight layout is the order in which a wavefront's lanes take an operand, so
 // every load of it is 1 KiB in a row.
+#include <type_traits>
+
 #include "common.h"
+#include "lds_dma.h"
 
 namespace moonep {
 
 constexpr int kMxThreads = 256;
 typedef float v4f_t __attribute__((ext_vector_type(4)));
-typedef int v4i_t __attribute__((ext_vector_type(4)));
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 
 __device__ inline uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
@@ -140,7 +142,7 @@ struct MxArgs {
   const TileEntry* tiles;
   const int32_t* ntiles;
   int K, Hp, KT, KC;
-  int64_t NK;
+  int64_t NK, xrows;
 };
 
 constexpr int kMxRows = 64;   // rows of a work entry
@@ -193,6 +195,193 @@ __global__ __launch_bounds__(256) void mx_gemm_kernel(MxArgs a) {
       for (int j = 0; j < 4; ++j)
         a.c[(int64_t(te.rowbase) + row) * a.Hp + n0 + j * 16 + (lane & 15)] = acc[j][r];
     }
+  }
+}
+
+// One 16 x 16 x 128 product of e2m1 operands (format 4); byte BYTE of each scale word counts.
+template <int BYTE>
+__device__ inline v4f_t mfma_e2m1(v8i_t a, v8i_t b, v4f_t c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, BYTE, sa, BYTE, sb);
+}
+
+// ---- tiled form: 128 x 256 output tiles, four wavefronts side by side in N (128 x 64 each),
+// 256 k per step.
+struct MxTile {
+  static constexpr int BM = 128, BN = 256, WAVES = 4;
+  static constexpr int STEPB = 128;                     // bytes of a row per step
+  static constexpr int A_BYTES = BM * STEPB;            // LDS per stage
+  static constexpr int S_BYTES = BM * 16;               // LDS per chunk of scales
+  static constexpr int FM = BM / 16, FN = 4;
+};
+
+template <bool GATHER>
+__global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
+  typedef MxTile T;
+  __shared__ __align__(1024) char smem[2 * T::A_BYTES + 2 * T::S_BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds0 = lds_addr(smem);
+  const char* s_scale = smem + 2 * T::A_BYTES;
+  const int NT = (a.Hp + T::BN - 1) / T::BN;
+  const int nent = *a.ntiles;
+  const int64_t total = int64_t(nent) * NT;
+  const int G = gridDim.x;
+  // the workgroups of one XCD take a contiguous run of tiles
+  const int slot = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
+  const int nsteps = (a.KT + 1) / 2;
+  const uint32_t qrow = uint32_t(a.KT) * 64, srow = uint32_t(a.KC) * 16;   // bytes per A row
+  const int r16 = lane & 15, kb = lane >> 4;
+
+  for (int64_t tau = slot; tau < total; tau += G) {
+    // blocks of 8 entries x all N-tiles, entries fastest inside groups of 8 N-tiles
+    const int64_t eb = tau / (int64_t(8) * NT);
+    const int j8 = int(tau % (int64_t(8) * NT));
+    const int ge = int(min(int64_t(8), nent - eb * 8));
+    const int ent = int(eb) * 8 + j8 % ge;
+    const int n0 = j8 / ge * T::BN;
+    const TileEntry e = a.tiles[ent];
+    const int rowbase = __builtin_amdgcn_readfirstlane(e.rowbase + e.m0);
+    const int wrow = __builtin_amdgcn_readfirstlane(e.wrow);
+    const int rows_valid = __builtin_amdgcn_readfirstlane(min(T::BM, e.n - e.m0));
+    const int col0 = n0 + wid * 64;
+    const bool idle = col0 >= a.Hp;    // uniform
+
+    // this lane's rows of A: 4 DMAs of 8 rows a wavefront, and one row of scales
+    uint32_t va[4], vs = kOffNone;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = (wid + 4 * j) * 8 + (lane >> 3);
+      const int c = (lane & 7) ^ swz_k(row);
+      uint32_t r = kOffNone;
+      if (row < rows_valid) {
+        r = row;
+        if (GATHER) {
+          const int u = a.src_index[rowbase + row];
+          r = u >= 0 && u < a.NK ? uint32_t(u) / uint32_t(a.K) : kOffNone;
+        }
+      }
+      va[j] = r == kOffNone ? kOffNone : r * qrow + c * 16;
+    }
+    if (wid < 2) {
+      const int row = wid * 64 + lane;
+      uint32_t r = kOffNone;
+      if (row < rows_valid) {
+        r = row;
+        if (GATHER) {
+          const int u = a.src_index[rowbase + row];
+          r = u >= 0 && u < a.NK ? uint32_t(u) / uint32_t(a.K) : kOffNone;
+        }
+      }
+      vs = r == kOffNone ? kOffNone : r * srow;
+    }
+    const int64_t first = GATHER ? 0 : rowbase;
+    const int64_t span = GATHER ? a.xrows : rows_valid;
+    const __amdgpu_buffer_rsrc_t ars = make_rsrc(a.xq + first * qrow, clamp_bytes(span * qrow));
+    const __amdgpu_buffer_rsrc_t srs = make_rsrc(a.xs + first * srow, clamp_bytes(span * srow));
+    const int64_t tile16 = int64_t(wrow) * (a.Hp / 16) + (idle ? 0 : col0 / 16);
+    const __amdgpu_buffer_rsrc_t brs = make_rsrc(a.wq + tile16 * a.KT * 1024, uint32_t(4 * a.KT) * 1024);
+    const __amdgpu_buffer_rsrc_t bss = make_rsrc(a.ws + tile16 * a.KC * 256, uint32_t(4 * a.KC) * 256);
+
+    auto issue_a = [&](int k) {     // step k into stage k % 2
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        dma16(ars, va[j], uint32_t(k) * T::STEPB, lds0 + (k & 1) * T::A_BYTES + (wid + 4 * j) * 1024);
+    };
+    auto issue_s = [&](int c) {     // scales of chunk c
+      if (wid < 2)
+        dma16(srs, vs, uint32_t(c) * 16, lds0 + 2 * T::A_BYTES + (c & 1) * T::S_BYTES + wid * 1024);
+    };
+    auto load_b = [&](int k, v4i_t (&b)[2][T::FN]) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+          b[t][j] = __builtin_bit_cast(v4i_t, __builtin_amdgcn_raw_buffer_load_b128(
+              brs, lane * 16, (j * a.KT + 2 * k + t) * 1024, 0));
+    };
+    auto load_bs = [&](int c, int (&s)[T::FN]) {
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+        s[j] = __builtin_amdgcn_raw_buffer_load_b32(bss, lane * 4, (j * a.KC + c) * 256, 0);
+    };
+    v4f_t acc[T::FM][T::FN];
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) acc[i][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+    v4i_t b0[2][T::FN], b1[2][T::FN];
+    int bs0[T::FN], as[T::FM], bsn[T::FN];
+
+    __syncthreads();     // every wavefront has read the previous tile's last stage
+    issue_a(0);
+    issue_s(0);
+    if (!idle) {
+      load_b(0, b0);
+      load_bs(0, bsn);
+    }
+    // the MFMAs of step k: fragments of 16 rows from LDS, both k-tiles of the step
+    auto compute = [&](int k, const v4i_t (&b)[2][T::FN], auto odd_c) {
+      constexpr int O = decltype(odd_c)::value * 2;
+      const char* st = smem + (k & 1) * T::A_BYTES;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t == 1 && 2 * k + 1 >= a.KT) break;   // the last step of an odd number of k-tiles
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+          const int row = i * 16 + r16;
+          const v4i_t x = *reinterpret_cast<const v4i_t*>(
+              st + row * T::STEPB + (((t * 4 + kb) ^ swz_k(row)) << 4));
+          const v8i_t fa = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < T::FN; ++j) {
+            const v8i_t fb = {b[t][j][0], b[t][j][1], b[t][j][2], b[t][j][3], 0, 0, 0, 0};
+            // operands swapped: the block is transposed, a lane holds 4 columns of one row
+            if (t == 0) acc[i][j] = mfma_e2m1<O>(fb, fa, acc[i][j], bs0[j], as[i]);
+            else acc[i][j] = mfma_e2m1<O + 1>(fb, fa, acc[i][j], bs0[j], as[i]);
+          }
+        }
+      }
+    };
+    for (int k = 0; k < nsteps; k += 2) {
+      wait_vm<0>();
+      __syncthreads();
+      if (k + 1 < nsteps) issue_a(k + 1);
+      if (!idle) {
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) bs0[j] = bsn[j];
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+          as[i] = *reinterpret_cast<const int*>(s_scale + ((k / 2) & 1) * T::S_BYTES +
+                                                (i * 16 + r16) * 16 + kb * 4);
+        if (k + 1 < nsteps) load_b(k + 1, b1);
+        compute(k, b0, std::integral_constant<int, 0>());
+      }
+      if (k + 1 < nsteps) {
+        wait_vm<0>();
+        __syncthreads();
+        if (k + 2 < nsteps) {
+          issue_a(k + 2);
+          issue_s(k / 2 + 1);
+        }
+        if (!idle) {
+          if (k + 2 < nsteps) {
+            load_b(k + 2, b0);
+            load_bs(k / 2 + 1, bsn);
+          }
+          compute(k + 1, b1, std::integral_constant<int, 1>());
+        }
+      }
+    }
+    if (idle) continue;
+    const __amdgpu_buffer_rsrc_t crs = make_rsrc(a.c + int64_t(rowbase) * a.Hp,
+                                                 clamp_bytes(int64_t(rows_valid) * a.Hp * 4));
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            __builtin_bit_cast(v4i_t, acc[i][j]), crs,
+            (uint32_t(i * 16 + r16) * a.Hp + col0 + j * 16 + 4 * kb) * 4, 0, 0);
   }
 }
 
@@ -273,9 +462,16 @@ extern "C" int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* 
   if (cus <= 0) return MOONEP_EHIP;
   hipStream_t strm = as_stream(stream);
   MxArgs a{xq, xscales, src_index, wq, wscales, c, nullptr, nullptr, s.K, s.Hp,
-           int(k_tiles(s.H)), int(k_chunks(s.H)), int64_t(s.R) * s.S * s.K};
-  st = launch_tile_list(s, cu_seqlens, kMxRows, ws, strm, &a.tiles, &a.ntiles);
+           int(k_tiles(s.H)), int(k_chunks(s.H)), int64_t(s.R) * s.S * s.K,
+           int64_t(s.R) * s.S * (src_index ? 1 : s.K)};
+  const bool tiled = a.NK >= 16 * int64_t(s.E) && (!src_index || a.xrows * a.KT * 64 < int64_t(kOffNone));
+  st = launch_tile_list(s, cu_seqlens, tiled ? MxTile::BM : kMxRows, ws, strm, &a.tiles, &a.ntiles);
   if (st) return st;
+  if (tiled) {
+    if (src_index) mx_gemm_tiled_kernel<true><<<cus * 2, 256, 0, strm>>>(a);
+    else mx_gemm_tiled_kernel<false><<<cus * 2, 256, 0, strm>>>(a);
+    return launch_status();
+  }
   mx_gemm_kernel<<<cus * 8, 256, 0, strm>>>(a);
   return launch_status();
 }
