@@ -143,6 +143,7 @@ struct MxArgs {
   const int32_t* ntiles;
   int K, Hp, KT, KC;
   int64_t NK, xrows;
+  int32_t* qcnt;    // 8 per-XCD tile-queue counters, zero at launch
 };
 
 constexpr int kMxRows = 64;   // rows of a work entry
@@ -204,6 +205,8 @@ __device__ inline v4f_t mfma_e2m1(v8i_t a, v8i_t b, v4f_t c, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, BYTE, sa, BYTE, sb);
 }
 
+constexpr int kNonTemporal = 2;   // buffer cache policy: the output is not read back here
+
 // ---- tiled form: 128 x 256 output tiles, four wavefronts side by side in N (128 x 64 each),
 // 256 k per step.
 struct MxTile {
@@ -212,6 +215,7 @@ struct MxTile {
   static constexpr int A_BYTES = BM * STEPB;            // LDS per stage
   static constexpr int S_BYTES = BM * 16;               // LDS per chunk of scales
   static constexpr int FM = BM / 16, FN = 4;
+  static constexpr int kBlockE = 4;                     // entries per tile-order block
 };
 
 template <bool GATHER>
@@ -226,19 +230,31 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
   const int nent = *a.ntiles;
   const int64_t total = int64_t(nent) * NT;
   const int G = gridDim.x;
-  // the workgroups of one XCD take a contiguous run of tiles
-  const int slot = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
+  // The workgroups of one XCD take a contiguous run of tiles per round, first come first
+  // served (queue position q of XCD x is tile (q / per) * G + x * per + q % per), so that the
+  // tiles in flight on an XCD stay together and share operand lines in its L2 however far
+  // its workgroups drift apart: 2.57 -> 2.43 ms at 524288 slots, H = 4096, H' = 1536, 5.39
+  // -> 5.05 ms at H = 7168, H' = 2048 against the same order taken statically.
+  __shared__ int s_claim;
+  const int xcd = blockIdx.x % 8, per = G / 8;
+  auto claim = [&]() {
+    const int q = atomicAdd(a.qcnt + xcd, 1);
+    s_claim = (q / per) * G + xcd * per + q % per;
+  };
+  auto next = [&]() { return __builtin_amdgcn_readfirstlane(s_claim); };
+  if (threadIdx.x == 0) claim();
+  __syncthreads();
   const int nsteps = (a.KT + 1) / 2;
   const uint32_t qrow = uint32_t(a.KT) * 64, srow = uint32_t(a.KC) * 16;   // bytes per A row
   const int r16 = lane & 15, kb = lane >> 4;
 
-  for (int64_t tau = slot; tau < total; tau += G) {
-    // blocks of 8 entries x all N-tiles, entries fastest inside groups of 8 N-tiles
-    const int64_t eb = tau / (int64_t(8) * NT);
-    const int j8 = int(tau % (int64_t(8) * NT));
-    const int ge = int(min(int64_t(8), nent - eb * 8));
-    const int ent = int(eb) * 8 + j8 % ge;
-    const int n0 = j8 / ge * T::BN;
+  for (int64_t tau = next(); tau < total; tau = next()) {
+    // blocks of kBlockE entries x all N-tiles, entries fastest
+    const int64_t eb = tau / (int64_t(T::kBlockE) * NT);
+    const int j = int(tau % (int64_t(T::kBlockE) * NT));
+    const int ge = int(min(int64_t(T::kBlockE), nent - eb * T::kBlockE));
+    const int ent = int(eb) * T::kBlockE + j % ge;
+    const int n0 = j / ge * T::BN;
     const TileEntry e = a.tiles[ent];
     const int rowbase = __builtin_amdgcn_readfirstlane(e.rowbase + e.m0);
     const int wrow = __builtin_amdgcn_readfirstlane(e.wrow);
@@ -312,7 +328,8 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
     v4i_t b0[2][T::FN], b1[2][T::FN];
     int bs0[T::FN], as[T::FM], bsn[T::FN];
 
-    __syncthreads();     // every wavefront has read the previous tile's last stage
+    __syncthreads();     // every wavefront has read the previous tile's last stage and its claim
+    if (threadIdx.x == 0) claim();   // read after the k-loop's barriers
     issue_a(0);
     issue_s(0);
     if (!idle) {
@@ -381,7 +398,7 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
       for (int j = 0; j < T::FN; ++j)
         __builtin_amdgcn_raw_buffer_store_b128(
             __builtin_bit_cast(v4i_t, acc[i][j]), crs,
-            (uint32_t(i * 16 + r16) * a.Hp + col0 + j * 16 + 4 * kb) * 4, 0, 0);
+            (uint32_t(i * 16 + r16) * a.Hp + col0 + j * 16 + 4 * kb) * 4, 0, kNonTemporal);
   }
 }
 
@@ -463,8 +480,10 @@ extern "C" int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* 
   hipStream_t strm = as_stream(stream);
   MxArgs a{xq, xscales, src_index, wq, wscales, c, nullptr, nullptr, s.K, s.Hp,
            int(k_tiles(s.H)), int(k_chunks(s.H)), int64_t(s.R) * s.S * s.K,
-           int64_t(s.R) * s.S * (src_index ? 1 : s.K)};
-  const bool tiled = a.NK >= 16 * int64_t(s.E) && (!src_index || a.xrows * a.KT * 64 < int64_t(kOffNone));
+           int64_t(s.R) * s.S * (src_index ? 1 : s.K),
+           ws_ptr<int32_t>(ws, ws_layout(s).flags) + kFlagQueue};
+  const bool tiled = cus % 4 == 0 && a.NK >= 16 * int64_t(s.E) &&
+                     (!src_index || a.xrows * a.KT * 64 < int64_t(kOffNone));
   st = launch_tile_list(s, cu_seqlens, tiled ? MxTile::BM : kMxRows, ws, strm, &a.tiles, &a.ntiles);
   if (st) return st;
   if (tiled) {
