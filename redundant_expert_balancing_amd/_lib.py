@@ -318,56 +318,90 @@ def moonep_swiglu_backward(shape, h_saved, da, dh, stream=None):
 
 
 # ---- router, gates' gradient, 8-bit checkpoints, 4-bit experts
-def _q(t, nbytes, name, dtype):
-    """_p for the calls below, which also refuse a missing tensor and one that is not on
-    the current device (whose stream the call goes to)."""
+#
+# These calls serve single tokens too, so the checks of _p are made in one expression per
+# tensor and the stream is asked for as a handle (a whole call's marshalling: 4-6 us).
+_torch = None
+
+
+def _device() -> int:
+    """Index of the current device."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
+
+
+def _q(t, nbytes, name, dtype, dev, optional=False):
+    """Address of a contiguous tensor of `dtype` (None: any) with at least `nbytes` bytes on
+    device `dev` (the current one, whose stream the call goes to); raises otherwise."""
     if t is None:
+        if optional:
+            return None
         raise ValueError(f"{name}: a tensor is required")
-    p = _p(t, nbytes, name, dtype)
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return p
+    if (t.get_device() == dev and (dtype is None or t.dtype is dtype) and t.is_contiguous()
+            and t.nbytes >= nbytes):
+        return t.data_ptr()
+    _p(t, nbytes, name, dtype)
+    raise ValueError(f"{name}: on {t.device}, the current device is cuda:{dev}")
 
 
-def _u8():
-    import torch
-    return torch.uint8
+def _h(stream, dev):
+    """hipStream_t of `stream` (None: torch's current one on `dev`)."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+    return getattr(stream, "cuda_stream", stream)
 
 
 def _logit(router: Router):
-    import torch
-    return (torch.bfloat16, 2) if router.dtype == BF16 else (torch.float32, 4)
+    return (_torch.bfloat16, 2) if router.dtype == BF16 else (_torch.float32, 4)
+
+
+def _types(shape: Shape):
+    """(activation type, its bytes) of the layer."""
+    return (_torch.bfloat16, 2) if shape.dtype == BF16 else (_torch.float32, 4)
 
 
 def moonep_route(shape, router, logits, bias, topk_idx, gates, stream=None):
-    N, NK, _, _ = _dims(shape)
+    d = _device()
+    N, E = shape.R * shape.S, shape.E
+    b = 4 * N * shape.K
     dt, lb = _logit(router)
-    _check("moonep_route", lib().moonep_route(
-        ctypes.byref(shape), ctypes.byref(router), _q(logits, N * shape.E * lb, "logits", dt),
-        None if bias is None else _q(bias, 4 * shape.E, "bias", _f32()),
-        _q(topk_idx, 4 * NK, "topk_idx", _i32()), _q(gates, 4 * NK, "gates", _f32()), _s(stream)))
+    f32 = _torch.float32
+    st = lib().moonep_route(
+        shape, router, _q(logits, N * E * lb, "logits", dt, d), _q(bias, 4 * E, "bias", f32, d, True),
+        _q(topk_idx, b, "topk_idx", _torch.int32, d), _q(gates, b, "gates", f32, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_route", st)
 
 
 def moonep_route_backward(shape, router, logits, bias, topk_idx, gates, dgates, dlogits,
                           stream=None):
-    N, NK, _, _ = _dims(shape)
+    d = _device()
+    N, E = shape.R * shape.S, shape.E
+    b = 4 * N * shape.K
     dt, lb = _logit(router)
-    _check("moonep_route_backward", lib().moonep_route_backward(
-        ctypes.byref(shape), ctypes.byref(router), _q(logits, N * shape.E * lb, "logits", dt),
-        None if bias is None else _q(bias, 4 * shape.E, "bias", _f32()),
-        _q(topk_idx, 4 * NK, "topk_idx", _i32()), _q(gates, 4 * NK, "gates", _f32()),
-        _q(dgates, 4 * NK, "dgates", _f32()), _q(dlogits, N * shape.E * lb, "dlogits", dt),
-        _s(stream)))
+    f32 = _torch.float32
+    st = lib().moonep_route_backward(
+        shape, router, _q(logits, N * E * lb, "logits", dt, d), _q(bias, 4 * E, "bias", f32, d, True),
+        _q(topk_idx, b, "topk_idx", _torch.int32, d), _q(gates, b, "gates", f32, d),
+        _q(dgates, b, "dgates", f32, d), _q(dlogits, N * E * lb, "dlogits", dt, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_route_backward", st)
 
 
 def moonep_gate_grad(shape, width, src, slot_map, dy, dgates, stream=None):
-    N, NK, _, eb = _dims(shape)
-    w = int(width)
-    _check("moonep_gate_grad", lib().moonep_gate_grad(
-        ctypes.byref(shape), w, _q(src, 4 * NK * w, "src", _f32()),
-        _q(slot_map, 4 * NK, "slot_map", _i32()), _q(dy, N * w * eb, "dy", _act(shape)),
-        _q(dgates, 4 * NK, "dgates", _f32()), _s(stream)))
+    d = _device()
+    N, w = shape.R * shape.S, int(width)
+    NK = N * shape.K
+    act, eb = _types(shape)
+    f32 = _torch.float32
+    st = lib().moonep_gate_grad(
+        shape, w, _q(src, 4 * NK * w, "src", f32, d), _q(slot_map, 4 * NK, "slot_map", _torch.int32, d),
+        _q(dy, N * w * eb, "dy", act, d), _q(dgates, 4 * NK, "dgates", f32, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_gate_grad", st)
 
 
 def checkpoint_scale_bytes(width: int) -> int:
@@ -376,60 +410,82 @@ def checkpoint_scale_bytes(width: int) -> int:
 
 
 def moonep_checkpoint_quantize(shape, width, src, q, scales, stream=None):
-    N, _, _, eb = _dims(shape)
-    w = int(width)
-    _check("moonep_checkpoint_quantize", lib().moonep_checkpoint_quantize(
-        ctypes.byref(shape), w, _q(src, N * w * eb, "src", _act(shape)), _q(q, N * w, "q", _u8()),
-        _q(scales, N * checkpoint_scale_bytes(w), "scales", _u8()), _s(stream)))
+    d = _device()
+    N, w = shape.R * shape.S, int(width)
+    act, eb = _types(shape)
+    u8 = _torch.uint8
+    st = lib().moonep_checkpoint_quantize(
+        shape, w, _q(src, N * w * eb, "src", act, d), _q(q, N * w, "q", u8, d),
+        _q(scales, N * checkpoint_scale_bytes(w), "scales", u8, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_checkpoint_quantize", st)
 
 
 def moonep_checkpoint_dispatch(shape, width, q, scales, slot_map, dst, stream=None):
-    N, NK, _, eb = _dims(shape)
-    w = int(width)
-    _check("moonep_checkpoint_dispatch", lib().moonep_checkpoint_dispatch(
-        ctypes.byref(shape), w, _q(q, N * w, "q", _u8()),
-        _q(scales, N * checkpoint_scale_bytes(w), "scales", _u8()),
-        _q(slot_map, 4 * NK, "slot_map", _i32()), _q(dst, NK * w * eb, "dst", _act(shape)),
-        _s(stream)))
+    d = _device()
+    N, w = shape.R * shape.S, int(width)
+    NK = N * shape.K
+    act, eb = _types(shape)
+    u8 = _torch.uint8
+    st = lib().moonep_checkpoint_dispatch(
+        shape, w, _q(q, N * w, "q", u8, d), _q(scales, N * checkpoint_scale_bytes(w), "scales", u8, d),
+        _q(slot_map, 4 * NK, "slot_map", _torch.int32, d), _q(dst, NK * w * eb, "dst", act, d),
+        _h(stream, d))
+    if st:
+        raise MoonepError("moonep_checkpoint_dispatch", st)
 
 
-def _checkpoint_h(shape, q, scales):
-    _, NK, _, _ = _dims(shape)
-    w = 2 * shape.Hp
-    return (_q(q, NK * w, "q", _u8()),
-            _q(scales, NK * checkpoint_scale_bytes(w), "scales", _u8()))
+def _checkpoint_h(shape, q, scales, d):
+    NK, w = shape.R * shape.S * shape.K, 2 * shape.Hp
+    return (_q(q, NK * w, "q", _torch.uint8, d),
+            _q(scales, NK * checkpoint_scale_bytes(w), "scales", _torch.uint8, d))
 
 
 def moonep_swiglu_checkpoint(shape, h, act, q, scales, stream=None):
-    _, NK, _, eb = _dims(shape)
-    Hp = shape.Hp
-    _check("moonep_swiglu_checkpoint", lib().moonep_swiglu_checkpoint(
-        ctypes.byref(shape), _q(h, 4 * NK * 2 * Hp, "h", _f32()),
-        _q(act, NK * Hp * eb, "act", _act(shape)), *_checkpoint_h(shape, q, scales), _s(stream)))
+    d = _device()
+    n = shape.R * shape.S * shape.K * shape.Hp
+    at, eb = _types(shape)
+    st = lib().moonep_swiglu_checkpoint(
+        shape, _q(h, 8 * n, "h", _torch.float32, d), _q(act, n * eb, "act", at, d),
+        *_checkpoint_h(shape, q, scales, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_swiglu_checkpoint", st)
+
+
+def _ws(shape, ws, d):
+    """(address, bytes) of a workspace."""
+    return _q(ws, lib().moonep_workspace_bytes(shape), "ws", None, d), ws.nbytes
 
 
 def moonep_grouped_gemm_swiglu_checkpoint(shape, xp, w1_all, cu_seqlens, act, q, scales, ws,
                                           stream=None):
-    _, NK, _, eb = _dims(shape)
-    H, Hp, a = shape.H, shape.Hp, _act(shape)
-    _check("moonep_grouped_gemm_swiglu_checkpoint", lib().moonep_grouped_gemm_swiglu_checkpoint(
-        ctypes.byref(shape), _q(xp, NK * H * eb, "xp", a),
-        _q(w1_all, (shape.E + shape.R * shape.B) * H * 2 * Hp * eb, "w1_all", a),
-        _q(cu_seqlens, 4 * shape.R * (shape.E + shape.B + 1), "cu_seqlens", _i32()),
-        _q(act, NK * Hp * eb, "act", a), *_checkpoint_h(shape, q, scales),
-        _q(ws, moonep_workspace_bytes(shape), "ws", None), _nbytes(ws), _s(stream)))
+    d = _device()
+    NK, H, Hp = shape.R * shape.S * shape.K, shape.H, shape.Hp
+    at, eb = _types(shape)
+    st = lib().moonep_grouped_gemm_swiglu_checkpoint(
+        shape, _q(xp, NK * H * eb, "xp", at, d),
+        _q(w1_all, (shape.E + shape.R * shape.B) * H * 2 * Hp * eb, "w1_all", at, d),
+        _q(cu_seqlens, 4 * shape.R * (shape.E + shape.B + 1), "cu_seqlens", _torch.int32, d),
+        _q(act, NK * Hp * eb, "act", at, d), *_checkpoint_h(shape, q, scales, d),
+        *_ws(shape, ws, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_grouped_gemm_swiglu_checkpoint", st)
 
 
 def moonep_swiglu_backward_checkpoint(shape, q, scales, da, src_index, gates, act, dh, dgates,
                                       stream=None):
-    _, NK, _, eb = _dims(shape)
-    Hp, a = shape.Hp, _act(shape)
-    opt = [None if t is None else _q(t, 4 * NK, name, dt) for t, name, dt in
-           ((src_index, "src_index", _i32()), (gates, "gates", _f32()), (dgates, "dgates", _f32()))]
-    _check("moonep_swiglu_backward_checkpoint", lib().moonep_swiglu_backward_checkpoint(
-        ctypes.byref(shape), *_checkpoint_h(shape, q, scales), _q(da, 4 * NK * Hp, "da", _f32()),
-        opt[0], opt[1], _q(act, NK * Hp * eb, "act", a), _q(dh, NK * 2 * Hp * eb, "dh", a), opt[2],
-        _s(stream)))
+    d = _device()
+    NK, Hp = shape.R * shape.S * shape.K, shape.Hp
+    at, eb = _types(shape)
+    f32 = _torch.float32
+    st = lib().moonep_swiglu_backward_checkpoint(
+        shape, *_checkpoint_h(shape, q, scales, d), _q(da, 4 * NK * Hp, "da", f32, d),
+        _q(src_index, 4 * NK, "src_index", _torch.int32, d, True),
+        _q(gates, 4 * NK, "gates", f32, d, True), _q(act, NK * Hp * eb, "act", at, d),
+        _q(dh, NK * 2 * Hp * eb, "dh", at, d), _q(dgates, 4 * NK, "dgates", f32, d, True),
+        _h(stream, d))
+    if st:
+        raise MoonepError("moonep_swiglu_backward_checkpoint", st)
 
 
 def mx_row_bytes(width: int):
@@ -444,46 +500,60 @@ def mx_weight_bytes(H: int, Hp: int):
 
 
 def moonep_mx_quantize(shape, rows, width, src, q, scales, stream=None):
-    eb = _dims(shape)[3]
+    d = _device()
     rows, w = int(rows), int(width)
+    act, eb = _types(shape)
     qb, sb = mx_row_bytes(w)
-    _check("moonep_mx_quantize", lib().moonep_mx_quantize(
-        ctypes.byref(shape), rows, w, _q(src, rows * w * eb, "src", _act(shape)),
-        _q(q, rows * qb, "q", _u8()), _q(scales, rows * sb, "scales", _u8()), _s(stream)))
+    st = lib().moonep_mx_quantize(
+        shape, rows, w, _q(src, rows * w * eb, "src", act, d), _q(q, rows * qb, "q", _torch.uint8, d),
+        _q(scales, rows * sb, "scales", _torch.uint8, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_mx_quantize", st)
 
 
 def moonep_mx_quantize_weight(shape, w, wq, wscales, stream=None):
-    E, eb = shape.E, _dims(shape)[3]
+    d = _device()
+    E = shape.E
+    act, eb = _types(shape)
     qb, sb = mx_weight_bytes(shape.H, shape.Hp)
-    _check("moonep_mx_quantize_weight", lib().moonep_mx_quantize_weight(
-        ctypes.byref(shape), _q(w, E * shape.H * shape.Hp * eb, "w", _act(shape)),
-        _q(wq, E * qb, "wq", _u8()), _q(wscales, E * sb, "wscales", _u8()), _s(stream)))
+    st = lib().moonep_mx_quantize_weight(
+        shape, _q(w, E * shape.H * shape.Hp * eb, "w", act, d), _q(wq, E * qb, "wq", _torch.uint8, d),
+        _q(wscales, E * sb, "wscales", _torch.uint8, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_mx_quantize_weight", st)
 
 
-def _mx_weights(shape, wq, wscales):
+def _mx_weights(shape, wq, wscales, d):
     rows = shape.E + shape.R * shape.B
     qb, sb = mx_weight_bytes(shape.H, shape.Hp)
-    return _q(wq, rows * qb, "wq", _u8()), _q(wscales, rows * sb, "wscales", _u8())
+    return (_q(wq, rows * qb, "wq", _torch.uint8, d),
+            _q(wscales, rows * sb, "wscales", _torch.uint8, d))
 
 
 def moonep_mx_prefetch_weight(shape, replica_expert, wq, wscales, stream=None):
-    _check("moonep_mx_prefetch_weight", lib().moonep_mx_prefetch_weight(
-        ctypes.byref(shape), _q(replica_expert, 4 * shape.R * shape.B, "replica_expert", _i32()),
-        *_mx_weights(shape, wq, wscales), _s(stream)))
+    d = _device()
+    st = lib().moonep_mx_prefetch_weight(
+        shape, _q(replica_expert, 4 * shape.R * shape.B, "replica_expert", _torch.int32, d),
+        *_mx_weights(shape, wq, wscales, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_mx_prefetch_weight", st)
 
 
 def moonep_mx_grouped_gemm(shape, xq, xscales, src_index, wq, wscales, cu_seqlens, c, ws,
                            stream=None):
-    N, NK, _, _ = _dims(shape)
+    d = _device()
+    N = shape.R * shape.S
+    NK = N * shape.K
     rows = NK if src_index is None else N
     qb, sb = mx_row_bytes(shape.H)
-    _check("moonep_mx_grouped_gemm", lib().moonep_mx_grouped_gemm(
-        ctypes.byref(shape), _q(xq, rows * qb, "xq", _u8()), _q(xscales, rows * sb, "xscales", _u8()),
-        None if src_index is None else _q(src_index, 4 * NK, "src_index", _i32()),
-        *_mx_weights(shape, wq, wscales),
-        _q(cu_seqlens, 4 * shape.R * (shape.E + shape.B + 1), "cu_seqlens", _i32()),
-        _q(c, 4 * NK * shape.Hp, "c", _f32()), _q(ws, moonep_workspace_bytes(shape), "ws", None),
-        _nbytes(ws), _s(stream)))
+    i32, u8 = _torch.int32, _torch.uint8
+    st = lib().moonep_mx_grouped_gemm(
+        shape, _q(xq, rows * qb, "xq", u8, d), _q(xscales, rows * sb, "xscales", u8, d),
+        _q(src_index, 4 * NK, "src_index", i32, d, True), *_mx_weights(shape, wq, wscales, d),
+        _q(cu_seqlens, 4 * shape.R * (shape.E + shape.B + 1), "cu_seqlens", i32, d),
+        _q(c, 4 * NK * shape.Hp, "c", _torch.float32, d), *_ws(shape, ws, d), _h(stream, d))
+    if st:
+        raise MoonepError("moonep_mx_grouped_gemm", st)
 
 
 def moonep_vm_granularity() -> int:
