@@ -12,7 +12,6 @@ namespace moonep {
 
 constexpr int kRouteWaves = 4;        // wavefronts (tokens) per workgroup
 constexpr int kMaxE = 1024;           // validate() bounds E
-constexpr int kMaxPer = kMaxE / 64;   // experts per lane
 constexpr float kNegInf = -__builtin_inff();
 constexpr double kNegInfD = -__builtin_inf();
 
@@ -45,6 +44,13 @@ __device__ inline float wave_sum_f(float v) {
   return v;
 }
 
+// Orders this wavefront's LDS accesses for the compiler; its lanes run in step.
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 struct RouteArgs {
   const void* logits;
   const float* bias;
@@ -53,6 +59,8 @@ struct RouteArgs {
   int N, E, K, groups, top_groups, group_top;
   bool softmax, renorm;
   float scale;
+  bool bf16;
+  int epl;   // packed form: experts per lane, a multiple of 4
 };
 
 // Gates of one token: lane k < K holds the logit l of its k-th choice and whether the
@@ -82,125 +90,495 @@ __device__ inline float gate_of(const RouteArgs& a, int lane, float l, bool live
   return bad ? __builtin_nanf("") : w;
 }
 
-// One wavefront per token; lane i holds experts i, i + 64, ...
-template <bool BF16>
+// One token by one wavefront, every key in float64. `val` is E doubles of LDS of this
+// wavefront's own; loops are kept rolled, so that a kernel that seldom comes here does not
+// pay for it in registers.
+__device__ void route_token(const RouteArgs& a, int64_t g, double* val) {
+  const int lane = threadIdx.x & 63;
+  const int per_group = a.E / a.groups;
+  auto logit = [&](int e) {
+    const float l = a.bf16 ? load_logit<true>(a.logits, g * a.E + e)
+                           : load_logit<false>(a.logits, g * a.E + e);
+    return a.bias ? effective_logit(l, a.bias[e]) : l;
+  };
+  float m = kNegInf;
+  bool bad = false;
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) {
+    const float l = logit(e);
+    bad |= l != l || (a.softmax && l == -kNegInf);
+    m = fmaxf(m, l);
+  }
+  bad = __any(bad);
+  m = wave_max(m);
+  float sum = 0.f;
+  double sumd = 0.0;
+  if (a.softmax) {
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      const float l = logit(e);
+      if (l == kNegInf) continue;
+      sum += expf(l - m);
+      sumd += exp(double(l) - double(m));
+    }
+    sum = wave_sum_f(sum);
+    sumd = wave_sum_d(sumd);
+  }
+  // float64 score + bias of an unmasked expert, -inf of any other or where it is NaN
+  auto value = [&](int e, float l) {
+    if (!(l > kNegInf)) return kNegInfD;
+    const double ld = double(l);
+    const double s = a.softmax ? exp(ld - double(m)) / sumd : 1.0 / (1.0 + exp(-ld));
+    const double v = a.bias ? s + double(a.bias[e]) : s;
+    return v == v ? v : kNegInfD;
+  };
+  // the ranking's key: without a bias the logit itself, whose order the scores keep
+  auto rank_key = [&](int e, float l) {
+    if (a.bias) return value(e, l);
+    return l > kNegInf ? double(l) : kNegInfD;
+  };
+  uint64_t kept = ~uint64_t(0);   // groups whose experts may be chosen
+  if (a.groups > 1) {
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64)
+      val[e] = a.group_top == 1 ? rank_key(e, logit(e)) : value(e, logit(e));
+    wave_sync();
+    // lane j scores group j; the rank of a group is the number of groups before it
+    double best = kNegInfD, second = kNegInfD;
+    if (lane < a.groups)
+#pragma unroll 1
+      for (int i = 0; i < per_group; ++i) {
+        const double v = val[lane * per_group + i];
+        if (v > best) { second = best; best = v; }
+        else if (v > second) second = v;
+      }
+    const double score = a.group_top == 2 && second != kNegInfD ? best + second : best;
+    int rank = 0;
+#pragma unroll 1
+    for (int j = 0; j < a.groups; ++j) {
+      const double o = __shfl(score, j, 64);
+      rank += (o > score || (o == score && j < lane)) ? 1 : 0;
+    }
+    kept = __ballot(lane < a.groups && rank < a.top_groups);
+    wave_sync();
+  }
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64)
+    val[e] = (kept >> (e / per_group)) & 1 ? rank_key(e, logit(e)) : kNegInfD;
+  // K rounds of the best expert left; a taken one's key becomes NaN. Lanes read only what
+  // they wrote.
+  int my_id = 0;
+  bool my_live = false;
+#pragma unroll 1
+  for (int k = 0; k < a.K; ++k) {
+    double best = kNegInfD;
+    int at = kMaxE;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      const double v = val[e];
+      if (v > best || (v == best && at == kMaxE)) {
+        best = v;
+        at = e;
+      }
+    }
+#pragma unroll 1
+    for (int d = 32; d > 0; d >>= 1) {
+      const double ob = __shfl_xor(best, d, 64);
+      const int oa = __shfl_xor(at, d, 64);
+      if (ob > best || (ob == best && oa < at)) {
+        best = ob;
+        at = oa;
+      }
+    }
+    if ((at & 63) == lane) val[at] = __builtin_nan("");
+    if (lane == k) {
+      my_id = at;
+      my_live = best != kNegInfD;
+    }
+  }
+  const float lk = lane < a.K ? logit(my_id) : kNegInf;
+  const float gate = gate_of(a, lane, lk, my_live, m, sum, bad);
+  if (lane < a.K) {
+    a.ids[g * a.K + lane] = my_id;
+    a.gates[g * a.K + lane] = gate;
+  }
+  wave_sync();
+}
+
 __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
   __shared__ double s_val[kRouteWaves][kMaxE];
-  __shared__ float s_logit[kRouteWaves][kMaxE];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  double* val = s_val[w];
-  float* row = s_logit[w];
-  const int per_group = a.E / a.groups;
+  const int w = threadIdx.x >> 6;
   for (int64_t g = int64_t(blockIdx.x) * kRouteWaves + w; g < a.N;
-       g += int64_t(gridDim.x) * kRouteWaves) {
-    // effective logits, their maximum and the softmax sum
-    float l[kMaxPer];
-    float m = kNegInf;
-    bool bad = false;
+       g += int64_t(gridDim.x) * kRouteWaves)
+    route_token(a, g, s_val[w]);
+}
+
+// ---- packed form: 16 lanes per token, four tokens per wavefront, K <= 8, E <= 512.
+//
+// Ranking by float64 keys costs an exponential and a 64-bit comparison network per expert,
+// and almost never decides anything: two scores have to agree to about 2^-21. So each
+// expert gets one 32-bit word, its float32 key as a 22-bit fixed-point number between the
+// token's lowest and highest key, above its complemented id: unsigned order is (key
+// descending, id ascending), a word is its own payload, and one comparator is a max and a
+// min. Each lane sorts its experts in columns of 8, merges them into its best 8, and four
+// butterfly merges give the token's best 8 to all its lanes. The result stands if no two
+// neighbours of the ranking that could change the choice are closer than the keys' error,
+// unless they are equal in logit and bias (then the id decides, as it should). Tokens where
+// one is (0.3% of normal ones, more with many ties of unequal experts), or that hold a NaN
+// or +inf, are done again by route_token.
+constexpr int kPackK = 8;
+constexpr int kTokens = 4;           // per wavefront
+constexpr uint32_t kIdMask = 1023;
+constexpr float kQMax = 4194300.f;   // fixed-point range: keys 1 .. 2^22 - 3, masked 0
+
+template <int CTRL>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, false));
+}
+// lane permutations whose pairs span 2, 4, 8 and 16 lanes
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+template <int CTRL>
+__device__ inline float dppf(float v) { return __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
+
+__device__ inline float row_max(float v) {
+  v = fmaxf(v, dppf<kXor1>(v));
+  v = fmaxf(v, dppf<kXor2>(v));
+  v = fmaxf(v, dppf<kHalfMirror>(v));
+  return fmaxf(v, dppf<kMirror>(v));
+}
+__device__ inline float row_min(float v) { return -row_max(-v); }
+__device__ inline float row_sum(float v) {
+  v += dppf<kXor1>(v);
+  v += dppf<kXor2>(v);
+  v += dppf<kHalfMirror>(v);
+  return v + dppf<kMirror>(v);
+}
+__device__ inline uint32_t row_or(uint32_t v) {
+  v |= dpp<kXor1>(v);
+  v |= dpp<kXor2>(v);
+  v |= dpp<kHalfMirror>(v);
+  return v | dpp<kMirror>(v);
+}
+
+__device__ inline void order(uint32_t& hi, uint32_t& lo) {
+  const uint32_t a = max(hi, lo), b = min(hi, lo);
+  hi = a;
+  lo = b;
+}
+// Descending sort of 8 (Batcher's odd-even merge sort, 19 comparators).
+__device__ inline void sort8(uint32_t* v) {
+  order(v[0], v[1]); order(v[2], v[3]); order(v[4], v[5]); order(v[6], v[7]);
+  order(v[0], v[2]); order(v[1], v[3]); order(v[4], v[6]); order(v[5], v[7]);
+  order(v[1], v[2]); order(v[5], v[6]);
+  order(v[0], v[4]); order(v[1], v[5]); order(v[2], v[6]); order(v[3], v[7]);
+  order(v[2], v[4]); order(v[3], v[5]);
+  order(v[1], v[2]); order(v[3], v[4]); order(v[5], v[6]);
+}
+// Descending sort of a bitonic sequence of 8.
+__device__ inline void bitonic8(uint32_t* v) {
 #pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) {
-      const int e = i * 64 + lane;
-      l[i] = kNegInf;
-      if (e < a.E) {
-        l[i] = load_logit<BF16>(a.logits, g * a.E + e);
-        if (a.bias) l[i] = effective_logit(l[i], a.bias[e]);
-        bad |= l[i] != l[i] || (a.softmax && l[i] == -kNegInf);
-        m = fmaxf(m, l[i]);
-        row[e] = l[i];
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) order(v[i], v[i + d]);
+}
+// v: the best 8 of two descending lists of 8, its own and its partner lane's; lost: the best
+// of what any merge dropped on the way.
+template <int CTRL>
+__device__ inline void merge_lanes(uint32_t* v, uint32_t& lost) {
+  uint32_t o[8];
+  lost = max(lost, dpp<CTRL>(lost));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t p = dpp<CTRL>(v[7 - i]);
+    o[i] = max(v[i], p);
+    lost = max(lost, min(v[i], p));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = o[i];
+  bitonic8(v);
+}
+
+// 1 / (1 + e^-x), within 2^-22
+__device__ inline float fast_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+
+// EPL: experts per lane that the registers hold (a.epl of them used, a multiple of 4).
+template <int EPL, bool SOFTMAX, bool BIAS>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArgs a) {
+  __shared__ __align__(16) float s_row[kRouteWaves][kTokens * 16 * EPL];
+  __shared__ __align__(16) float s_bias[BIAS ? 16 * EPL : 4];
+  __shared__ __align__(16) uint32_t s_list[kRouteWaves][kTokens][kPackK];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, t = lane >> 4, i16 = lane & 15;
+  const int E = a.E, epl = a.epl, e0 = i16 * epl;
+  float* rows = s_row[w];
+  if (BIAS) {
+    for (int e = threadIdx.x; e < 16 * EPL; e += kRouteWaves * 64)
+      s_bias[e] = e < E ? a.bias[e] : 0.f;
+    __syncthreads();
+  }
+  const bool vec = E % 4 == 0;
+  const int64_t g0 = (int64_t(blockIdx.x) * kRouteWaves + w) * kTokens;
+  if (g0 < a.N) {   // uniform per wavefront; no workgroup barrier inside
+    const int ntok = int(min(int64_t(kTokens), a.N - g0));
+    // the tokens' logits lie together: copy them to LDS as float32
+    const int count = ntok * E;
+    if (vec && a.bf16) {
+      const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + g0 * E);
+      for (int i = lane; i < count / 4; i += 64) {
+        const uint2 u = src[i];
+        reinterpret_cast<float4*>(rows)[i] =
+            make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                        __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
       }
+    } else if (vec) {
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + g0 * E);
+      for (int i = lane; i < count / 4; i += 64) reinterpret_cast<float4*>(rows)[i] = src[i];
+    } else {
+      for (int i = lane; i < count; i += 64)
+        rows[i] = a.bf16 ? load_logit<true>(a.logits, g0 * E + i) : load_logit<false>(a.logits, g0 * E + i);
     }
-    bad = __any(bad);
-    m = wave_max(m);
-    float sum = 0.f;
-    double sumd = 0.0;
-    if (a.softmax) {
-#pragma unroll
-      for (int i = 0; i < kMaxPer; ++i)
-        if (i * 64 + lane < a.E && l[i] != kNegInf) {
-          sum += expf(l[i] - m);
-          sumd += exp(double(l[i]) - double(m));
+    wave_sync();
+    const bool on = t < ntok;
+    const float* row = rows + t * E;
+    // 4 effective logits of this lane; experts that are not there count as masked
+    auto logits4 = [&](int c, float* l) {
+      float4 v = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+      const int e = e0 + c;
+      if (c < epl && e < E) {
+        if (vec) {
+          v = *reinterpret_cast<const float4*>(row + e);
+        } else {
+          v.x = row[e];
+          if (e + 1 < E) v.y = row[e + 1];
+          if (e + 2 < E) v.z = row[e + 2];
+          if (e + 3 < E) v.w = row[e + 3];
         }
-      sum = wave_sum_f(sum);
-      sumd = wave_sum_d(sumd);
-    }
-    // keys: the logit itself without a bias (scores keep its order), else score + bias
-    double key[kMaxPer];
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) {
-      const int e = i * 64 + lane;
-      key[i] = kNegInfD;
-      double sc = kNegInfD;
-      if (e < a.E && l[i] == l[i] && l[i] != kNegInf) {
-        const double ld = double(l[i]);
-        const double s = a.softmax ? exp(ld - double(m)) / sumd : 1.0 / (1.0 + exp(-ld));
-        sc = a.bias ? s + double(a.bias[e]) : s;
-        key[i] = a.bias ? sc : ld;
-        if (key[i] != key[i]) key[i] = kNegInfD;
-        if (sc != sc) sc = kNegInfD;
       }
-      if (e < a.E) val[e] = a.group_top == 1 ? key[i] : sc;
+      l[0] = v.x; l[1] = v.y; l[2] = v.z; l[3] = v.w;
+      if (BIAS) {
+        const float4 b = *reinterpret_cast<const float4*>(s_bias + min(e, 16 * EPL - 4));
+        l[0] = effective_logit(l[0], b.x); l[1] = effective_logit(l[1], b.y);
+        l[2] = effective_logit(l[2], b.z); l[3] = effective_logit(l[3], b.w);
+      }
+    };
+    float top = kNegInf, inv = 0.f, sum = 0.f;   // the largest logit, the softmax sum, 1 / sum
+    // keys of 4 effective logits: -inf of a masked one
+    auto keys4 = [&](int c, float* l) {
+      if (!BIAS) return;
+      const float4 b4 = *reinterpret_cast<const float4*>(s_bias + min(e0 + c, 16 * EPL - 4));
+      const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float s = SOFTMAX ? __builtin_amdgcn_exp2f((l[i] - top) * 1.44269504f) * inv
+                                : fast_sigmoid(l[i]);
+        l[i] = l[i] == kNegInf ? kNegInf : s + b[i];
+      }
+    };
+    float key[EPL];
+    bool unsure = false;
+    float hi = kNegInf, lo = -kNegInf;
+#pragma unroll
+    for (int c = 0; c < EPL; c += 4) {
+      logits4(c, key + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        unsure |= key[c + i] != key[c + i];
+        hi = fmaxf(hi, key[c + i]);
+      }
     }
-    uint64_t kept = ~uint64_t(0);   // groups whose experts may be chosen
+    unsure |= hi == -kNegInf;
+    if (SOFTMAX) {
+      top = row_max(hi);
+      top = top == kNegInf ? 0.f : top;   // nothing left: every e^(l - top) is 0
+      if (BIAS || !a.renorm) {
+#pragma unroll
+        for (int c = 0; c < EPL; ++c) sum += __builtin_amdgcn_exp2f((key[c] - top) * 1.44269504f);
+        sum = row_sum(sum);
+        inv = __builtin_amdgcn_rcpf(sum);
+      }
+    }
+    if (BIAS) {
+      hi = kNegInf;
+#pragma unroll
+      for (int c = 0; c < EPL; c += 4) {
+        keys4(c, key + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          unsure |= key[c + i] != key[c + i];
+          hi = fmaxf(hi, key[c + i]);
+        }
+      }
+      unsure |= hi == -kNegInf;
+    }
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) lo = fminf(lo, key[c] == kNegInf ? lo : key[c]);
+    hi = row_max(hi);
+    lo = row_min(lo);
+    // float32 keys are off by at most `err`: sigmoid 2^-22, softmax 2^-18 of the largest
+    // score (at most 36 roundings of the sum, 6 of the rest, in units of 2^-24), the sum
+    // with the bias 2^-23 of itself; logits are exact
+    const float err = !BIAS ? 0.f
+                            : (SOFTMAX ? 3.8146973e-6f * inv : 2.3841858e-7f) +
+                                  1.1920929e-7f * fmaxf(fabsf(hi), fabsf(lo));
+    // a long tail of low keys would take the range's resolution: keys more than 64 below the
+    // highest get the number of masked ones
+    const bool tail = lo < hi - 64.f;
+    if (tail) lo = hi - 64.f;
+    const float f = hi > lo ? kQMax * 0.9999995f * __builtin_amdgcn_rcpf(hi - lo) : 0.f;
+    const uint32_t near = BIAS ? uint32_t(fminf(2.f * err * f, 4.0e6f)) + 2 : 0;
+
+    // groups: the token's groups are runs of its lanes (checked by the host)
+    uint32_t mask = ~0u;      // keeps a word, or the id alone where the group does not stay
     if (a.groups > 1) {
-      // lane j scores group j; rank of a group = groups that precede it
-      __builtin_amdgcn_wave_barrier();
-      double best = kNegInfD, second = kNegInfD;
-      if (lane < a.groups)
-        for (int i = 0; i < per_group; ++i) {
-          const double v = val[lane * per_group + i];
-          if (v > best) { second = best; best = v; }
-          else if (v > second) second = v;
+      float m1 = kNegInf, m2 = kNegInf;
+#pragma unroll
+      for (int c = 0; c < EPL; ++c) {
+        m2 = __builtin_amdgcn_fmed3f(m1, m2, key[c]);
+        m1 = fmaxf(m1, key[c]);
+      }
+      const int run = 16 / a.groups;
+      auto join = [&](float o1, float o2) {
+        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+        m1 = fmaxf(m1, o1);
+      };
+      if (run >= 2) join(dppf<kXor1>(m1), dppf<kXor1>(m2));
+      if (run >= 4) join(dppf<kXor2>(m1), dppf<kXor2>(m2));
+      if (run >= 8) join(dppf<kHalfMirror>(m1), dppf<kHalfMirror>(m2));
+      float score = m1, tol = 2.f * err;
+      if (a.group_top == 2) {
+        if (!BIAS) {   // the two best logits' scores (softmax: all by the same factor)
+          if (SOFTMAX) {
+            m1 = __builtin_amdgcn_exp2f((m1 - top) * 1.44269504f);
+            m2 = __builtin_amdgcn_exp2f((m2 - top) * 1.44269504f);
+          } else {
+            m1 = fast_sigmoid(m1);
+            m2 = fast_sigmoid(m2);
+          }
+          // a masked logit's score is 0, which is what it adds; a group with none is last
+          score = score == kNegInf ? kNegInf : m1 + m2;
+          tol = 3.8146973e-6f;
+        } else {
+          score = m2 == kNegInf ? m1 : m1 + m2;
+          tol = 4.f * err + 2.3841858e-7f * (score == kNegInf ? 0.f : fabsf(score));
         }
-      const double score = a.group_top == 2 && second != kNegInfD ? best + second : best;
+      }
+      const int mine = i16 / run;
       int rank = 0;
       for (int j = 0; j < a.groups; ++j) {
-        const double o = __shfl(score, j, 64);
-        rank += (o > score || (o == score && j < lane)) ? 1 : 0;
+        const float o = __shfl(score, (lane & 48) + j * run, 64);
+        rank += (o > score || (o == score && j < mine)) ? 1 : 0;
       }
-      kept = __ballot(lane < a.groups && rank < a.top_groups);
+      const bool kept = rank < a.top_groups;
+      const float worst = row_min(kept ? score : -kNegInf);
+      const float best = row_max(kept ? kNegInf : score);
+      // float32 maxima of exact keys decide exactly; sums and biased keys only beyond tol
+      unsure |= (BIAS || a.group_top == 2) && best != kNegInf && worst - best <= tol;
+      mask = kept ? ~0u : kIdMask;
     }
-    uint32_t taken = 0;
+    // key as a fixed-point number from 1; 0 for a masked (or far lower) one
+    auto fix = [&](float k) { return uint32_t(fmaxf(fmaf(k - lo, f, 1.0f), 0.f)); };
+    uint32_t v[EPL < 8 ? 8 : EPL];
 #pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) {
-      const int e = i * 64 + lane;
-      if (e >= a.E) taken |= 1u << i;
-      else if (!((kept >> (e / per_group)) & 1)) key[i] = kNegInfD;
+    for (int c = 0; c < (EPL < 8 ? 8 : EPL); ++c)
+      v[c] = c < EPL && c < epl ? ((fix(key[c < EPL ? c : 0]) << 10) | (kIdMask - uint32_t(e0 + c))) & mask : 0u;
+    // the lane's best 8, then the token's
+    uint32_t lost = 0;
+#pragma unroll
+    for (int c = 0; c < EPL; c += 8) sort8(v + c);
+#pragma unroll
+    for (int c = 8; c < EPL; c += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lost = max(lost, min(v[i], v[c + 7 - i]));
+        v[i] = max(v[i], v[c + 7 - i]);
+      }
+      bitonic8(v);
     }
-    int my_id = 0;
-    bool my_live = false;
-    for (int k = 0; k < a.K; ++k) {
-      double best = kNegInfD;
-      int at = kMaxE;
+    merge_lanes<kXor1>(v, lost);
+    merge_lanes<kXor2>(v, lost);
+    merge_lanes<kHalfMirror>(v, lost);
+    merge_lanes<kMirror>(v, lost);
+    if (i16 == 0) {
 #pragma unroll
-      for (int i = 0; i < kMaxPer; ++i)
-        if (!((taken >> i) & 1) && (at == kMaxE || key[i] > best)) {
-          best = key[i];
-          at = i * 64 + lane;
+      for (int i = 0; i < kPackK; ++i) s_list[w][t][i] = v[i];
+    }
+    wave_sync();
+    // lane j of a token: its j-th best (from 0) and the next
+    const int j = min(i16, kPackK - 1);
+    const uint32_t wj = s_list[w][t][j], wn = s_list[w][t][min(j + 1, kPackK - 1)];
+    const uint32_t wl = s_list[w][t][a.K - 1];             // the last chosen
+    const uint32_t last = wl >> 10, qj = wj >> 10, qn = wn >> 10;
+    // positions of absent experts and tokens are in the row's LDS too
+    const int id = int(kIdMask - (wj & kIdMask)) & 511;
+    const int idn = int(kIdMask - (wn & kIdMask)) & 511;
+    auto at_logit = [&](int e) {
+      const float x = e < E ? row[e] : kNegInf;
+      return BIAS ? effective_logit(x, s_bias[min(e, 16 * EPL - 1)]) : x;
+    };
+    const float lj = at_logit(id);
+    if (j + 1 < kPackK && qj != 0 && qj - qn <= near && (j < a.K || last - qn <= near)) {
+      // too close to tell, unless equal
+      if (at_logit(idn) != lj || (BIAS && s_bias[min(idn, 16 * EPL - 1)] != s_bias[min(id, 16 * EPL - 1)]))
+        unsure = true;
+    }
+    unsure |= tail && last == 0;
+    // experts that did not make the list but are as near to the last chosen one
+    if (last != 0 && last - (lost >> 10) <= near) {
+      const int idl = int(kIdMask - (wl & kIdMask)) & 511;
+      const float ll = at_logit(idl), bl = BIAS ? s_bias[min(idl, 16 * EPL - 1)] : 0.f;
+      const uint32_t w8 = s_list[w][t][kPackK - 1];
+#pragma unroll 1
+      for (int c = 0; c < epl; c += 4) {
+        float l[4], k[4];
+        logits4(c, l);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = l[i];
+        keys4(c, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = ((fix(k[i]) << 10) | (kIdMask - uint32_t(e0 + c + i))) & mask;
+          if (x < w8 && x >> 10 != 0 && last - (x >> 10) <= near &&
+              (l[i] != ll || (BIAS && s_bias[min(e0 + c + i, 16 * EPL - 1)] != bl)))
+            unsure = true;
         }
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) {
-        const double ob = __shfl_xor(best, d, 64);
-        const int oa = __shfl_xor(at, d, 64);
-        if (ob > best || (ob == best && oa < at)) {
-          best = ob;
-          at = oa;
-        }
-      }
-      if ((at & 63) == lane) taken |= 1u << (at >> 6);
-      if (lane == k) {
-        my_id = at;
-        my_live = best != kNegInfD;
       }
     }
-    __builtin_amdgcn_wave_barrier();
-    const float lk = lane < a.K ? row[my_id] : kNegInf;
-    const float gate = gate_of(a, lane, lk, my_live, m, sum, bad);
-    if (lane < a.K) {
-      a.ids[g * a.K + lane] = my_id;
-      a.gates[g * a.K + lane] = gate;
+    uint32_t again = row_or(unsure && on ? 1u : 0u);
+    // gates
+    const bool live = on && i16 < a.K && qj != 0;
+    float gate;
+    if (!a.renorm) {
+      gate = SOFTMAX ? expf(lj - top) / sum : 1.0f / (1.0f + expf(-lj));
+      gate = live ? gate : 0.f;
+    } else {
+      const float m = row_max(live ? lj : kNegInf);
+      if (SOFTMAX) gate = expf(lj - m);
+      else gate = m >= 0.f ? 1.0f / (1.0f + expf(-lj)) : expf(lj - m) / (1.0f + expf(lj));
+      gate = live ? gate : 0.f;
+      const float total = row_sum(gate);
+      gate = total > 0.f ? gate / total : 0.f;
     }
-    __builtin_amdgcn_wave_barrier();
+    if (on && i16 < a.K && !again) {
+      a.ids[(g0 + t) * a.K + i16] = id;
+      a.gates[(g0 + t) * a.K + i16] = gate * a.scale;
+    }
+    wave_sync();
+    for (uint64_t todo = __ballot(again != 0 && i16 == 0); todo; todo &= todo - 1) {
+      const int64_t g = g0 + __builtin_ctzll(todo) / 16;
+      route_token(a, g, reinterpret_cast<double*>(rows));
+    }
   }
+}
+
+template <int EPL>
+static void launch_packed(const RouteArgs& a, int grid, hipStream_t strm) {
+  const int threads = kRouteWaves * 64;
+  if (a.softmax && a.bias) route_packed_kernel<EPL, true, true><<<grid, threads, 0, strm>>>(a);
+  else if (a.softmax) route_packed_kernel<EPL, true, false><<<grid, threads, 0, strm>>>(a);
+  else if (a.bias) route_packed_kernel<EPL, false, true><<<grid, threads, 0, strm>>>(a);
+  else route_packed_kernel<EPL, false, false><<<grid, threads, 0, strm>>>(a);
 }
 
 struct RouteBackwardArgs {
@@ -307,13 +685,25 @@ extern "C" int moonep_route(const moonep_shape* shape, const moonep_router* rout
     return MOONEP_EINVAL;
   const RouteArgs a{logits, bias, topk_idx, gates, N, s.E, s.K, router->groups,
                     router->top_groups, router->group_top, router->score == MOONEP_SOFTMAX,
-                    router->renorm != 0, router->scale};
+                    router->renorm != 0, router->scale, router->dtype == MOONEP_BF16,
+                    (s.E + 63) / 64 * 4};
+  // packed: the choice fits its list, the experts its registers, and groups, where there
+  // are any, are whole runs of 1, 2, 4 or 8 lanes
+  const bool runs = a.groups == 1 || (a.groups <= 16 && 16 % a.groups == 0 && s.E == 16 * a.epl);
+  if (s.K <= kPackK && s.E <= 512 && runs) {
+    const int64_t blocks = (int64_t(N) + kRouteWaves * kTokens - 1) / (kRouteWaves * kTokens);
+    const int grid = int(blocks);   // N < 2^31: below 2^27
+    hipStream_t strm = as_stream(stream);
+    if (a.epl <= 4) launch_packed<4>(a, grid, strm);
+    else if (a.epl <= 8) launch_packed<8>(a, grid, strm);
+    else if (a.epl <= 16) launch_packed<16>(a, grid, strm);
+    else if (a.epl <= 24) launch_packed<24>(a, grid, strm);
+    else launch_packed<32>(a, grid, strm);
+    return launch_status();
+  }
   const int64_t blocks = (int64_t(N) + kRouteWaves - 1) / kRouteWaves;
   const int grid = int(blocks < 65536 ? blocks : 65536);
-  if (router->dtype == MOONEP_BF16)
-    route_kernel<true><<<grid, kRouteWaves * 64, 0, as_stream(stream)>>>(a);
-  else
-    route_kernel<false><<<grid, kRouteWaves * 64, 0, as_stream(stream)>>>(a);
+  route_kernel<<<grid, kRouteWaves * 64, 0, as_stream(stream)>>>(a);
   return launch_status();
 }
 
