@@ -223,28 +223,35 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
 // min. Each lane sorts its experts in columns of 8, merges them into its best 8, and four
 // butterfly merges give the token's best 8 to all its lanes. The result stands if no two
 // neighbours of the ranking that could change the choice are closer than the keys' error,
-// unless they are equal in logit and bias (then the id decides, as it should). Tokens where
-// one is (0.3% of normal ones, more with many ties of unequal experts), or that hold a NaN
-// or +inf, are done again by route_token.
+// unless they are equal in logit and bias (then the id decides, as it should). Where two
+// are (0.1% of the tokens of a normal sigmoid router), the experts in question are ranked
+// by float64 keys, one per lane; so are groups that are too close. Tokens with a NaN or
+// +inf, or with more than 16 experts in question, are done again by route_token.
 constexpr int kPackK = 8;
 constexpr int kTokens = 4;           // per wavefront
 constexpr uint32_t kIdMask = 1023;
-constexpr float kQMax = 4194300.f;   // fixed-point range: keys 1 .. 2^22 - 3, masked 0
+constexpr uint32_t kNearMax = 4096;  // a wider band of doubt sends the token to route_token
+constexpr float kQMax = 4186000.f;   // fixed-point range: keys 1 .. below 2^22 - kNearMax, masked 0
 
 template <int CTRL>
 __device__ inline uint32_t dpp(uint32_t v) {
-  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, false));
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, true));
 }
 // lane permutations whose pairs span 2, 4, 8 and 16 lanes
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
 template <int CTRL>
 __device__ inline float dppf(float v) { return __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
 
+// Larger and smaller of two numbers in one instruction each (fmaxf also quiets its operands,
+// an instruction per operand that the compiler cannot prove quiet).
+__device__ inline float max2(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -kNegInf); }
+__device__ inline float min2(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, kNegInf); }
+
 __device__ inline float row_max(float v) {
-  v = fmaxf(v, dppf<kXor1>(v));
-  v = fmaxf(v, dppf<kXor2>(v));
-  v = fmaxf(v, dppf<kHalfMirror>(v));
-  return fmaxf(v, dppf<kMirror>(v));
+  v = max2(v, dppf<kXor1>(v));
+  v = max2(v, dppf<kXor2>(v));
+  v = max2(v, dppf<kHalfMirror>(v));
+  return max2(v, dppf<kMirror>(v));
 }
 __device__ inline float row_min(float v) { return -row_max(-v); }
 __device__ inline float row_sum(float v) {
@@ -304,116 +311,145 @@ __device__ inline float fast_sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
 
-// EPL: experts per lane that the registers hold (a.epl of them used, a multiple of 4).
+// Unsigned integer of x, saturating: 0 for a negative x or a NaN.
+__device__ inline uint32_t saturating_uint(float x) {
+  uint32_t r;
+  asm("v_cvt_u32_f32 %0, %1" : "=v"(r) : "v"(x));
+  return r;
+}
+
+// EPL: experts per lane, 4 * ceil(E / 64); the token's row is padded with masked experts.
 template <int EPL, bool SOFTMAX, bool BIAS>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArgs a) {
-  __shared__ __align__(16) float s_row[kRouteWaves][kTokens * 16 * EPL];
-  __shared__ __align__(16) float s_bias[BIAS ? 16 * EPL : 4];
+  constexpr int kRow = 16 * EPL;
+  constexpr int kCols = (EPL + 7) / 8 * 8;     // whole columns of 8
+  constexpr float kLog2e = 1.44269504f;
+  __shared__ __align__(16) float s_row[kRouteWaves][kTokens * kRow];
+  __shared__ __align__(16) float s_bias[BIAS ? kRow : 4];
   __shared__ __align__(16) uint32_t s_list[kRouteWaves][kTokens][kPackK];
+  __shared__ uint32_t s_cand[kRouteWaves][kTokens][16];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, t = lane >> 4, i16 = lane & 15;
-  const int E = a.E, epl = a.epl, e0 = i16 * epl;
+  const int E = a.E, e0 = i16 * EPL;
   float* rows = s_row[w];
+  bool nan_bias = false;
   if (BIAS) {
-    for (int e = threadIdx.x; e < 16 * EPL; e += kRouteWaves * 64)
-      s_bias[e] = e < E ? a.bias[e] : 0.f;
-    __syncthreads();
+    int bad = 0;
+    for (int e = threadIdx.x; e < kRow; e += kRouteWaves * 64) {
+      const float b = e < E ? a.bias[e] : 0.f;
+      s_bias[e] = b;
+      bad |= b != b;
+    }
+    nan_bias = __syncthreads_or(bad) != 0;
   }
-  const bool vec = E % 4 == 0;
   const int64_t g0 = (int64_t(blockIdx.x) * kRouteWaves + w) * kTokens;
   if (g0 < a.N) {   // uniform per wavefront; no workgroup barrier inside
     const int ntok = int(min(int64_t(kTokens), a.N - g0));
-    // the tokens' logits lie together: copy them to LDS as float32
-    const int count = ntok * E;
-    if (vec && a.bf16) {
-      const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + g0 * E);
-      for (int i = lane; i < count / 4; i += 64) {
-        const uint2 u = src[i];
-        reinterpret_cast<float4*>(rows)[i] =
-            make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                        __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+    // the logits as float32, in rows of kRow
+    if (E == kRow && ntok == kTokens) {      // the four rows lie together in memory as well
+      if (a.bf16) {
+        const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + g0 * E);
+#pragma unroll
+        for (int i = 0; i < EPL / 4; ++i) {
+          const uint2 u = src[i * 256 / 4 + lane];
+          uint2 lo2 = make_uint2(u.x << 16, u.x & 0xFFFF0000u), hi2 = make_uint2(u.y << 16, u.y & 0xFFFF0000u);
+          reinterpret_cast<float4*>(rows)[i * 64 + lane] =
+              make_float4(__uint_as_float(lo2.x), __uint_as_float(lo2.y), __uint_as_float(hi2.x),
+                          __uint_as_float(hi2.y));
+        }
+      } else {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + g0 * E);
+#pragma unroll
+        for (int i = 0; i < EPL / 4; ++i) reinterpret_cast<float4*>(rows)[i * 64 + lane] = src[i * 64 + lane];
       }
-    } else if (vec) {
-      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + g0 * E);
-      for (int i = lane; i < count / 4; i += 64) reinterpret_cast<float4*>(rows)[i] = src[i];
     } else {
-      for (int i = lane; i < count; i += 64)
-        rows[i] = a.bf16 ? load_logit<true>(a.logits, g0 * E + i) : load_logit<false>(a.logits, g0 * E + i);
+      for (int r = 0; r < kTokens; ++r)
+        for (int e = lane; e < kRow; e += 64) {
+          float x = kNegInf;
+          if (r < ntok && e < E)
+            x = a.bf16 ? load_logit<true>(a.logits, (g0 + r) * E + e) : load_logit<false>(a.logits, (g0 + r) * E + e);
+          rows[r * kRow + e] = x;
+        }
     }
     wave_sync();
     const bool on = t < ntok;
-    const float* row = rows + t * E;
-    // 4 effective logits of this lane; experts that are not there count as masked
+    const float* row = rows + t * kRow;
     auto logits4 = [&](int c, float* l) {
-      float4 v = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
-      const int e = e0 + c;
-      if (c < epl && e < E) {
-        if (vec) {
-          v = *reinterpret_cast<const float4*>(row + e);
-        } else {
-          v.x = row[e];
-          if (e + 1 < E) v.y = row[e + 1];
-          if (e + 2 < E) v.z = row[e + 2];
-          if (e + 3 < E) v.w = row[e + 3];
-        }
-      }
+      const float4 v = *reinterpret_cast<const float4*>(row + e0 + c);
       l[0] = v.x; l[1] = v.y; l[2] = v.z; l[3] = v.w;
-      if (BIAS) {
-        const float4 b = *reinterpret_cast<const float4*>(s_bias + min(e, 16 * EPL - 4));
-        l[0] = effective_logit(l[0], b.x); l[1] = effective_logit(l[1], b.y);
-        l[2] = effective_logit(l[2], b.z); l[3] = effective_logit(l[3], b.w);
+      if (SOFTMAX && BIAS) {     // a switched-off expert has no part in the softmax
+        const float4 b = *reinterpret_cast<const float4*>(s_bias + e0 + c);
+        l[0] = b.x == kNegInf ? kNegInf : l[0];
+        l[1] = b.y == kNegInf ? kNegInf : l[1];
+        l[2] = b.z == kNegInf ? kNegInf : l[2];
+        l[3] = b.w == kNegInf ? kNegInf : l[3];
       }
     };
-    float top = kNegInf, inv = 0.f, sum = 0.f;   // the largest logit, the softmax sum, 1 / sum
-    // keys of 4 effective logits: -inf of a masked one
+    float top = 0.f, inv = 0.f, sum = 0.f;   // the largest logit, 1 / softmax sum, the sum
+    // keys of 4 logits: -inf of a masked expert (a bias of -inf makes it so by itself)
     auto keys4 = [&](int c, float* l) {
       if (!BIAS) return;
-      const float4 b4 = *reinterpret_cast<const float4*>(s_bias + min(e0 + c, 16 * EPL - 4));
+      const float4 b4 = *reinterpret_cast<const float4*>(s_bias + e0 + c);
       const float b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float s = SOFTMAX ? __builtin_amdgcn_exp2f((l[i] - top) * 1.44269504f) * inv
+        const float s = SOFTMAX ? __builtin_amdgcn_exp2f((l[i] - top) * kLog2e) * inv
                                 : fast_sigmoid(l[i]);
         l[i] = l[i] == kNegInf ? kNegInf : s + b[i];
       }
     };
+    // the same in float64, for the few tokens whose float32 keys are too close: the sum of
+    // e^(l - top) over the token, and score + bias of expert e
+    auto softmax_sum = [&]() {
+      double d = 0.0;
+#pragma unroll 1
+      for (int c = 0; c < EPL; ++c) {
+        float l = row[e0 + c];
+        if (BIAS) l = s_bias[e0 + c] == kNegInf ? kNegInf : l;
+        d += exp(double(l) - double(top));
+      }
+      for (int o = 1; o < 16; o <<= 1) d += __shfl_xor(d, o, 64);
+      return d;
+    };
+    auto value = [&](int e, double total) {
+      const float l = row[e], b = BIAS ? s_bias[e] : 0.f;
+      if (l == kNegInf || b == kNegInf) return kNegInfD;
+      const double s = SOFTMAX ? exp(double(l) - double(top)) / total : 1.0 / (1.0 + exp(-double(l)));
+      return BIAS ? s + double(b) : s;
+    };
     float key[EPL];
-    bool unsure = false;
     float hi = kNegInf, lo = -kNegInf;
 #pragma unroll
-    for (int c = 0; c < EPL; c += 4) {
-      logits4(c, key + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        unsure |= key[c + i] != key[c + i];
-        hi = fmaxf(hi, key[c + i]);
-      }
-    }
-    unsure |= hi == -kNegInf;
+    for (int c = 0; c < EPL; c += 4) logits4(c, key + c);
     if (SOFTMAX) {
+#pragma unroll
+      for (int c = 0; c < EPL; ++c) hi = max2(hi, key[c]);
       top = row_max(hi);
       top = top == kNegInf ? 0.f : top;   // nothing left: every e^(l - top) is 0
       if (BIAS || !a.renorm) {
 #pragma unroll
-        for (int c = 0; c < EPL; ++c) sum += __builtin_amdgcn_exp2f((key[c] - top) * 1.44269504f);
+        for (int c = 0; c < EPL; ++c) sum += __builtin_amdgcn_exp2f((key[c] - top) * kLog2e);
         sum = row_sum(sum);
         inv = __builtin_amdgcn_rcpf(sum);
       }
-    }
-    if (BIAS) {
       hi = kNegInf;
-#pragma unroll
-      for (int c = 0; c < EPL; c += 4) {
-        keys4(c, key + c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          unsure |= key[c + i] != key[c + i];
-          hi = fmaxf(hi, key[c + i]);
-        }
-      }
-      unsure |= hi == -kNegInf;
     }
+    bool unsure = nan_bias;
 #pragma unroll
-    for (int c = 0; c < EPL; ++c) lo = fminf(lo, key[c] == kNegInf ? lo : key[c]);
+    for (int c = 0; c < EPL; c += 4) {
+      keys4(c, key + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        unsure |= key[c + i] != key[c + i];
+        hi = max2(hi, key[c + i]);
+        lo = min2(lo, key[c + i]);
+      }
+    }
+    unsure |= hi == -kNegInf;
+    if (__any(lo == kNegInf)) {     // masked experts: the lowest of the others
+      lo = -kNegInf;
+#pragma unroll
+      for (int c = 0; c < EPL; ++c) lo = min2(lo, key[c] == kNegInf ? lo : key[c]);
+    }
     hi = row_max(hi);
     lo = row_min(lo);
     // float32 keys are off by at most `err`: sigmoid 2^-22, softmax 2^-18 of the largest
@@ -421,27 +457,28 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
     // with the bias 2^-23 of itself; logits are exact
     const float err = !BIAS ? 0.f
                             : (SOFTMAX ? 3.8146973e-6f * inv : 2.3841858e-7f) +
-                                  1.1920929e-7f * fmaxf(fabsf(hi), fabsf(lo));
+                                  1.1920929e-7f * max2(fabsf(hi), fabsf(lo));
     // a long tail of low keys would take the range's resolution: keys more than 64 below the
     // highest get the number of masked ones
     const bool tail = lo < hi - 64.f;
     if (tail) lo = hi - 64.f;
-    const float f = hi > lo ? kQMax * 0.9999995f * __builtin_amdgcn_rcpf(hi - lo) : 0.f;
-    const uint32_t near = BIAS ? uint32_t(fminf(2.f * err * f, 4.0e6f)) + 2 : 0;
+    float f = hi > lo ? kQMax * 0.9999995f * __builtin_amdgcn_rcpf(hi - lo) : 0.f;
+    const uint32_t near = BIAS ? saturating_uint(2.f * err * f) + 3 : 0;
+    unsure |= near > kNearMax;
 
     // groups: the token's groups are runs of its lanes (checked by the host)
-    uint32_t mask = ~0u;      // keeps a word, or the id alone where the group does not stay
+    bool kept = true;
     if (a.groups > 1) {
       float m1 = kNegInf, m2 = kNegInf;
 #pragma unroll
       for (int c = 0; c < EPL; ++c) {
         m2 = __builtin_amdgcn_fmed3f(m1, m2, key[c]);
-        m1 = fmaxf(m1, key[c]);
+        m1 = max2(m1, key[c]);
       }
       const int run = 16 / a.groups;
       auto join = [&](float o1, float o2) {
-        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-        m1 = fmaxf(m1, o1);
+        m2 = max2(min2(m1, o1), max2(m2, o2));
+        m1 = max2(m1, o1);
       };
       if (run >= 2) join(dppf<kXor1>(m1), dppf<kXor1>(m2));
       if (run >= 4) join(dppf<kXor2>(m1), dppf<kXor2>(m2));
@@ -450,8 +487,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
       if (a.group_top == 2) {
         if (!BIAS) {   // the two best logits' scores (softmax: all by the same factor)
           if (SOFTMAX) {
-            m1 = __builtin_amdgcn_exp2f((m1 - top) * 1.44269504f);
-            m2 = __builtin_amdgcn_exp2f((m2 - top) * 1.44269504f);
+            m1 = __builtin_amdgcn_exp2f((m1 - top) * kLog2e);
+            m2 = __builtin_amdgcn_exp2f((m2 - top) * kLog2e);
           } else {
             m1 = fast_sigmoid(m1);
             m2 = fast_sigmoid(m2);
@@ -465,30 +502,54 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
         }
       }
       const int mine = i16 / run;
-      int rank = 0;
-      for (int j = 0; j < a.groups; ++j) {
-        const float o = __shfl(score, (lane & 48) + j * run, 64);
-        rank += (o > score || (o == score && j < mine)) ? 1 : 0;
-      }
-      const bool kept = rank < a.top_groups;
+      auto ranked = [&](auto v) {      // groups before mine
+        int rank = 0;
+        for (int j = 0; j < a.groups; ++j) {
+          const auto o = __shfl(v, (lane & 48) + j * run, 64);
+          rank += (o > v || (o == v && j < mine)) ? 1 : 0;
+        }
+        return rank;
+      };
+      kept = ranked(score) < a.top_groups;
       const float worst = row_min(kept ? score : -kNegInf);
       const float best = row_max(kept ? kNegInf : score);
       // float32 maxima of exact keys decide exactly; sums and biased keys only beyond tol
-      unsure |= (BIAS || a.group_top == 2) && best != kNegInf && worst - best <= tol;
-      mask = kept ? ~0u : kIdMask;
+      if ((BIAS || a.group_top == 2) && __any(on && best != kNegInf && worst - best <= tol)) {
+        double d1 = kNegInfD, d2 = kNegInfD;
+        const double total = SOFTMAX ? softmax_sum() : 0.0;
+#pragma unroll 1
+        for (int c = 0; c < EPL; ++c) {
+          const double x = value(e0 + c, total);
+          d2 = fmax(fmin(d1, x), d2);
+          d1 = fmax(d1, x);
+        }
+        for (int d = 1; d < run; d <<= 1) {
+          const double o1 = __shfl_xor(d1, d, 64), o2 = __shfl_xor(d2, d, 64);
+          d2 = fmax(fmin(d1, o1), fmax(d2, o2));
+          d1 = fmax(d1, o1);
+        }
+        kept = ranked(a.group_top == 2 && d2 != kNegInfD ? d1 + d2 : d1) < a.top_groups;
+      }
     }
-    // key as a fixed-point number from 1; 0 for a masked (or far lower) one
-    auto fix = [&](float k) { return uint32_t(fmaxf(fmaf(k - lo, f, 1.0f), 0.f)); };
-    uint32_t v[EPL < 8 ? 8 : EPL];
+    // Key as a fixed-point number from 1; 0 for a masked (or far lower) one and for any of a
+    // group that does not stay. Exact keys keep their order exactly; with a bias one fused
+    // multiply-add will do, whose rounding of the offset `near` covers.
+    const float add = kept ? (BIAS ? float(near) + 1.f - lo * f : 1.f) : 0.f;
+    if (!kept) f = 0.f;
+    auto fix = [&](float k) {
+      if (BIAS) return saturating_uint(fmaf(k, f, add));
+      return saturating_uint(fmaf(k - lo, f, add));
+    };
+    uint32_t v[kCols];
+    const uint32_t id0 = kIdMask - uint32_t(e0);
 #pragma unroll
-    for (int c = 0; c < (EPL < 8 ? 8 : EPL); ++c)
-      v[c] = c < EPL && c < epl ? ((fix(key[c < EPL ? c : 0]) << 10) | (kIdMask - uint32_t(e0 + c))) & mask : 0u;
+    for (int c = 0; c < kCols; ++c) v[c] = c < EPL ? (fix(key[c < EPL ? c : 0]) << 10) | (id0 - c) : 0u;
     // the lane's best 8, then the token's
     uint32_t lost = 0;
 #pragma unroll
-    for (int c = 0; c < EPL; c += 8) sort8(v + c);
+    for (int c = 0; c < kCols; c += 8) sort8(v + c);
 #pragma unroll
-    for (int c = 8; c < EPL; c += 8) {
+    for (int c = 8; c < kCols; c += 8) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         lost = max(lost, min(v[i], v[c + 7 - i]));
@@ -507,44 +568,81 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
     wave_sync();
     // lane j of a token: its j-th best (from 0) and the next
     const int j = min(i16, kPackK - 1);
-    const uint32_t wj = s_list[w][t][j], wn = s_list[w][t][min(j + 1, kPackK - 1)];
-    const uint32_t wl = s_list[w][t][a.K - 1];             // the last chosen
-    const uint32_t last = wl >> 10, qj = wj >> 10, qn = wn >> 10;
-    // positions of absent experts and tokens are in the row's LDS too
-    const int id = int(kIdMask - (wj & kIdMask)) & 511;
-    const int idn = int(kIdMask - (wn & kIdMask)) & 511;
-    auto at_logit = [&](int e) {
-      const float x = e < E ? row[e] : kNegInf;
-      return BIAS ? effective_logit(x, s_bias[min(e, 16 * EPL - 1)]) : x;
-    };
-    const float lj = at_logit(id);
-    if (j + 1 < kPackK && qj != 0 && qj - qn <= near && (j < a.K || last - qn <= near)) {
-      // too close to tell, unless equal
-      if (at_logit(idn) != lj || (BIAS && s_bias[min(idn, 16 * EPL - 1)] != s_bias[min(id, 16 * EPL - 1)]))
-        unsure = true;
-    }
+    // (a list of fewer than 8 experts ends in zeros, whose id is cut to a place in the row)
+    auto expert = [&](uint32_t x) { return min(int(kIdMask - (x & kIdMask)), kRow - 1); };
+    const uint32_t wl = s_list[w][t][a.K - 1], last = wl >> 10;      // the last chosen
     unsure |= tail && last == 0;
-    // experts that did not make the list but are as near to the last chosen one
-    if (last != 0 && last - (lost >> 10) <= near) {
-      const int idl = int(kIdMask - (wl & kIdMask)) & 511;
-      const float ll = at_logit(idl), bl = BIAS ? s_bias[min(idl, 16 * EPL - 1)] : 0.f;
-      const uint32_t w8 = s_list[w][t][kPackK - 1];
+    bool close = false;
+    {
+      const uint32_t wj = s_list[w][t][j], wn = s_list[w][t][min(j + 1, kPackK - 1)];
+      const uint32_t qj = wj >> 10, qn = wn >> 10;
+      if (j + 1 < kPackK && qj != 0 && qj - qn <= near && (j < a.K || last - qn <= near)) {
+        // too close to tell, unless equal
+        const int idj = expert(wj), idn = expert(wn);
+        close = row[idn] != row[idj] || (BIAS && s_bias[idn] != s_bias[idj]);
+      }
+    }
+    // this lane's experts by number: calls f(fixed-point key, logit, expert)
+    auto scan = [&](auto f) {
 #pragma unroll 1
-      for (int c = 0; c < epl; c += 4) {
+      for (int c = 0; c < EPL; c += 4) {
         float l[4], k[4];
         logits4(c, l);
 #pragma unroll
         for (int i = 0; i < 4; ++i) k[i] = l[i];
         keys4(c, k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x = ((fix(k[i]) << 10) | (kIdMask - uint32_t(e0 + c + i))) & mask;
-          if (x < w8 && x >> 10 != 0 && last - (x >> 10) <= near &&
-              (l[i] != ll || (BIAS && s_bias[min(e0 + c + i, 16 * EPL - 1)] != bl)))
-            unsure = true;
-        }
+        for (int i = 0; i < 4; ++i) f(fix(k[i]), l[i], e0 + c + i);
       }
+    };
+    // experts that did not make the list but are as near to the last chosen one
+    if (last != 0 && last - (lost >> 10) <= near) {
+      const int idl = expert(wl);
+      const float ll = row[idl], bl = BIAS ? s_bias[idl] : 0.f;
+      const uint32_t w8 = s_list[w][t][kPackK - 1];
+      scan([&](uint32_t q, float l, int e) {
+        if (((q << 10) | (kIdMask - uint32_t(e))) < w8 && q != 0 && last - min(q, last) <= near)
+          close |= l != ll || (BIAS && s_bias[e] != bl);
+      });
     }
+    close = row_or(close ? 1u : 0u) != 0;
+    if (__any(on && close)) {
+      // Every expert that could be among the best K, one per lane, in the order of float64
+      // keys; more than 16 of them are left to route_token.
+      const double total = SOFTMAX && BIAS ? softmax_sum() : 0.0;
+      const uint32_t bar = last > near ? last - near : 1;
+      int n = 0;
+      scan([&](uint32_t q, float, int) { n += q >= bar ? 1 : 0; });
+      int incl = n;
+      for (int d = 1; d < 16; d <<= 1) {
+        const int o = __shfl_up(incl, d, 16);
+        if (i16 >= d) incl += o;
+      }
+      const int count = __shfl(incl, 15, 16);
+      int at = incl - n;
+      scan([&](uint32_t q, float, int e) {
+        if (q >= bar) {
+          if (at < 16) s_cand[w][t][at] = (q << 10) | (kIdMask - uint32_t(e));
+          ++at;
+        }
+      });
+      wave_sync();
+      const uint32_t mine = i16 < count ? s_cand[w][t][i16] : 0;
+      const int e = expert(mine);
+      const double x = i16 >= count ? kNegInfD : BIAS ? value(e, total) : double(row[e]);
+      int rank = 0;
+      for (int r = 0; r < 16; ++r) {
+        const double o = __shfl(x, r, 16);
+        const int oe = __shfl(e, r, 16);
+        rank += r < count && (o > x || (o == x && oe < e)) ? 1 : 0;
+      }
+      if (close && count <= 16 && i16 < count && rank < a.K) s_list[w][t][rank] = mine;
+      unsure |= close && count > 16;
+      wave_sync();
+    }
+    const uint32_t wj = s_list[w][t][j], qj = wj >> 10;
+    const int id = expert(wj);
+    const float lj = row[id];
     uint32_t again = row_or(unsure && on ? 1u : 0u);
     // gates
     const bool live = on && i16 < a.K && qj != 0;
@@ -694,11 +792,16 @@ extern "C" int moonep_route(const moonep_shape* shape, const moonep_router* rout
     const int64_t blocks = (int64_t(N) + kRouteWaves * kTokens - 1) / (kRouteWaves * kTokens);
     const int grid = int(blocks);   // N < 2^31: below 2^27
     hipStream_t strm = as_stream(stream);
-    if (a.epl <= 4) launch_packed<4>(a, grid, strm);
-    else if (a.epl <= 8) launch_packed<8>(a, grid, strm);
-    else if (a.epl <= 16) launch_packed<16>(a, grid, strm);
-    else if (a.epl <= 24) launch_packed<24>(a, grid, strm);
-    else launch_packed<32>(a, grid, strm);
+    switch (a.epl) {
+      case 4: launch_packed<4>(a, grid, strm); break;
+      case 8: launch_packed<8>(a, grid, strm); break;
+      case 12: launch_packed<12>(a, grid, strm); break;
+      case 16: launch_packed<16>(a, grid, strm); break;
+      case 20: launch_packed<20>(a, grid, strm); break;
+      case 24: launch_packed<24>(a, grid, strm); break;
+      case 28: launch_packed<28>(a, grid, strm); break;
+      default: launch_packed<32>(a, grid, strm); break;
+    }
     return launch_status();
   }
   const int64_t blocks = (int64_t(N) + kRouteWaves - 1) / kRouteWaves;
