@@ -220,8 +220,10 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
 // expert gets one 32-bit word, its float32 key as a 22-bit fixed-point number between the
 // token's lowest and highest key, above its complemented id: unsigned order is (key
 // descending, id ascending), a word is its own payload, and one comparator is a max and a
-// min. Each lane sorts its experts in columns of 8, merges them into its best 8, and four
-// butterfly merges give the token's best 8 to all its lanes. The result stands if no two
+// min. Each lane sorts its experts in columns of 8 and merges them into its best 8; the
+// token's best 8 are then taken one by one from the heads of its lanes' lists (a maximum
+// over 16 lanes is four instructions; merging the lists lane by lane took 216 instead of
+// 85). The result stands if no two
 // neighbours of the ranking that could change the choice are closer than the keys' error,
 // unless they are equal in logit and bias (then the id decides, as it should). Where two
 // are (0.1% of the tokens of a normal sigmoid router), the experts in question are ranked
@@ -242,10 +244,28 @@ constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
 template <int CTRL>
 __device__ inline float dppf(float v) { return __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
 
-// Larger and smaller of two numbers in one instruction each (fmaxf also quiets its operands,
-// an instruction per operand that the compiler cannot prove quiet).
-__device__ inline float max2(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -kNegInf); }
-__device__ inline float min2(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, kNegInf); }
+// Larger and smaller of numbers in one instruction: fmaxf also quiets each operand that the
+// compiler cannot prove quiet, at an instruction apiece.
+__device__ inline float max2(float a, float b) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ inline float min2(float a, float b) {
+  float r;
+  asm("v_min_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ inline float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ inline float min3(float a, float b, float c) {
+  float r;
+  asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
 
 __device__ inline float row_max(float v) {
   v = max2(v, dppf<kXor1>(v));
@@ -289,21 +309,11 @@ __device__ inline void bitonic8(uint32_t* v) {
     for (int i = 0; i < 8; ++i)
       if (!(i & d)) order(v[i], v[i + d]);
 }
-// v: the best 8 of two descending lists of 8, its own and its partner lane's; lost: the best
-// of what any merge dropped on the way.
-template <int CTRL>
-__device__ inline void merge_lanes(uint32_t* v, uint32_t& lost) {
-  uint32_t o[8];
-  lost = max(lost, dpp<CTRL>(lost));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t p = dpp<CTRL>(v[7 - i]);
-    o[i] = max(v[i], p);
-    lost = max(lost, min(v[i], p));
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = o[i];
-  bitonic8(v);
+__device__ inline uint32_t row_max_u(uint32_t v) {
+  v = max(v, dpp<kXor1>(v));
+  v = max(v, dpp<kXor2>(v));
+  v = max(v, dpp<kHalfMirror>(v));
+  return max(v, dpp<kMirror>(v));
 }
 
 // 1 / (1 + e^-x), within 2^-22
@@ -422,7 +432,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
     for (int c = 0; c < EPL; c += 4) logits4(c, key + c);
     if (SOFTMAX) {
 #pragma unroll
-      for (int c = 0; c < EPL; ++c) hi = max2(hi, key[c]);
+      for (int c = 0; c < EPL; c += 2) hi = max3(hi, key[c], key[c + 1]);
       top = row_max(hi);
       top = top == kNegInf ? 0.f : top;   // nothing left: every e^(l - top) is 0
       if (BIAS || !a.renorm) {
@@ -438,11 +448,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
     for (int c = 0; c < EPL; c += 4) {
       keys4(c, key + c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        unsure |= key[c + i] != key[c + i];
-        hi = max2(hi, key[c + i]);
-        lo = min2(lo, key[c + i]);
-      }
+      for (int i = 0; i < 4; ++i) unsure |= key[c + i] != key[c + i];
+      hi = max3(max3(hi, key[c], key[c + 1]), key[c + 2], key[c + 3]);
+      lo = min3(min3(lo, key[c], key[c + 1]), key[c + 2], key[c + 3]);
     }
     unsure |= hi == -kNegInf;
     if (__any(lo == kNegInf)) {     // masked experts: the lowest of the others
@@ -557,13 +565,19 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
       }
       bitonic8(v);
     }
-    merge_lanes<kXor1>(v, lost);
-    merge_lanes<kXor2>(v, lost);
-    merge_lanes<kHalfMirror>(v, lost);
-    merge_lanes<kMirror>(v, lost);
+    // the token's: 8 times the best head of its lanes' lists, which then move up
+    uint32_t found[kPackK];
+#pragma unroll
+    for (int k = 0; k < kPackK; ++k) {
+      found[k] = row_max_u(v[0]);
+      const bool mine = v[0] == found[k];
+#pragma unroll
+      for (int i = 0; i + k < kPackK; ++i) v[i] = mine ? (i + k + 1 < kPackK ? v[i + 1] : 0u) : v[i];
+    }
+    lost = row_max_u(max(lost, v[0]));
     if (i16 == 0) {
 #pragma unroll
-      for (int i = 0; i < kPackK; ++i) s_list[w][t][i] = v[i];
+      for (int i = 0; i < kPackK; ++i) s_list[w][t][i] = found[i];
     }
     wave_sync();
     // lane j of a token: its j-th best (from 0) and the next
