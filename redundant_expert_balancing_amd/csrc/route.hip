@@ -703,9 +703,10 @@ struct RouteBackwardArgs {
   int N, E, K;
   bool softmax, renorm;
   float scale;
+  bool bf16;
 };
 
-// One wavefront per token: lane k < K forms the gradient d of its choice's logit, then
+// Any E: one wavefront per token. Lane k < K forms the gradient of its choice's logit, then
 // the row is written, each expert adding the choices that name it in k order.
 template <bool BF16>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteBackwardArgs a) {
@@ -761,6 +762,124 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteB
       }
     }
   }
+}
+
+// Packed form for rows of whole 16-byte (float32) vectors, E <= 512: 16 lanes per token, four
+// tokens per wavefront. The row (zeros, or -s sum g dg of the dense form) is put into LDS,
+// the choices' gradients are added there, and the row is written out in vectors.
+template <int EPL, bool DENSE>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_backward_packed_kernel(RouteBackwardArgs a) {
+  constexpr int kRow = 16 * EPL;
+  constexpr float kLog2e = 1.44269504f;
+  __shared__ __align__(16) float s_row[kRouteWaves][kTokens * kRow];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, t = lane >> 4, i16 = lane & 15;
+  const int64_t g = (int64_t(blockIdx.x) * kRouteWaves + w) * kTokens + t;
+  const bool on = g < a.N;
+  float* row = s_row[w] + t * kRow;
+  // this lane's vectors of 4 experts: i16, i16 + 16, ...
+  float x[EPL];
+  if (DENSE) {
+#pragma unroll
+    for (int c = 0; c < EPL; c += 4) {
+      const int e = c * 16 + i16 * 4;
+      float4 v = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+      if (on && e < a.E) {
+        if (a.bf16) {
+          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + g * a.E + e);
+          v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                          __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+        } else {
+          v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + g * a.E + e);
+        }
+        if (a.bias) {
+          const float4 b = *reinterpret_cast<const float4*>(a.bias + e);
+          v = make_float4(effective_logit(v.x, b.x), effective_logit(v.y, b.y),
+                          effective_logit(v.z, b.z), effective_logit(v.w, b.w));
+        }
+      }
+      x[c] = v.x; x[c + 1] = v.y; x[c + 2] = v.z; x[c + 3] = v.w;
+    }
+  }
+  // the choices, 16 at a time, K <= 32
+  int id[2];
+  float gate[2], d[2], mean = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int k = h * 16 + i16;
+    id[h] = -1;
+    gate[h] = d[h] = 0.f;
+    if (on && k < a.K) {
+      id[h] = a.ids[g * a.K + k];
+      if (id[h] < 0 || id[h] >= a.E) id[h] = -1;
+      gate[h] = id[h] >= 0 ? a.gates[g * a.K + k] : 0.f;
+      d[h] = gate[h] != 0.f ? a.dgates[g * a.K + k] : 0.f;   // a gate of 0 has no gradient
+    }
+    mean += gate[h] * d[h];
+  }
+  mean = row_sum(mean);
+  if (DENSE) {
+    float m = kNegInf, sum = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) {
+      m = max2(m, x[c]);
+      nan |= x[c] != x[c];
+    }
+    m = row_max(m);
+    m = m == kNegInf ? 0.f : m;
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) {
+      x[c] = __builtin_amdgcn_exp2f((x[c] - m) * kLog2e);
+      sum += x[c];
+    }
+    sum = row_sum(nan ? __builtin_nanf("") : sum);
+    const float f = sum != 0.f ? -mean / sum : 0.f;
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) x[c] *= f;
+  } else {
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) x[c] = 0.f;
+  }
+#pragma unroll
+  for (int c = 0; c < EPL; c += 4)
+    *reinterpret_cast<float4*>(row + c * 16 + i16 * 4) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+  wave_sync();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (id[h] < 0) continue;
+    float v = gate[h] * (a.renorm ? d[h] - mean / a.scale : d[h]);
+    if (!a.softmax && gate[h] != 0.f) {
+      const float l = a.bf16 ? load_logit<true>(a.logits, g * a.E + id[h])
+                             : load_logit<false>(a.logits, g * a.E + id[h]);
+      v /= 1.0f + expf(l);   // 1 - sigmoid
+    }
+    // lanes of one instruction add in lane order, so a repeated id is summed in k order
+    atomicAdd(row + id[h], v);
+  }
+  wave_sync();
+  if (!on) return;
+#pragma unroll
+  for (int c = 0; c < EPL; c += 4) {
+    const int e = c * 16 + i16 * 4;
+    if (e >= a.E) continue;
+    const float4 v = *reinterpret_cast<const float4*>(row + e);
+    if (a.bf16) {
+      uint2 u;
+      u.x = bf16_rne_any(v.x) | (bf16_rne_any(v.y) << 16);
+      u.y = bf16_rne_any(v.z) | (bf16_rne_any(v.w) << 16);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + g * a.E + e) = u;
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + g * a.E + e) = v;
+    }
+  }
+}
+
+template <int EPL>
+static void launch_backward_packed(const RouteBackwardArgs& a, int grid, hipStream_t strm) {
+  if (a.softmax && !a.renorm)
+    route_backward_packed_kernel<EPL, true><<<grid, kRouteWaves * 64, 0, strm>>>(a);
+  else
+    route_backward_packed_kernel<EPL, false><<<grid, kRouteWaves * 64, 0, strm>>>(a);
 }
 
 static int check_router(const moonep_shape& s, const moonep_router* r) {
@@ -840,7 +959,20 @@ extern "C" int moonep_route_backward(const moonep_shape* shape, const moonep_rou
       !aligned16(gates) || !aligned16(dgates) || !aligned16(dlogits))
     return MOONEP_EINVAL;
   const RouteBackwardArgs a{logits, bias, topk_idx, gates, dgates, dlogits, N, s.E, s.K,
-                            router->score == MOONEP_SOFTMAX, router->renorm != 0, router->scale};
+                            router->score == MOONEP_SOFTMAX, router->renorm != 0, router->scale,
+                            router->dtype == MOONEP_BF16};
+  if (s.E % 4 == 0 && s.E <= 512) {
+    const int64_t blocks = (int64_t(N) + kRouteWaves * kTokens - 1) / (kRouteWaves * kTokens);
+    const int grid = int(blocks);
+    hipStream_t strm = as_stream(stream);
+    const int epl = (s.E + 63) / 64 * 4;
+    if (epl <= 4) launch_backward_packed<4>(a, grid, strm);
+    else if (epl <= 8) launch_backward_packed<8>(a, grid, strm);
+    else if (epl <= 16) launch_backward_packed<16>(a, grid, strm);
+    else if (epl <= 24) launch_backward_packed<24>(a, grid, strm);
+    else launch_backward_packed<32>(a, grid, strm);
+    return launch_status();
+  }
   const int64_t blocks = (int64_t(N) + kRouteWaves - 1) / kRouteWaves;
   const int grid = int(blocks < 65536 ? blocks : 65536);
   if (router->dtype == MOONEP_BF16)
