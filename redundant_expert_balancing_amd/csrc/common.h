@@ -113,6 +113,24 @@ __device__ inline float swiglu_f32(float g, float u) { return g / (1.0f + expf(-
 // + p % kSwigluBlock and its up projection kSwigluBlock further.
 constexpr int kSwigluBlock = MOONEP_SWIGLU_BLOCK;
 
+// Row-wise kernels of kRowThreads threads: rows are spread over a workgroup as 256 >> shift rows of 1 << shift threads, so that rows
+// narrower than a workgroup share one, and no thread divides.
+constexpr int kRowThreads = 256;
+struct RowSplit {
+  int shift;
+  __device__ int row() const { return int(threadIdx.x) >> shift; }
+  __device__ int first() const { return int(threadIdx.x) & ((1 << shift) - 1); }
+  __device__ int step() const { return 1 << shift; }
+  __host__ __device__ int rows() const { return kRowThreads >> shift; }
+};
+
+// Threads per row for `items` work items of a row, at most `most`.
+inline RowSplit row_split(int64_t items, int most) {
+  int shift = 0;
+  while ((1 << shift) < items && (1 << shift) < most) ++shift;
+  return RowSplit{shift};
+}
+
 // Layouts of the 4-bit expert operands (moonep.h, "Experts in 4 bits"): tiles of 128 and
 // chunks of 512 along the reduction.
 constexpr int kScaleBlock = 32;

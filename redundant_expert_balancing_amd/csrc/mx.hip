@@ -46,32 +46,31 @@ __device__ inline void load8(const void* base, int64_t idx, float* v) {
 // One thread per 8 values, 4 neighbouring lanes per block; rows padded to whole chunks of
 // 512, whose threads past the k-tiles only write the padding scales.
 template <bool BF16>
-__global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const void* __restrict__ src,
-                                                                 int64_t rows, int width, int KT,
-                                                                 int KC, uint8_t* __restrict__ q,
-                                                                 uint8_t* __restrict__ scales) {
-  const int per_row = KC * 64;
-  const int64_t total = rows * per_row;
-  for (int64_t i = blockIdx.x * int64_t(kMxThreads) + threadIdx.x; i < total;
-       i += int64_t(gridDim.x) * kMxThreads) {
-    const int64_t r = i / per_row;
-    const int c = int(i - r * per_row);       // 8 values each
-    float v[8];
-    uint32_t m = 0;
+__global__ __launch_bounds__(kRowThreads) void mx_quantize_kernel(const void* __restrict__ src,
+                                                                  int64_t rows, int width, int KT,
+                                                                  int KC, RowSplit sp,
+                                                                  uint8_t* __restrict__ q,
+                                                                  uint8_t* __restrict__ scales) {
+  for (int64_t r = int64_t(blockIdx.x) * sp.rows() + sp.row(); r < rows;
+       r += int64_t(gridDim.x) * sp.rows()) {
+    for (int c = sp.first(); c < KC * 64; c += sp.step()) {
+      float v[8];
+      uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    if (c * 8 < width) load8<BF16>(src, r * width + c * 8, v);
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      if (c * 8 < width) load8<BF16>(src, r * width + c * 8, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, mag_bits(v[j]));
-    m = max(m, uint32_t(__shfl_xor(int(m), 1, 64)));
-    m = max(m, uint32_t(__shfl_xor(int(m), 2, 64)));
-    const uint32_t b = scale_byte<E2M1>(m);
-    if (c * 8 < KT * 128)
-      *reinterpret_cast<uint32_t*>(q + r * (KT * 64) + c * 4) =
-          b == 255 ? 0u : pack_e2m1(v, scale_inverse(b));
-    if ((c & 3) == 0) {
-      const int blk = c >> 2;
-      scales[r * (KC * 16) + (blk >> 4) * 16 + (blk & 3) * 4 + ((blk >> 2) & 3)] = uint8_t(b);
+      for (int j = 0; j < 8; ++j) m = max(m, mag_bits(v[j]));
+      m = max(m, uint32_t(__shfl_xor(int(m), 1, 64)));
+      m = max(m, uint32_t(__shfl_xor(int(m), 2, 64)));
+      const uint32_t b = scale_byte<E2M1>(m);
+      if (c < KT * 16)
+        *reinterpret_cast<uint32_t*>(q + r * (KT * 64) + c * 4) =
+            b == 255 ? 0u : pack_e2m1(v, scale_inverse(b));
+      if ((c & 3) == 0) {
+        const int blk = c >> 2;
+        scales[r * (KC * 16) + (blk >> 4) * 16 + (blk & 3) * 4 + ((blk >> 2) & 3)] = uint8_t(b);
+      }
     }
   }
 }
@@ -420,11 +419,13 @@ extern "C" int moonep_mx_quantize(const moonep_shape* shape, int64_t rows, int32
   if (rows == 0) return MOONEP_OK;
   if (!aligned16(src) || !aligned16(q) || !aligned16(scales)) return MOONEP_EINVAL;
   const int KT = int(k_tiles(width)), KC = int(k_chunks(width));
-  const int grid = mx_grid(rows * KC * 64, 65536);
+  const RowSplit sp = row_split(int64_t(KC) * 64, kRowThreads);
+  const int64_t blocks = (rows + sp.rows() - 1) / sp.rows();
+  const int grid = int(blocks < 65536 ? blocks : 65536);
   if (shape->dtype == MOONEP_BF16)
-    mx_quantize_kernel<true><<<grid, kMxThreads, 0, as_stream(stream)>>>(src, rows, width, KT, KC, q, scales);
+    mx_quantize_kernel<true><<<grid, kRowThreads, 0, as_stream(stream)>>>(src, rows, width, KT, KC, sp, q, scales);
   else
-    mx_quantize_kernel<false><<<grid, kMxThreads, 0, as_stream(stream)>>>(src, rows, width, KT, KC, q, scales);
+    mx_quantize_kernel<false><<<grid, kRowThreads, 0, as_stream(stream)>>>(src, rows, width, KT, KC, sp, q, scales);
   return launch_status();
 }
 
