@@ -207,27 +207,31 @@ __device__ inline v4f_t mfma_e2m1(v8i_t a, v8i_t b, v4f_t c, int sa, int sb) {
 constexpr int kNonTemporal = 2;   // buffer cache policy: the output is not read back here
 
 // ---- tiled form: 128 x 256 output tiles, four wavefronts side by side in N (128 x 64 each),
-// 256 k per step.
+// 256 k per step. (64-row tiles measured 10-20% slower wherever the card is full.)
 struct MxTile {
-  static constexpr int BM = 128, BN = 256, WAVES = 4;
+  static constexpr int FM = 8, FN = 4;                  // 16 x 16 blocks of a wavefront
+  static constexpr int BM = 16 * FM, BN = 256, WAVES = 4;
   static constexpr int STEPB = 128;                     // bytes of a row per step
   static constexpr int A_BYTES = BM * STEPB;            // LDS per stage
-  static constexpr int S_BYTES = BM * 16;               // LDS per chunk of scales
-  static constexpr int FM = BM / 16, FN = 4;
+  static constexpr int AS_BYTES = BM * 16, BS_BYTES = BN * 16;   // LDS per chunk of scales
+  static constexpr int OUT_BYTES = 16 * BN * 4;         // 16 output rows
+  static constexpr int RING = 2 * A_BYTES > 2 * OUT_BYTES ? 2 * A_BYTES : 2 * OUT_BYTES;
+  static constexpr int DMAS = A_BYTES / 1024 / WAVES;   // per wavefront and step
   static constexpr int kBlockE = 4;                     // entries per tile-order block
 };
 
 template <bool GATHER>
 __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
   typedef MxTile T;
-  __shared__ __align__(1024) char smem[2 * T::A_BYTES + 2 * T::S_BYTES];
+  constexpr int FM = T::FM;
+  __shared__ __align__(1024) char smem[T::RING + 2 * T::AS_BYTES + 2 * T::BS_BYTES];
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lds0 = lds_addr(smem);
-  const char* s_scale = smem + 2 * T::A_BYTES;
+  const char* s_scale = smem + T::RING;
   const int NT = (a.Hp + T::BN - 1) / T::BN;
   const int nent = *a.ntiles;
-  const int64_t total = int64_t(nent) * NT;
+  const int total = nent * NT;      // below 2^31 (host)
   const int G = gridDim.x;
   // The workgroups of one XCD take a contiguous run of tiles per round, first come first
   // served (queue position q of XCD x is tile (q / per) * G + x * per + q % per), so that the
@@ -236,35 +240,33 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
   // -> 5.05 ms at H = 7168, H' = 2048 against the same order taken statically.
   __shared__ int s_claim;
   const int xcd = blockIdx.x % 8, per = G / 8;
-  auto claim = [&]() {
-    const int q = atomicAdd(a.qcnt + xcd, 1);
-    s_claim = (q / per) * G + xcd * per + q % per;
-  };
+  int q = 0;      // thread 0: its claim
+  auto claim = [&]() { if (threadIdx.x == 0) q = atomicAdd(a.qcnt + xcd, 1); };
+  auto publish = [&]() { if (threadIdx.x == 0) s_claim = (q / per) * G + xcd * per + q % per; };
   auto next = [&]() { return __builtin_amdgcn_readfirstlane(s_claim); };
-  if (threadIdx.x == 0) claim();
+  claim();
+  publish();
   __syncthreads();
   const int nsteps = (a.KT + 1) / 2;
   const uint32_t qrow = uint32_t(a.KT) * 64, srow = uint32_t(a.KC) * 16;   // bytes per A row
   const int r16 = lane & 15, kb = lane >> 4;
 
-  for (int64_t tau = next(); tau < total; tau = next()) {
+  for (int tau = next(); tau < total; tau = next()) {
     // blocks of kBlockE entries x all N-tiles, entries fastest
-    const int64_t eb = tau / (int64_t(T::kBlockE) * NT);
-    const int j = int(tau % (int64_t(T::kBlockE) * NT));
-    const int ge = int(min(int64_t(T::kBlockE), nent - eb * T::kBlockE));
-    const int ent = int(eb) * T::kBlockE + j % ge;
+    const int eb = tau / (T::kBlockE * NT), j = tau % (T::kBlockE * NT);
+    const int ge = min(T::kBlockE, nent - eb * T::kBlockE);
     const int n0 = j / ge * T::BN;
-    const TileEntry e = a.tiles[ent];
+    const TileEntry e = a.tiles[eb * T::kBlockE + j % ge];
     const int rowbase = __builtin_amdgcn_readfirstlane(e.rowbase + e.m0);
     const int wrow = __builtin_amdgcn_readfirstlane(e.wrow);
     const int rows_valid = __builtin_amdgcn_readfirstlane(min(T::BM, e.n - e.m0));
     const int col0 = n0 + wid * 64;
     const bool idle = col0 >= a.Hp;    // uniform
 
-    // this lane's rows of A: 4 DMAs of 8 rows a wavefront, and one row of scales
-    uint32_t va[4], vs = kOffNone;
+    // this lane's rows of A (DMAS times 8 rows a wavefront) and its row of scales
+    uint32_t va[T::DMAS], vs = kOffNone;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < T::DMAS; ++j) {
       const int row = (wid + 4 * j) * 8 + (lane >> 3);
       const int c = (lane & 7) ^ swz_k(row);
       uint32_t r = kOffNone;
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
       }
       va[j] = r == kOffNone ? kOffNone : r * qrow + c * 16;
     }
-    if (wid < 2) {
+    if (wid < T::BM / 64) {
       const int row = wid * 64 + lane;
       uint32_t r = kOffNone;
       if (row < rows_valid) {
@@ -297,14 +299,17 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
     const __amdgpu_buffer_rsrc_t brs = make_rsrc(a.wq + tile16 * a.KT * 1024, uint32_t(4 * a.KT) * 1024);
     const __amdgpu_buffer_rsrc_t bss = make_rsrc(a.ws + tile16 * a.KC * 256, uint32_t(4 * a.KC) * 256);
 
+    const uint32_t vbs = (lane >> 4) * uint32_t(a.KC) * 256 + (lane & 15) * 16;
     auto issue_a = [&](int k) {     // step k into stage k % 2
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < T::DMAS; ++j)
         dma16(ars, va[j], uint32_t(k) * T::STEPB, lds0 + (k & 1) * T::A_BYTES + (wid + 4 * j) * 1024);
     };
     auto issue_s = [&](int c) {     // scales of chunk c
-      if (wid < 2)
-        dma16(srs, vs, uint32_t(c) * 16, lds0 + 2 * T::A_BYTES + (c & 1) * T::S_BYTES + wid * 1024);
+      if (wid < T::BM / 64)
+        dma16(srs, vs, uint32_t(c) * 16, lds0 + T::RING + (c & 1) * T::AS_BYTES + wid * 1024);
+      dma16(bss, vbs, uint32_t(c) * 256,
+            lds0 + T::RING + 2 * T::AS_BYTES + (c & 1) * T::BS_BYTES + wid * 1024);
     };
     auto load_b = [&](int k, v4i_t (&b)[2][T::FN]) {
 #pragma unroll
@@ -312,62 +317,62 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
 #pragma unroll
         for (int j = 0; j < T::FN; ++j)
           b[t][j] = __builtin_bit_cast(v4i_t, __builtin_amdgcn_raw_buffer_load_b128(
-              brs, lane * 16, (j * a.KT + 2 * k + t) * 1024, 0));
+              brs, 2 * k + t < a.KT ? lane * 16 : int(kOffNone), (j * a.KT + 2 * k + t) * 1024, 0));
     };
-    auto load_bs = [&](int c, int (&s)[T::FN]) {
+    v4f_t acc[FM][T::FN];
 #pragma unroll
-      for (int j = 0; j < T::FN; ++j)
-        s[j] = __builtin_amdgcn_raw_buffer_load_b32(bss, lane * 4, (j * a.KC + c) * 256, 0);
-    };
-    v4f_t acc[T::FM][T::FN];
-#pragma unroll
-    for (int i = 0; i < T::FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) acc[i][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
     v4i_t b0[2][T::FN], b1[2][T::FN];
-    int bs0[T::FN], as[T::FM], bsn[T::FN];
+    int bs[T::FN], as[FM];
 
     __syncthreads();     // every wavefront has read the previous tile's last stage and its claim
-    if (threadIdx.x == 0) claim();   // read after the k-loop's barriers
     issue_a(0);
     issue_s(0);
-    if (!idle) {
-      load_b(0, b0);
-      load_bs(0, bsn);
-    }
-    // the MFMAs of step k: fragments of 16 rows from LDS, both k-tiles of the step
+    if (!idle) load_b(0, b0);
+    claim();             // the next tile, published at the first step
+    // The MFMAs of step k: 2 * FM fragments of 16 rows (both k-tiles), each read from LDS
+    // while the MFMAs of the one before it run.
     auto compute = [&](int k, const v4i_t (&b)[2][T::FN], auto odd_c) {
       constexpr int O = decltype(odd_c)::value * 2;
       const char* st = smem + (k & 1) * T::A_BYTES;
+      v4i_t f[2];
+      auto read = [&](int n) {
+        const int row = (n % FM) * 16 + r16;
+        f[n & 1] = *reinterpret_cast<const v4i_t*>(
+            st + row * T::STEPB + (((n / FM * 4 + kb) ^ swz_k(row)) << 4));
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+      };
+      read(0);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t == 1 && 2 * k + 1 >= a.KT) break;   // the last step of an odd number of k-tiles
+      for (int n = 0; n < 2 * FM; ++n) {
+        if (n + 1 < 2 * FM) read(n + 1);
+        const int t = n / FM, i = n % FM;
+        const v8i_t fa = {f[n & 1][0], f[n & 1][1], f[n & 1][2], f[n & 1][3], 0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i) {
-          const int row = i * 16 + r16;
-          const v4i_t x = *reinterpret_cast<const v4i_t*>(
-              st + row * T::STEPB + (((t * 4 + kb) ^ swz_k(row)) << 4));
-          const v8i_t fa = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < T::FN; ++j) {
-            const v8i_t fb = {b[t][j][0], b[t][j][1], b[t][j][2], b[t][j][3], 0, 0, 0, 0};
-            // operands swapped: the block is transposed, a lane holds 4 columns of one row
-            if (t == 0) acc[i][j] = mfma_e2m1<O>(fb, fa, acc[i][j], bs0[j], as[i]);
-            else acc[i][j] = mfma_e2m1<O + 1>(fb, fa, acc[i][j], bs0[j], as[i]);
-          }
+        for (int j = 0; j < T::FN; ++j) {
+          const v8i_t fb = {b[t][j][0], b[t][j][1], b[t][j][2], b[t][j][3], 0, 0, 0, 0};
+          // operands swapped: the block is transposed, a lane holds 4 columns of one row
+          if (t == 0) acc[i][j] = mfma_e2m1<O>(fb, fa, acc[i][j], bs[j], as[i]);
+          else acc[i][j] = mfma_e2m1<O + 1>(fb, fa, acc[i][j], bs[j], as[i]);
         }
+        __builtin_amdgcn_sched_group_barrier(0x008, T::FN, 0);   // its MFMAs
       }
     };
     for (int k = 0; k < nsteps; k += 2) {
       wait_vm<0>();
+      if (k == 0) publish();
       __syncthreads();
       if (k + 1 < nsteps) issue_a(k + 1);
       if (!idle) {
 #pragma unroll
-        for (int j = 0; j < T::FN; ++j) bs0[j] = bsn[j];
+        for (int j = 0; j < T::FN; ++j)
+          bs[j] = *reinterpret_cast<const int*>(s_scale + 2 * T::AS_BYTES + ((k / 2) & 1) * T::BS_BYTES +
+                                                 (wid * 4 + j) * 256 + lane * 4);
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i)
-          as[i] = *reinterpret_cast<const int*>(s_scale + ((k / 2) & 1) * T::S_BYTES +
+        for (int i = 0; i < FM; ++i)
+          as[i] = *reinterpret_cast<const int*>(s_scale + ((k / 2) & 1) * T::AS_BYTES +
                                                 (i * 16 + r16) * 16 + kb * 4);
         if (k + 1 < nsteps) load_b(k + 1, b1);
         compute(k, b0, std::integral_constant<int, 0>());
@@ -380,24 +385,37 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
           issue_s(k / 2 + 1);
         }
         if (!idle) {
-          if (k + 2 < nsteps) {
-            load_b(k + 2, b0);
-            load_bs(k / 2 + 1, bsn);
-          }
+          if (k + 2 < nsteps) load_b(k + 2, b0);
           compute(k + 1, b1, std::integral_constant<int, 1>());
         }
       }
     }
-    if (idle) continue;
-    const __amdgpu_buffer_rsrc_t crs = make_rsrc(a.c + int64_t(rowbase) * a.Hp,
-                                                 clamp_bytes(int64_t(rows_valid) * a.Hp * 4));
+    // Epilogue: a store of the lanes' own 16 x 16 block covers 16 rows of 64 bytes, which the
+    // memory side takes at a third of the rate of whole rows (11000 cycles per tile against
+    // 3800); so the four wavefronts exchange 16 rows at a time through the ring and each
+    // stores 4 whole rows of the tile, 1 KiB per instruction: 2.34 -> 2.01 ms at 524288
+    // slots, H = 4096, H' = 1536, 4.99 -> 4.63 ms at H = 7168, H' = 2048.
+    const __amdgpu_buffer_rsrc_t crs = make_rsrc(a.c + int64_t(rowbase) * a.Hp + n0,
+                                                 clamp_bytes((int64_t(rows_valid) * a.Hp - n0) * 4));
+    const uint32_t lcol = n0 + lane * 4 < a.Hp ? uint32_t(lane) * 16 : kOffNone;
+    __syncthreads();     // every wavefront has read the last stage
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i)
+    for (int i = 0; i < FM; ++i) {
+      char* buf = smem + (i & 1) * T::OUT_BYTES;    // 16 rows of 1 KiB, chunks swizzled by row
+      if (!idle) {
 #pragma unroll
-      for (int j = 0; j < T::FN; ++j)
-        __builtin_amdgcn_raw_buffer_store_b128(
-            __builtin_bit_cast(v4i_t, acc[i][j]), crs,
-            (uint32_t(i * 16 + r16) * a.Hp + col0 + j * 16 + 4 * kb) * 4, 0, kNonTemporal);
+        for (int j = 0; j < T::FN; ++j)
+          *reinterpret_cast<v4f_t*>(buf + r16 * 1024 + (((wid * 16 + j * 4 + kb) ^ r16) << 4)) = acc[i][j];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int row = wid * 4 + h;
+        const v4f_t x = *reinterpret_cast<const v4f_t*>(buf + row * 1024 + ((lane ^ row) << 4));
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i_t, x), crs,
+                                               lcol + uint32_t(i * 16 + row) * a.Hp * 4, 0, kNonTemporal);
+      }
+    }
   }
 }
 
@@ -483,11 +501,14 @@ extern "C" int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* 
            int(k_tiles(s.H)), int(k_chunks(s.H)), int64_t(s.R) * s.S * s.K,
            int64_t(s.R) * s.S * (src_index ? 1 : s.K),
            ws_ptr<int32_t>(ws, ws_layout(s).flags) + kFlagQueue};
+  const int64_t nt = (s.Hp + MxTile::BN - 1) / MxTile::BN;
   const bool tiled = cus % 4 == 0 && a.NK >= 16 * int64_t(s.E) &&
-                     (!src_index || a.xrows * a.KT * 64 < int64_t(kOffNone));
+                     (!src_index || a.xrows * a.KT * 64 < int64_t(kOffNone)) &&
+                     (a.NK / 64 + int64_t(s.R) * (s.E + s.B)) * nt < INT32_MAX;
   st = launch_tile_list(s, cu_seqlens, tiled ? MxTile::BM : kMxRows, ws, strm, &a.tiles, &a.ntiles);
   if (st) return st;
   if (tiled) {
+    // two workgroups per CU: one's stores and waits run under the other's products
     if (src_index) mx_gemm_tiled_kernel<true><<<cus * 2, 256, 0, strm>>>(a);
     else mx_gemm_tiled_kernel<false><<<cus * 2, 256, 0, strm>>>(a);
     return launch_status();
