@@ -145,63 +145,95 @@ struct MxArgs {
   int32_t* qcnt;    // 8 per-XCD tile-queue counters, zero at launch
 };
 
+// One 16 x 16 x 128 product of e2m1 operands (format 4); byte BYTE of each scale word counts.
+template <int BYTE>
+__device__ inline v4f_t mfma_e2m1(v8i_t a, v8i_t b, v4f_t c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, BYTE, sa, BYTE, sb);
+}
+
+// ---- few rows per expert: the call is bound by reading each touched expert's weights once.
+// One workgroup per (entry of at most 64 rows, 64 columns). Its four wavefronts take the
+// entry's blocks of 16 rows; where there are fewer than three, the wavefronts of a block
+// share its k-chunks in turn and their sums are added in the wavefronts' order. Operands go
+// straight to registers, a chunk (512 k, 17 KiB of weights) in flight per wavefront.
 constexpr int kMxRows = 64;   // rows of a work entry
 
-// One workgroup per (entry, 64 columns): wavefront w multiplies 16 rows with 64 columns,
-// operands straight from memory.
 __global__ __launch_bounds__(256) void mx_gemm_kernel(MxArgs a) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  __shared__ __align__(16) v4f_t s_part[3][4][64];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kb = lane >> 4, r16 = lane & 15;
   const int NT = a.Hp / 64;
   const int64_t total = int64_t(*a.ntiles) * NT;
   for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
     const TileEntry te = a.tiles[t / NT];
     const int n0 = int(t % NT) * 64;
-    const int r0 = te.m0 + w * 16;
-    if (r0 >= te.n) continue;
-    int64_t arow = int64_t(te.rowbase) + r0 + (lane & 15);
-    bool in = r0 + (lane & 15) < te.n;
-    if (a.src_index) {
-      const int u = in ? a.src_index[arow] : -1;
-      in = u >= 0 && u < a.NK;
-      arow = in ? u / a.K : 0;
-    }
+    const int rows = __builtin_amdgcn_readfirstlane(min(kMxRows, te.n - te.m0));
+    const int split = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;   // wavefronts per block of rows
+    const int part = w % split, r0 = w / split * 16;
+    const bool work = r0 < rows;    // uniform
     v4f_t acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = v4f_t{0.f, 0.f, 0.f, 0.f};
-    const int kb = lane >> 4;
-    for (int kt = 0; kt < a.KT; ++kt) {
-      v8i_t fa = {0, 0, 0, 0, 0, 0, 0, 0};
-      int sa = 0;
-      if (in) {
-        const v4i_t x = *reinterpret_cast<const v4i_t*>(a.xq + (arow * a.KT + kt) * 64 + kb * 16);
-        fa[0] = x[0]; fa[1] = x[1]; fa[2] = x[2]; fa[3] = x[3];
-        sa = a.xs[(arow * a.KC + kt / 4) * 16 + kb * 4 + kt % 4];
+    if (work) {
+      int64_t arow = int64_t(te.rowbase) + te.m0 + r0 + r16;
+      bool in = r0 + r16 < rows;
+      if (a.src_index) {
+        const int u = in ? a.src_index[arow] : -1;
+        in = u >= 0 && u < a.NK;
+        arow = in ? u / a.K : 0;
       }
+      const v4i_t* xq = reinterpret_cast<const v4i_t*>(a.xq) + arow * a.KT * 4 + kb;
+      const int* xs = reinterpret_cast<const int*>(a.xs) + arow * a.KC * 4 + kb;
+      const int64_t tile = int64_t(te.wrow) * (a.Hp / 16) + n0 / 16;
+      const v4i_t* wq = reinterpret_cast<const v4i_t*>(a.wq) + tile * a.KT * 64 + lane;
+      const int* ws = reinterpret_cast<const int*>(a.ws) + tile * a.KC * 64 + lane;
+      for (int c = part; c < a.KC; c += split) {
+        v4i_t fa[4], fb[4][4];
+        int sb[4];
+        const int sa = in ? xs[c * 4] : 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t tile = int64_t(te.wrow) * (a.Hp / 16) + n0 / 16 + j;
-        const v4i_t x = reinterpret_cast<const v4i_t*>(a.wq)[(tile * a.KT + kt) * 64 + lane];
-        const v8i_t fb = {x[0], x[1], x[2], x[3], 0, 0, 0, 0};
-        const int sb = a.ws[((tile * a.KC + kt / 4) * 64 + lane) * 4 + kt % 4];
-        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa, fb, acc[j], 4, 4, 0, sa, 0, sb);
+        for (int j = 0; j < 4; ++j) sb[j] = ws[(j * a.KC + c) * 64];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool there = c * 4 + k < a.KT;   // uniform
+          fa[k] = there && in ? xq[(c * 4 + k) * 4] : v4i_t{0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            fb[k][j] = there ? wq[(j * a.KT + c * 4 + k) * 64] : v4i_t{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const v8i_t xa = {fa[k][0], fa[k][1], fa[k][2], fa[k][3], 0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const v8i_t xb = {fb[k][j][0], fb[k][j][1], fb[k][j][2], fb[k][j][3], 0, 0, 0, 0};
+            // operands swapped: a lane holds 4 columns of one row
+            if (k == 0) acc[j] = mfma_e2m1<0>(xb, xa, acc[j], sb[j], sa);
+            else if (k == 1) acc[j] = mfma_e2m1<1>(xb, xa, acc[j], sb[j], sa);
+            else if (k == 2) acc[j] = mfma_e2m1<2>(xb, xa, acc[j], sb[j], sa);
+            else acc[j] = mfma_e2m1<3>(xb, xa, acc[j], sb[j], sa);
+          }
+        }
       }
     }
-    // lane holds column lane % 16 and rows 4 * (lane / 16) + r of each block
+    if (split > 1) {       // uniform
+      if (part > 0)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = r0 + 4 * (lane >> 4) + r;
-      if (row >= te.n) continue;
+        for (int j = 0; j < 4; ++j) s_part[w - 1][j][lane] = acc[j];
+      __syncthreads();
+      if (part == 0)
+        for (int o = 1; o < split; ++o)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        a.c[(int64_t(te.rowbase) + row) * a.Hp + n0 + j * 16 + (lane & 15)] = acc[j][r];
+          for (int j = 0; j < 4; ++j) acc[j] += s_part[w + o - 1][j][lane];
+      __syncthreads();     // read before the next entry's sums
+    }
+    if (work && part == 0 && r0 + r16 < rows) {
+      float* c = a.c + (int64_t(te.rowbase) + te.m0 + r0 + r16) * a.Hp + n0 + 4 * kb;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<v4f_t*>(c + j * 16) = acc[j];
     }
   }
-}
-
-// One 16 x 16 x 128 product of e2m1 operands (format 4); byte BYTE of each scale word counts.
-template <int BYTE>
-__device__ inline v4f_t mfma_e2m1(v8i_t a, v8i_t b, v4f_t c, int sa, int sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, BYTE, sa, BYTE, sb);
 }
 
 constexpr int kNonTemporal = 2;   // buffer cache policy: the output is not read back here
@@ -247,50 +279,49 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
   claim();
   publish();
   __syncthreads();
+  __shared__ uint32_t s_row[T::DMAS + 1][T::WAVES * 64];
   const int nsteps = (a.KT + 1) / 2;
   const uint32_t qrow = uint32_t(a.KT) * 64, srow = uint32_t(a.KC) * 16;   // bytes per A row
   const int r16 = lane & 15, kb = lane >> 4;
 
-  for (int tau = next(); tau < total; tau = next()) {
+  // A tile's place, and in s_row the byte offsets behind this lane's rows of A (DMAS times 8
+  // rows a wavefront, then the row of scales): worked out for the next tile before a tile's
+  // epilogue, so that the loads they hang on run under other wavefronts' work.
+  int rowbase = 0, wrow = 0, rows_valid = 0, n0 = 0;
+  auto place = [&](int tau) {
     // blocks of kBlockE entries x all N-tiles, entries fastest
     const int eb = tau / (T::kBlockE * NT), j = tau % (T::kBlockE * NT);
     const int ge = min(T::kBlockE, nent - eb * T::kBlockE);
-    const int n0 = j / ge * T::BN;
     const TileEntry e = a.tiles[eb * T::kBlockE + j % ge];
-    const int rowbase = __builtin_amdgcn_readfirstlane(e.rowbase + e.m0);
-    const int wrow = __builtin_amdgcn_readfirstlane(e.wrow);
-    const int rows_valid = __builtin_amdgcn_readfirstlane(min(T::BM, e.n - e.m0));
+    n0 = j / ge * T::BN;
+    rowbase = __builtin_amdgcn_readfirstlane(e.rowbase + e.m0);
+    wrow = __builtin_amdgcn_readfirstlane(e.wrow);
+    rows_valid = __builtin_amdgcn_readfirstlane(min(T::BM, e.n - e.m0));
+    int u[T::DMAS + 1];
+#pragma unroll
+    for (int i = 0; i <= T::DMAS; ++i) {
+      const int row = i < T::DMAS ? (wid + 4 * i) * 8 + (lane >> 3) : (wid & 1) * 64 + lane;
+      u[i] = row < rows_valid ? (GATHER ? a.src_index[rowbase + row] : row) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i <= T::DMAS; ++i) {
+      uint32_t off = kOffNone;
+      if (u[i] >= 0 && (!GATHER || u[i] < a.NK)) {
+        const uint32_t r = GATHER ? uint32_t(u[i]) / uint32_t(a.K) : uint32_t(u[i]);
+        off = i < T::DMAS ? r * qrow + ((lane & 7) ^ swz_k((wid + 4 * i) * 8 + (lane >> 3))) * 16 : r * srow;
+      }
+      s_row[i][threadIdx.x] = off;
+    }
+  };
+  int tau = next();
+  if (tau < total) place(tau);
+  while (tau < total) {
     const int col0 = n0 + wid * 64;
     const bool idle = col0 >= a.Hp;    // uniform
-
-    // this lane's rows of A (DMAS times 8 rows a wavefront) and its row of scales
-    uint32_t va[T::DMAS], vs = kOffNone;
+    uint32_t va[T::DMAS];
 #pragma unroll
-    for (int j = 0; j < T::DMAS; ++j) {
-      const int row = (wid + 4 * j) * 8 + (lane >> 3);
-      const int c = (lane & 7) ^ swz_k(row);
-      uint32_t r = kOffNone;
-      if (row < rows_valid) {
-        r = row;
-        if (GATHER) {
-          const int u = a.src_index[rowbase + row];
-          r = u >= 0 && u < a.NK ? uint32_t(u) / uint32_t(a.K) : kOffNone;
-        }
-      }
-      va[j] = r == kOffNone ? kOffNone : r * qrow + c * 16;
-    }
-    if (wid < T::BM / 64) {
-      const int row = wid * 64 + lane;
-      uint32_t r = kOffNone;
-      if (row < rows_valid) {
-        r = row;
-        if (GATHER) {
-          const int u = a.src_index[rowbase + row];
-          r = u >= 0 && u < a.NK ? uint32_t(u) / uint32_t(a.K) : kOffNone;
-        }
-      }
-      vs = r == kOffNone ? kOffNone : r * srow;
-    }
+    for (int i = 0; i < T::DMAS; ++i) va[i] = s_row[i][threadIdx.x];
+    const uint32_t vs = s_row[T::DMAS][threadIdx.x];
     const int64_t first = GATHER ? 0 : rowbase;
     const int64_t span = GATHER ? a.xrows : rows_valid;
     const __amdgpu_buffer_rsrc_t ars = make_rsrc(a.xq + first * qrow, clamp_bytes(span * qrow));
@@ -398,6 +429,8 @@ __global__ __launch_bounds__(256, 2) void mx_gemm_tiled_kernel(MxArgs a) {
     const __amdgpu_buffer_rsrc_t crs = make_rsrc(a.c + int64_t(rowbase) * a.Hp + n0,
                                                  clamp_bytes((int64_t(rows_valid) * a.Hp - n0) * 4));
     const uint32_t lcol = n0 + lane * 4 < a.Hp ? uint32_t(lane) * 16 : kOffNone;
+    tau = next();
+    if (tau < total) place(tau);
     __syncthreads();     // every wavefront has read the last stage
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -501,10 +534,20 @@ extern "C" int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* 
            int(k_tiles(s.H)), int(k_chunks(s.H)), int64_t(s.R) * s.S * s.K,
            int64_t(s.R) * s.S * (src_index ? 1 : s.K),
            ws_ptr<int32_t>(ws, ws_layout(s).flags) + kFlagQueue};
+  // The tiled form reads each weight once per 128 rows, the other once per 64 (and per block
+  // of 16 rows from the CU's cache), but needs the card full of tiles. Measured on both
+  // sides, tiled / few rows, us (H, H', E; slots): 4096, 1536, 256: 66000 slots and more 5x
+  // faster; 2048: 161 / 166, 512: 152 / 136, 128: 95 / 66. 7168, 2048, 64: 1024: 106 / 118,
+  // 512: 106 / 104. 1024, 512, 64: 16384 (320 tiles): 34 / 39, 8192 (192 tiles): 33 / 28.
+  // 512, 512, 16: 16384 (272 tiles): 33 / 31. So: at least 8 slots per weight row, and a tile
+  // for every CU, counting half a tile of padding per weight row.
   const int64_t nt = (s.Hp + MxTile::BN - 1) / MxTile::BN;
-  const bool tiled = cus % 4 == 0 && a.NK >= 16 * int64_t(s.E) &&
+  const int64_t held = int64_t(s.E) + s.R;      // a plan has at most this many segments
+  const bool tiled = cus % 4 == 0 && a.NK >= 8 * held &&
+                     (a.NK + MxTile::BM / 2 * held) / MxTile::BM * nt >= cus &&
+                     // 32-bit offsets of gathered rows and tile numbers
                      (!src_index || a.xrows * a.KT * 64 < int64_t(kOffNone)) &&
-                     (a.NK / 64 + int64_t(s.R) * (s.E + s.B)) * nt < INT32_MAX;
+                     (a.NK / MxTile::BM + int64_t(s.R) * (s.E + s.B)) * nt < INT32_MAX;
   st = launch_tile_list(s, cu_seqlens, tiled ? MxTile::BM : kMxRows, ws, strm, &a.tiles, &a.ntiles);
   if (st) return st;
   if (tiled) {
