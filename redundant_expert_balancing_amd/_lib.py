@@ -330,6 +330,8 @@ def _device() -> int:
     if _torch is None:
         import torch
         _torch = torch
+    if _torch.cuda.is_initialized():
+        return _torch._C._cuda_getDevice()
     return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
 
 
@@ -452,9 +454,9 @@ def moonep_swiglu_checkpoint(shape, h, act, q, scales, stream=None):
         raise MoonepError("moonep_swiglu_checkpoint", st)
 
 
-def _ws(shape, ws, d):
-    """(address, bytes) of a workspace."""
-    return _q(ws, lib().moonep_workspace_bytes(shape), "ws", None, d), ws.nbytes
+def _ws(ws, d):
+    """(address, bytes) of a workspace, whose size the library checks."""
+    return _q(ws, 0, "ws", None, d), ws.nbytes
 
 
 def moonep_grouped_gemm_swiglu_checkpoint(shape, xp, w1_all, cu_seqlens, act, q, scales, ws,
@@ -467,7 +469,7 @@ def moonep_grouped_gemm_swiglu_checkpoint(shape, xp, w1_all, cu_seqlens, act, q,
         _q(w1_all, (shape.E + shape.R * shape.B) * H * 2 * Hp * eb, "w1_all", at, d),
         _q(cu_seqlens, 4 * shape.R * (shape.E + shape.B + 1), "cu_seqlens", _torch.int32, d),
         _q(act, NK * Hp * eb, "act", at, d), *_checkpoint_h(shape, q, scales, d),
-        *_ws(shape, ws, d), _h(stream, d))
+        *_ws(ws, d), _h(stream, d))
     if st:
         raise MoonepError("moonep_grouped_gemm_swiglu_checkpoint", st)
 
@@ -551,7 +553,7 @@ def moonep_mx_grouped_gemm(shape, xq, xscales, src_index, wq, wscales, cu_seqlen
         shape, _q(xq, rows * qb, "xq", u8, d), _q(xscales, rows * sb, "xscales", u8, d),
         _q(src_index, 4 * NK, "src_index", i32, d, True), *_mx_weights(shape, wq, wscales, d),
         _q(cu_seqlens, 4 * shape.R * (shape.E + shape.B + 1), "cu_seqlens", i32, d),
-        _q(c, 4 * NK * shape.Hp, "c", _torch.float32, d), *_ws(shape, ws, d), _h(stream, d))
+        _q(c, 4 * NK * shape.Hp, "c", _torch.float32, d), *_ws(ws, d), _h(stream, d))
     if st:
         raise MoonepError("moonep_mx_grouped_gemm", st)
 

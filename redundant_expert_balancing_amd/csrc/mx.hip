@@ -151,88 +151,143 @@ __device__ inline v4f_t mfma_e2m1(v8i_t a, v8i_t b, v4f_t c, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, BYTE, sa, BYTE, sb);
 }
 
-// ---- few rows per expert: the call is bound by reading each touched expert's weights once.
-// One workgroup per (entry of at most 64 rows, 64 columns). Its four wavefronts take the
-// entry's blocks of 16 rows; where there are fewer than three, the wavefronts of a block
-// share its k-chunks in turn and their sums are added in the wavefronts' order. Operands go
-// straight to registers, a chunk (512 k, 17 KiB of weights) in flight per wavefront.
-constexpr int kMxRows = 64;   // rows of a work entry
+// ---- few rows per expert: the call is bound by reading each touched expert's weights once,
+// and, for one token, by its launches; so this form needs no list of work. Its work items
+// are (share of the rows, segment of the view, 64 columns), dealt out to the workgroups in
+// turn; a workgroup's threads look up one item's cu_seqlens each and list the ones that
+// have rows. A workgroup's four wavefronts take blocks of 16 rows; where there are fewer
+// than three, the wavefronts of a block share its k-chunks in turn and their sums are added
+// in the wavefronts' order. Operands go straight to registers, a chunk (512 k, 17 KiB of
+// weights) in flight per wavefront.
+constexpr int kMxRows = 64;      // rows at a time
+constexpr int kMxItems = 256;    // items looked up at a time
 
-__global__ __launch_bounds__(256) void mx_gemm_kernel(MxArgs a) {
-  __shared__ __align__(16) v4f_t s_part[3][4][64];
+// Rows m0 .. m0 + 63 (at most) of one segment, columns n0 .. n0 + 63, by one workgroup.
+__device__ inline void few_rows(const MxArgs& a, int rowbase_v, int wrow_v, int m0_v, int n,
+                                int n0_v, v4f_t (*s_part)[4][64]) {
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kb = lane >> 4, r16 = lane & 15;
-  const int NT = a.Hp / 64;
-  const int64_t total = int64_t(*a.ntiles) * NT;
-  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
-    const TileEntry te = a.tiles[t / NT];
-    const int n0 = int(t % NT) * 64;
-    const int rows = __builtin_amdgcn_readfirstlane(min(kMxRows, te.n - te.m0));
-    const int split = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;   // wavefronts per block of rows
-    const int part = w % split, r0 = w / split * 16;
-    const bool work = r0 < rows;    // uniform
-    v4f_t acc[4];
+  const int rowbase = __builtin_amdgcn_readfirstlane(rowbase_v);
+  const int wrow = __builtin_amdgcn_readfirstlane(wrow_v);
+  const int m0 = __builtin_amdgcn_readfirstlane(m0_v), n0 = __builtin_amdgcn_readfirstlane(n0_v);
+  const int rows = __builtin_amdgcn_readfirstlane(min(kMxRows, n - m0));
+  const int split = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;   // wavefronts per block of rows
+  const int part = w % split, r0 = w / split * 16;
+  const bool work = r0 < rows;    // uniform
+  v4f_t acc[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = v4f_t{0.f, 0.f, 0.f, 0.f};
-    if (work) {
-      int64_t arow = int64_t(te.rowbase) + te.m0 + r0 + r16;
-      bool in = r0 + r16 < rows;
-      if (a.src_index) {
-        const int u = in ? a.src_index[arow] : -1;
-        in = u >= 0 && u < a.NK;
-        arow = in ? u / a.K : 0;
+  for (int j = 0; j < 4; ++j) acc[j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+  if (work) {
+    int64_t arow = int64_t(rowbase) + m0 + r0 + r16;
+    bool in = r0 + r16 < rows;
+    if (a.src_index) {
+      const int u = in ? a.src_index[arow] : -1;
+      in = u >= 0 && u < a.NK;
+      arow = in ? u / a.K : 0;
+    }
+    const v4i_t* xq = reinterpret_cast<const v4i_t*>(a.xq) + arow * a.KT * 4 + kb;
+    const int* xs = reinterpret_cast<const int*>(a.xs) + arow * a.KC * 4 + kb;
+    const int64_t tile = int64_t(wrow) * (a.Hp / 16) + n0 / 16;
+    const v4i_t* wq = reinterpret_cast<const v4i_t*>(a.wq) + tile * a.KT * 64 + lane;
+    const int* ws = reinterpret_cast<const int*>(a.ws) + tile * a.KC * 64 + lane;
+    for (int c = part; c < a.KC; c += split) {
+      v4i_t fa[4], fb[4][4];
+      int sb[4];
+      const int sa = in ? xs[c * 4] : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sb[j] = ws[(j * a.KC + c) * 64];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool there = c * 4 + k < a.KT;   // uniform
+        fa[k] = there && in ? xq[(c * 4 + k) * 4] : v4i_t{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          fb[k][j] = there ? wq[(j * a.KT + c * 4 + k) * 64] : v4i_t{0, 0, 0, 0};
       }
-      const v4i_t* xq = reinterpret_cast<const v4i_t*>(a.xq) + arow * a.KT * 4 + kb;
-      const int* xs = reinterpret_cast<const int*>(a.xs) + arow * a.KC * 4 + kb;
-      const int64_t tile = int64_t(te.wrow) * (a.Hp / 16) + n0 / 16;
-      const v4i_t* wq = reinterpret_cast<const v4i_t*>(a.wq) + tile * a.KT * 64 + lane;
-      const int* ws = reinterpret_cast<const int*>(a.ws) + tile * a.KC * 64 + lane;
-      for (int c = part; c < a.KC; c += split) {
-        v4i_t fa[4], fb[4][4];
-        int sb[4];
-        const int sa = in ? xs[c * 4] : 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sb[j] = ws[(j * a.KC + c) * 64];
+      for (int k = 0; k < 4; ++k) {
+        const v8i_t xa = {fa[k][0], fa[k][1], fa[k][2], fa[k][3], 0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool there = c * 4 + k < a.KT;   // uniform
-          fa[k] = there && in ? xq[(c * 4 + k) * 4] : v4i_t{0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            fb[k][j] = there ? wq[(j * a.KT + c * 4 + k) * 64] : v4i_t{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const v8i_t xa = {fa[k][0], fa[k][1], fa[k][2], fa[k][3], 0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const v8i_t xb = {fb[k][j][0], fb[k][j][1], fb[k][j][2], fb[k][j][3], 0, 0, 0, 0};
-            // operands swapped: a lane holds 4 columns of one row
-            if (k == 0) acc[j] = mfma_e2m1<0>(xb, xa, acc[j], sb[j], sa);
-            else if (k == 1) acc[j] = mfma_e2m1<1>(xb, xa, acc[j], sb[j], sa);
-            else if (k == 2) acc[j] = mfma_e2m1<2>(xb, xa, acc[j], sb[j], sa);
-            else acc[j] = mfma_e2m1<3>(xb, xa, acc[j], sb[j], sa);
-          }
+        for (int j = 0; j < 4; ++j) {
+          const v8i_t xb = {fb[k][j][0], fb[k][j][1], fb[k][j][2], fb[k][j][3], 0, 0, 0, 0};
+          // operands swapped: a lane holds 4 columns of one row
+          if (k == 0) acc[j] = mfma_e2m1<0>(xb, xa, acc[j], sb[j], sa);
+          else if (k == 1) acc[j] = mfma_e2m1<1>(xb, xa, acc[j], sb[j], sa);
+          else if (k == 2) acc[j] = mfma_e2m1<2>(xb, xa, acc[j], sb[j], sa);
+          else acc[j] = mfma_e2m1<3>(xb, xa, acc[j], sb[j], sa);
         }
       }
     }
-    if (split > 1) {       // uniform
-      if (part > 0)
+  }
+  if (split > 1) {       // uniform
+    if (part > 0)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s_part[w - 1][j][lane] = acc[j];
-      __syncthreads();
-      if (part == 0)
-        for (int o = 1; o < split; ++o)
+      for (int j = 0; j < 4; ++j) s_part[w - 1][j][lane] = acc[j];
+    __syncthreads();
+    if (part == 0)
+      for (int o = 1; o < split; ++o)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] += s_part[w + o - 1][j][lane];
-      __syncthreads();     // read before the next entry's sums
+        for (int j = 0; j < 4; ++j) acc[j] += s_part[w + o - 1][j][lane];
+    __syncthreads();     // read before the next entry's sums
+  }
+  if (work && part == 0 && r0 + r16 < rows) {
+    float* c = a.c + (int64_t(rowbase) + m0 + r0 + r16) * a.Hp + n0 + 4 * kb;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<v4f_t*>(c + j * 16) = acc[j];
+  }
+}
+
+struct MxItem {
+  int32_t rowbase, wrow, m0, n;  // as TileEntry, and n0 below
+};
+
+__global__ __launch_bounds__(256) void mx_gemm_kernel(MxArgs a, const int32_t* __restrict__ cu,
+                                                      int R, int E, int B, int SK, int shares) {
+  __shared__ __align__(16) v4f_t s_part[3][4][64];
+  __shared__ MxItem s_item[kMxItems];
+  __shared__ int s_n0[kMxItems];
+  __shared__ int s_wave[4];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kb = lane >> 4, r16 = lane & 15;
+  const int NT = a.Hp / 64, EB = E + B;
+  const int64_t total = int64_t(R) * EB * shares * NT;
+  for (int64_t t0 = blockIdx.x; t0 < total; t0 += int64_t(gridDim.x) * kMxItems) {
+    const int64_t t = t0 + int64_t(threadIdx.x) * gridDim.x;
+    MxItem it{0, 0, 0, 0};
+    int n0 = 0;
+    if (t < total) {
+      // shares slowest: the empty ones of short segments lie together, over all CUs
+      const int64_t rest = t / NT;
+      const int seg = int(rest % (R * EB)), share = int(rest / (R * EB));
+      const int rank = seg / EB, i = seg % EB;
+      const int c0 = cu[int64_t(rank) * (EB + 1) + i];
+      n0 = int(t % NT) * 64;
+      it = MxItem{rank * SK + c0, i < E ? i : E + rank * B + (i - E), share * kMxRows,
+                  cu[int64_t(rank) * (EB + 1) + i + 1] - c0};
     }
-    if (work && part == 0 && r0 + r16 < rows) {
-      float* c = a.c + (int64_t(te.rowbase) + te.m0 + r0 + r16) * a.Hp + n0 + 4 * kb;
+    const bool some = it.m0 < it.n;
+    const uint64_t have = __ballot(some);
+    if (lane == 0) s_wave[w] = __popcll(have);
+    __syncthreads();
+    int at = __popcll(have & ((uint64_t(1) << lane) - 1)), count = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<v4f_t*>(c + j * 16) = acc[j];
+    for (int i = 0; i < 4; ++i) {
+      if (i < w) at += s_wave[i];
+      count += s_wave[i];
     }
+    if (some) {
+      s_item[at] = it;
+      s_n0[at] = n0;
+    }
+    __syncthreads();
+    for (int i = 0; i < count; ++i) {
+      const MxItem te = s_item[i];
+      for (int m0 = te.m0; m0 < te.n; m0 += shares * kMxRows)
+        few_rows(a, te.rowbase, te.wrow, m0, te.n, s_n0[i], s_part);
+    }
+    __syncthreads();     // the list is read before the next one
   }
 }
 
@@ -548,14 +603,17 @@ extern "C" int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* 
                      // 32-bit offsets of gathered rows and tile numbers
                      (!src_index || a.xrows * a.KT * 64 < int64_t(kOffNone)) &&
                      (a.NK / MxTile::BM + int64_t(s.R) * (s.E + s.B)) * nt < INT32_MAX;
-  st = launch_tile_list(s, cu_seqlens, tiled ? MxTile::BM : kMxRows, ws, strm, &a.tiles, &a.ntiles);
-  if (st) return st;
   if (tiled) {
+    st = launch_tile_list(s, cu_seqlens, MxTile::BM, ws, strm, &a.tiles, &a.ntiles);
+    if (st) return st;
     // two workgroups per CU: one's stores and waits run under the other's products
     if (src_index) mx_gemm_tiled_kernel<true><<<cus * 2, 256, 0, strm>>>(a);
     else mx_gemm_tiled_kernel<false><<<cus * 2, 256, 0, strm>>>(a);
     return launch_status();
   }
-  mx_gemm_kernel<<<cus * 8, 256, 0, strm>>>(a);
+  // a segment's rows are shared out twice as finely as an even plan would need
+  const int64_t share = (2 * a.NK + held * kMxRows - 1) / (held * kMxRows);
+  const int shares = int(share < 64 ? share : 64);
+  mx_gemm_kernel<<<cus * 8, 256, 0, strm>>>(a, cu_seqlens, s.R, s.E, s.B, s.S * s.K, shares);
   return launch_status();
 }
