@@ -231,6 +231,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
 // +inf, or with more than 16 experts in question, are done again by route_token.
 constexpr int kPackK = 8;
 constexpr int kTokens = 4;           // per wavefront
+// Tokens per launch of the packed forms, which do not loop (a loop's invariants took 40
+// registers): a launch holds at most 2^32 threads.
+constexpr int kLaunchTokens = 1 << 26;
 constexpr uint32_t kIdMask = 1023;
 constexpr uint32_t kNearMax = 4096;  // a wider band of doubt sends the token to route_token
 constexpr float kQMax = 4186000.f;   // fixed-point range: keys 1 .. below 2^22 - kNearMax, masked 0
@@ -693,6 +696,20 @@ static void launch_packed(const RouteArgs& a, int grid, hipStream_t strm) {
   else route_packed_kernel<EPL, false, false><<<grid, threads, 0, strm>>>(a);
 }
 
+static void launch_packed_any(const RouteArgs& a, hipStream_t strm) {
+  const int grid = (a.N + kRouteWaves * kTokens - 1) / (kRouteWaves * kTokens);
+  switch (a.epl) {
+    case 4: launch_packed<4>(a, grid, strm); break;
+    case 8: launch_packed<8>(a, grid, strm); break;
+    case 12: launch_packed<12>(a, grid, strm); break;
+    case 16: launch_packed<16>(a, grid, strm); break;
+    case 20: launch_packed<20>(a, grid, strm); break;
+    case 24: launch_packed<24>(a, grid, strm); break;
+    case 28: launch_packed<28>(a, grid, strm); break;
+    default: launch_packed<32>(a, grid, strm); break;
+  }
+}
+
 struct RouteBackwardArgs {
   const void* logits;
   const float* bias;
@@ -882,6 +899,16 @@ static void launch_backward_packed(const RouteBackwardArgs& a, int grid, hipStre
     route_backward_packed_kernel<EPL, false><<<grid, kRouteWaves * 64, 0, strm>>>(a);
 }
 
+static void launch_backward_any(const RouteBackwardArgs& a, hipStream_t strm) {
+  const int grid = (a.N + kRouteWaves * kTokens - 1) / (kRouteWaves * kTokens);
+  const int epl = (a.E + 63) / 64 * 4;
+  if (epl <= 4) launch_backward_packed<4>(a, grid, strm);
+  else if (epl <= 8) launch_backward_packed<8>(a, grid, strm);
+  else if (epl <= 16) launch_backward_packed<16>(a, grid, strm);
+  else if (epl <= 24) launch_backward_packed<24>(a, grid, strm);
+  else launch_backward_packed<32>(a, grid, strm);
+}
+
 static int check_router(const moonep_shape& s, const moonep_router* r) {
   if (!r) return MOONEP_EINVAL;
   if (r->score != MOONEP_SOFTMAX && r->score != MOONEP_SIGMOID) return MOONEP_EINVAL;
@@ -922,20 +949,17 @@ extern "C" int moonep_route(const moonep_shape* shape, const moonep_router* rout
   // are any, are whole runs of 1, 2, 4 or 8 lanes
   const bool runs = a.groups == 1 || (a.groups <= 16 && 16 % a.groups == 0 && s.E == 16 * a.epl);
   if (s.K <= kPackK && s.E <= 512 && runs) {
-    const int64_t blocks = (int64_t(N) + kRouteWaves * kTokens - 1) / (kRouteWaves * kTokens);
-    const int grid = int(blocks);   // N < 2^31: below 2^27
-    hipStream_t strm = as_stream(stream);
-    switch (a.epl) {
-      case 4: launch_packed<4>(a, grid, strm); break;
-      case 8: launch_packed<8>(a, grid, strm); break;
-      case 12: launch_packed<12>(a, grid, strm); break;
-      case 16: launch_packed<16>(a, grid, strm); break;
-      case 20: launch_packed<20>(a, grid, strm); break;
-      case 24: launch_packed<24>(a, grid, strm); break;
-      case 28: launch_packed<28>(a, grid, strm); break;
-      default: launch_packed<32>(a, grid, strm); break;
+    for (int n0 = 0; n0 < N; n0 += kLaunchTokens) {
+      RouteArgs c = a;
+      c.N = N - n0 < kLaunchTokens ? N - n0 : kLaunchTokens;
+      c.logits = static_cast<const char*>(logits) + int64_t(n0) * s.E * (a.bf16 ? 2 : 4);
+      c.ids += int64_t(n0) * s.K;
+      c.gates += int64_t(n0) * s.K;
+      launch_packed_any(c, as_stream(stream));
+      if (launch_status()) return MOONEP_EHIP;
+      if (N - n0 <= kLaunchTokens) break;     // n0 would pass 2^31
     }
-    return launch_status();
+    return MOONEP_OK;
   }
   const int64_t blocks = (int64_t(N) + kRouteWaves - 1) / kRouteWaves;
   const int grid = int(blocks < 65536 ? blocks : 65536);
@@ -962,16 +986,20 @@ extern "C" int moonep_route_backward(const moonep_shape* shape, const moonep_rou
                             router->score == MOONEP_SOFTMAX, router->renorm != 0, router->scale,
                             router->dtype == MOONEP_BF16};
   if (s.E % 4 == 0 && s.E <= 512) {
-    const int64_t blocks = (int64_t(N) + kRouteWaves * kTokens - 1) / (kRouteWaves * kTokens);
-    const int grid = int(blocks);
-    hipStream_t strm = as_stream(stream);
-    const int epl = (s.E + 63) / 64 * 4;
-    if (epl <= 4) launch_backward_packed<4>(a, grid, strm);
-    else if (epl <= 8) launch_backward_packed<8>(a, grid, strm);
-    else if (epl <= 16) launch_backward_packed<16>(a, grid, strm);
-    else if (epl <= 24) launch_backward_packed<24>(a, grid, strm);
-    else launch_backward_packed<32>(a, grid, strm);
-    return launch_status();
+    for (int n0 = 0; n0 < N; n0 += kLaunchTokens) {
+      RouteBackwardArgs c = a;
+      c.N = N - n0 < kLaunchTokens ? N - n0 : kLaunchTokens;
+      const int64_t at = int64_t(n0) * s.E * (a.bf16 ? 2 : 4), k = int64_t(n0) * s.K;
+      c.logits = static_cast<const char*>(logits) + at;
+      c.dlogits = static_cast<char*>(dlogits) + at;
+      c.ids += k;
+      c.gates += k;
+      c.dgates += k;
+      launch_backward_any(c, as_stream(stream));
+      if (launch_status()) return MOONEP_EHIP;
+      if (N - n0 <= kLaunchTokens) break;
+    }
+    return MOONEP_OK;
   }
   const int64_t blocks = (int64_t(N) + kRouteWaves - 1) / kRouteWaves;
   const int grid = int(blocks < 65536 ? blocks : 65536);

@@ -102,6 +102,102 @@ def test_odd_expert_counts(E):
                   renorm=False)
 
 
+@pytest.mark.parametrize("E,groups", [(64, 2), (64, 8), (64, 16), (128, 8), (256, 8), (384, 8),
+                                      (192, 16), (320, 4), (448, 2), (512, 16)])
+def test_groups_of_whole_lanes(E, groups):
+    """Group counts of the packed form, with both group scores, plain and biased."""
+    say("route groups", E, groups)
+    rng = np.random.default_rng(E + groups)
+    for top in {max(1, groups // 2), groups}:
+        for group_top in (1, 2):
+            for score in ("softmax", "sigmoid"):
+                for bias in (None, 0.05 * rng.standard_normal(E)):
+                    K = min(8, top * (E // groups))
+                    check(cfg_of(21, E, K), rng.standard_normal((21, E)), bias, score=score,
+                          groups=groups, top_groups=top, group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 384])
+def test_near_ties_are_settled_in_64_bits(score, E):
+    """Biased scores and group scores that float32 cannot order: pairs, runs of a dozen (the
+    refined list) and of forty (beyond it), tokens of both kinds side by side."""
+    say("route near ties", score, E)
+    rng = np.random.default_rng(E)
+    N = 23
+    for run in (2, 12, 40):
+        l = rng.standard_normal((N, E)).astype(np.float32)
+        for g in range(N):
+            if g % 3 == 2:
+                continue                       # an ordinary token between them
+            at = rng.permutation(E)[:run]
+            l[g, at] = 3.0 + 2.0 ** -22 * rng.integers(0, 3, run)
+        b = np.zeros(E, np.float32)
+        b[::3] = 2.0 ** -25                    # equal logits, biases below float32's step at 1
+        for g in (dict(), dict(groups=8, top_groups=3, group_top=2), dict(groups=4, top_groups=2)):
+            check(cfg_of(N, E, 8), l, b, score=score, **g)
+            check(cfg_of(N, E, 5), l, None, score=score, **g)
+    # groups whose best pairs differ by a step or not at all
+    l = np.tile(rng.standard_normal(E // 8).astype(np.float32), (N, 8))
+    for g in range(N):
+        l[g, rng.integers(0, E)] += np.float32(2.0 ** -20)
+    for group_top in (1, 2):
+        for b in (None, np.full(E, 0.125, np.float32)):
+            check(cfg_of(N, E, 6), l, b, score=score, groups=8, top_groups=3, group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_wide_ranges_and_masks_with_groups(score):
+    """Rows whose keys span more than the packed range resolves, and masked rows, with the
+    groups of the packed form."""
+    say("route wide", score)
+    rng = np.random.default_rng(8)
+    E, N = 128, 24
+    l = rng.standard_normal((N, E))
+    lowest = float(torch.finfo(torch.float32).min)
+    l[0] *= 1e4
+    l[1] *= 1e30
+    l[2, 3:] = lowest
+    l[3] = lowest
+    l[4, :120] = -np.inf
+    l[5] = -np.inf
+    l[6, 64:] = np.nan
+    l[7, 9] = np.inf
+    l[8, ::2] -= 200.0
+    l[9, 5:] -= 1000.0
+    l[10, :4] = 50.0
+    off = 0.1 * rng.standard_normal(E)
+    off[32:64] = -np.inf                       # a whole group switched off
+    off[70] = -np.inf
+    for renorm in (True, False):
+        for g in (dict(), dict(groups=4, top_groups=2, group_top=2), dict(groups=4, top_groups=3)):
+            for bias in (None, off):
+                for K in (8, 3):
+                    check(cfg_of(N, E, K), l, bias, score=score, renorm=renorm, **g)
+
+
+def test_more_tokens_than_one_launch():
+    """2^26 + 5 tokens: the rows behind the first launch are those of a call on them alone."""
+    N, E, K = (1 << 26) + 5, 4, 1
+    say("route many tokens", N)
+    tail = 9
+    l = torch.empty((N, E), dtype=torch.bfloat16, device="cuda")
+    l.normal_(generator=torch.Generator(device="cuda").manual_seed(0))
+    big = MoERouter(cfg_of(N, E, K), score="sigmoid", dtype="bf16", renorm=False, backward=True)
+    small = MoERouter(cfg_of(tail, E, K), score="sigmoid", dtype="bf16", renorm=False, backward=True)
+    dg = torch.ones((N, K), device="cuda")
+    big.forward(l)
+    big.backward(l, dg)
+    part = l[N - tail:].clone()
+    small.forward(part)
+    small.backward(part, dg[:tail].contiguous())
+    torch.cuda.synchronize()
+    for name in ("topk_idx", "gates", "dlogits"):
+        assert torch.equal(getattr(big, name)[N - tail:], getattr(small, name)), name
+    assert torch.equal(big.topk_idx.long(), l.argmax(1, keepdim=True)) or bool(
+        (l.gather(1, big.topk_idx.long()) == l.amax(1, keepdim=True)).all())
+
+
 def test_empty_layer():
     say("route empty")
     rt = MoERouter(cfg_of(0, 16, 2), backward=True)
