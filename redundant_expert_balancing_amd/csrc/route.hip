@@ -575,7 +575,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
       found[k] = row_max_u(v[0]);
       const bool mine = v[0] == found[k];
 #pragma unroll
-      for (int i = 0; i + k < kPackK; ++i) v[i] = mine ? (i + k + 1 < kPackK ? v[i + 1] : 0u) : v[i];
+      for (int i = 0; i + k < kPackK; ++i) v[i] = mine ? (i + 1 < kPackK ? v[i + 1] : 0u) : v[i];
     }
     lost = row_max_u(max(lost, v[0]));
     if (i16 == 0) {

@@ -118,6 +118,28 @@ def test_groups_of_whole_lanes(E, groups):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K", [(64, 8), (384, 8), (384, 5), (100, 1), (384, 16), (256, 10),
+                                 (1000, 8), (1024, 12)])
+def test_last_choice_next_to_its_neighbour(score, E, K):
+    """The K-th best and the next differ by one float32 step and have neighbouring ids, all
+    others are far from each other: the higher id is right where it is the larger."""
+    say("route last choice", score, E, K)
+    rng = np.random.default_rng(E + K)
+    N = 61
+    l = rng.uniform(-3.0, -1.0, (N, E)).astype(np.float32)
+    for g in range(N):
+        a = 2 * int(rng.integers(0, E // 2))
+        others = np.setdiff1d(np.arange(E), [a, a + 1])
+        l[g, rng.permutation(others)[:K - 1]] = 2.0 + 0.125 * np.arange(K - 1)
+        l[g, a] = 1.0
+        l[g, a + 1] = np.nextafter(np.float32(1.0), np.float32(2.0))
+        if g % 3 == 0:
+            l[g, [a, a + 1]] = l[g, [a + 1, a]]
+    for bias in (None, np.zeros(E, np.float32)):
+        check(cfg_of(N, E, K), l, bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E", [64, 384])
 def test_near_ties_are_settled_in_64_bits(score, E):
     """Biased scores and group scores that float32 cannot order: pairs, runs of a dozen (the
