@@ -117,6 +117,38 @@ def test_groups_of_whole_lanes(E, groups):
                           groups=groups, top_groups=top, group_top=group_top)
 
 
+@pytest.mark.parametrize("E,groups", [(60, 4), (60, 3), (376, 8), (75, 5), (45, 15), (112, 16),
+                                      (200, 2), (10, 5), (16, 16), (48, 3), (512, 8), (480, 15),
+                                      (340, 17), (1020, 4), (18, 2), (1024, 8), (720, 3), (600, 1)])
+def test_groups_that_do_not_fill_their_lanes(E, groups):
+    """Group sizes and counts that leave places empty behind every group, or whole lanes; rows
+    with fewer than K experts left among them, near ties, masks and NaN."""
+    say("route odd groups", E, groups)
+    rng = np.random.default_rng(E * groups)
+    per, N = E // groups, 27
+    l = rng.standard_normal((N, E))
+    l[0] = -np.inf
+    l[1, 1:] = -np.inf
+    l[2, : E // 2] = -np.inf
+    l[3, per:] = -np.inf                       # one group left
+    l[4] = float(torch.finfo(torch.float32).min)
+    l[5, E - 1] = np.nan
+    l[6, E - 1] = 1e30
+    l[7] = 1.5 + 2.0 ** -22 * rng.integers(0, 3, E)
+    l[8] = 1.5
+    l[9] *= 1e4
+    off = 0.05 * rng.standard_normal(E)
+    off[-per:] = -np.inf                       # the last group switched off
+    off[0] = -np.inf
+    for top in {1, max(1, groups // 2), groups}:
+        for group_top in {1, min(2, per)}:
+            for score in ("softmax", "sigmoid"):
+                for bias in (None, 0.05 * rng.standard_normal(E), off):
+                    for K in {min(8, top * per), min(13, top * per)}:
+                        check(cfg_of(N, E, K), l, bias, score=score, groups=groups,
+                              top_groups=top, group_top=group_top, renorm=bias is not None)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,K", [(64, 8), (384, 8), (384, 5), (100, 1), (384, 16), (256, 10),
                                  (1000, 8), (1024, 12)])
@@ -137,6 +169,27 @@ def test_last_choice_next_to_its_neighbour(score, E, K):
             l[g, [a, a + 1]] = l[g, [a + 1, a]]
     for bias in (None, np.zeros(E, np.float32)):
         check(cfg_of(N, E, K), l, bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K", [(128, 16), (384, 12), (384, 9), (1024, 16), (96, 10)])
+def test_choices_that_lie_together(score, E, K):
+    """All of the K best among consecutive ids, rows with fewer than K experts left, and
+    ordinary rows between them."""
+    say("route together", score, E, K)
+    rng = np.random.default_rng(E * K)
+    N = 31
+    l = rng.standard_normal((N, E)).astype(np.float32)
+    for g in range(0, N, 2):
+        at = int(rng.integers(0, E - K + 1))
+        l[g, at:at + K] += 20.0
+    l[1] = -np.inf
+    l[3, 5:] = -np.inf
+    l[5] = 0.5
+    for renorm in (True, False):
+        for bias in (None, 0.05 * rng.standard_normal(E)):
+            check(cfg_of(N, E, K), l, bias, score=score, renorm=renorm)
+            check(cfg_of(N, E, K), l, bias, "bf16", score=score, renorm=renorm)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
