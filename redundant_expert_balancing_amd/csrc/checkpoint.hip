@@ -123,29 +123,23 @@ __global__ __launch_bounds__(kCkThreads) void ck_quantize_kernel(const void* __r
   }
 }
 
-// One workgroup per token, as the plain dispatch: read and convert the row once, write it
-// to the K destinations.
+// Read and convert a token's row once, write it to the K destinations, whose numbers stay in
+// the CU's cache.
 template <bool BF16, int V>
 __global__ __launch_bounds__(kCkThreads) void ck_dispatch_kernel(
     const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, int width, int N, int K,
-    const int32_t* __restrict__ slot_map, void* __restrict__ dst, int64_t ndst) {
-  __shared__ int32_t s_slot[32];
+    RowSplit sp, const int32_t* __restrict__ slot_map, void* __restrict__ dst, int64_t ndst) {
   const int srow = (width + 127) / 128 * 4;
-  for (int64_t g = blockIdx.x; g < N; g += gridDim.x) {
-    if (threadIdx.x < K) {
-      const int d = slot_map[g * K + threadIdx.x];
-      s_slot[threadIdx.x] = (d >= 0 && d < ndst) ? d : -1;
-    }
-    __syncthreads();
-    for (int c = threadIdx.x * V; c < width; c += kCkThreads * V) {
+  for (int64_t g = int64_t(blockIdx.x) * sp.rows() + sp.row(); g < N;
+       g += int64_t(gridDim.x) * sp.rows()) {
+    for (int c = sp.first() * V; c < width; c += sp.step() * V) {
       float v[V];
       load_q<V>(q + g * width + c, scale_value(scales[g * srow + c / 32]), v);
       for (int k = 0; k < K; ++k) {
-        const int d = s_slot[k];
-        if (d >= 0) store_v<BF16, V>(dst, int64_t(d) * width + c, v);
+        const int d = slot_map[g * K + k];
+        if (d >= 0 && d < ndst) store_v<BF16, V>(dst, int64_t(d) * width + c, v);
       }
     }
-    __syncthreads();
   }
 }
 
@@ -296,12 +290,13 @@ extern "C" int moonep_checkpoint_dispatch(const moonep_shape* shape, int32_t wid
   if (!aligned16(q) || !aligned16(scales) || !aligned16(slot_map) || !aligned16(dst))
     return MOONEP_EINVAL;
   const int64_t ndst = int64_t(N) * s.K;
-  const int grid = ck_grid(N, 1);
+  const RowSplit sp = row_split(width / (s.dtype == MOONEP_BF16 ? 8 : 4), kCkThreads);
+  const int grid = ck_grid(N, sp.rows());
   hipStream_t strm = as_stream(stream);
   if (s.dtype == MOONEP_BF16)
-    ck_dispatch_kernel<true, 8><<<grid, kCkThreads, 0, strm>>>(q, scales, width, N, s.K, slot_map, dst, ndst);
+    ck_dispatch_kernel<true, 8><<<grid, kCkThreads, 0, strm>>>(q, scales, width, N, s.K, sp, slot_map, dst, ndst);
   else
-    ck_dispatch_kernel<false, 4><<<grid, kCkThreads, 0, strm>>>(q, scales, width, N, s.K, slot_map, dst, ndst);
+    ck_dispatch_kernel<false, 4><<<grid, kCkThreads, 0, strm>>>(q, scales, width, N, s.K, sp, slot_map, dst, ndst);
   return launch_status();
 }
 

@@ -113,8 +113,8 @@ __device__ inline float swiglu_f32(float g, float u) { return g / (1.0f + expf(-
 // + p % kSwigluBlock and its up projection kSwigluBlock further.
 constexpr int kSwigluBlock = MOONEP_SWIGLU_BLOCK;
 
-// Row-wise kernels of kRowThreads threads: rows are spread over a workgroup as 256 >> shift rows of 1 << shift threads, so that rows
-// narrower than a workgroup share one, and no thread divides.
+// Row-wise kernels of kRowThreads threads: a workgroup has 256 >> shift rows of 1 << shift
+// threads, so that rows narrower than a workgroup share one, and no thread divides.
 constexpr int kRowThreads = 256;
 struct RowSplit {
   int shift;
