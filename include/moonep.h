@@ -389,7 +389,8 @@ int moonep_gate_grad(const moonep_shape* shape, int32_t width, const float* src,
  * or 2^-10 of the scale where that is more. A block that holds an Inf or a NaN becomes NaN.
  */
 
-/* Checkpoint of token rows: src dtype [N, width], width H or Hp. */
+/* Checkpoint of token rows: src dtype [N, width], width H or Hp. As all of the checkpoint
+ * calls, for training layers only (MOONEP_EMODE). */
 int moonep_checkpoint_quantize(const moonep_shape* shape, int32_t width, const void* src,
                                uint8_t* q, uint8_t* scales, void* stream);
 

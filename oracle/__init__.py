@@ -35,4 +35,8 @@ Modules:
             the layer's rounding points; column-selective helpers for sampled
             checks at full size. The activation is a reading: the pages name
             the intermediate size H' but no activation.
+  route  -- the router's choice and gates, and the gradient of its logits. The
+            pages start at a router's top-K output; the rule is moonep.h's.
+  formats -- e4m3 and e2m1 values with power-of-two block scales: rounding,
+            checkpoints, and the packed layouts of the 4-bit experts.
 """

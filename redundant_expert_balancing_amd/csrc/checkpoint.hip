@@ -102,7 +102,8 @@ __device__ inline uint32_t quantise_v(const float* v, bool in, uint8_t* p) {
 }
 
 // One thread per V columns; a row is padded to whole groups of 128 columns, whose threads
-// past the width only write the padding scales.
+// past the width only write the padding scales. 16384 bfloat16 rows of 7168: 104 us from HBM,
+// 66 us where the rows lie in the Infinity Cache (0.36 GB at 3.4 and 5.4 TB/s).
 template <bool BF16, int V>
 __global__ __launch_bounds__(kCkThreads) void ck_quantize_kernel(const void* __restrict__ src,
                                                                  int64_t rows, int width, RowSplit sp,
@@ -124,7 +125,9 @@ __global__ __launch_bounds__(kCkThreads) void ck_quantize_kernel(const void* __r
 }
 
 // Read and convert a token's row once, write it to the K destinations, whose numbers stay in
-// the CU's cache.
+// the CU's cache. Bound by its writes: 16384 bfloat16 rows of 7168 to K = 8 places, 383 us,
+// 2.0 GB at 5.2 TB/s. Rows that do not fill a workgroup share one: 32768 rows of 32, with
+// their quantisation, 12 us against 38 with a workgroup per row; of 256, 37 against 54.
 template <bool BF16, int V>
 __global__ __launch_bounds__(kCkThreads) void ck_dispatch_kernel(
     const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, int width, int N, int K,
@@ -159,6 +162,7 @@ static Divider divider(int d) { return Divider{~uint64_t(0) / uint64_t(d) + 1, d
 // One thread per 4 intermediate columns, 8 lanes per (gate, up) block pair, rows and
 // columns in one index (a workgroup per row leaves a third of its threads idle at
 // H' = 1408, 11% slower; 8 columns per thread split each 128-byte line over two loads).
+// 262144 bfloat16 rows, H' = 1408: 832 us, 4.45 GB at 5.3 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(kCkThreads) void ck_swiglu_kernel(const float* __restrict__ h,
                                                                int64_t rows, int Hp, Divider per_row,
@@ -191,7 +195,7 @@ __global__ __launch_bounds__(kCkThreads) void ck_swiglu_kernel(const float* __re
 }
 
 // 1 << shift threads of a wavefront per row; the row's dot product is summed over them by
-// butterfly.
+// butterfly. 262144 bfloat16 rows, H' = 1408, with gates: 868-912 us, 4.46 GB at 5 TB/s.
 template <bool BF16, bool GATED>
 __global__ __launch_bounds__(kCkThreads) void ck_swiglu_backward_kernel(
     const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales,
