@@ -236,10 +236,10 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
 // groups that are too close. Tokens with a NaN or +inf, with more than 16 experts in
 // question, or with more than 8 of the best 16 in one lane, are done again by route_token.
 //
-// Bound by the vector instructions: 1083 per wavefront at E = 384 with sigmoid, bias and
-// groups (782 with softmax and no bias), so 16 wavefronts of a SIMD issue 69000 cycles of
-// the 93000 that 65536 tokens take, 39 us (softmax bf16 26 us); reading the logits alone
-// is 22 us (12). Against one float64 wavefront per token (route_kernel): 470 us (410).
+// Bound by the vector instructions: 999 per wavefront at E = 384 with sigmoid, bias and groups
+// (757 with softmax and no bias), which issue in 67000 of the 73000 cycles that a CU is busy
+// with 65536 tokens, 37 us (softmax bf16 25 us); reading the logits alone is 22 us (12).
+// Against one float64 wavefront per token (route_kernel): 470 us (410).
 // E = 376 in 8 groups, whose places lie apart: 43 us, E = 1024 in 8 groups 131 us, K = 16
 // 91 us; route_kernel 535, 1000 and 690 us.
 constexpr int kHeads = 8;            // best experts that a lane lists
@@ -281,6 +281,10 @@ __device__ inline float min3(float a, float b, float c) {
   float r;
   asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
   return r;
+}
+// NaN if one of them is.
+__device__ inline float nan_min3(float a, float b, float c) {
+  return __builtin_elementwise_minimum(__builtin_elementwise_minimum(a, b), c);
 }
 
 __device__ inline float row_max(float v) {
@@ -430,7 +434,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
       }
     };
     float top = 0.f, inv = 0.f, sum = 0.f;   // the largest logit, 1 / softmax sum, the sum
-    // keys of 4 logits: -inf of a masked expert (a bias of -inf makes it so by itself)
+    // keys of 4 logits: score + bias (a masked expert's, whose score is 0, is made -inf by the
+    // callers where the logit is)
     auto keys4 = [&](int c, float* l) {
       if (!BIAS) return;
       const float4 b4 = *reinterpret_cast<const float4*>(s_bias + e0 + c);
@@ -439,7 +444,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
       for (int i = 0; i < 4; ++i) {
         const float s = SOFTMAX ? __builtin_amdgcn_exp2f((l[i] - top) * kLog2e) * inv
                                 : fast_sigmoid(l[i]);
-        l[i] = l[i] == kNegInf ? kNegInf : s + b[i];
+        l[i] = s + b[i];
       }
     };
     // the same in float64, for the few tokens whose float32 keys are too close: the sum of
@@ -464,10 +469,13 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
     float key[EPL];
     float hi = kNegInf, lo = -kNegInf;
 #pragma unroll
-    for (int c = 0; c < EPL; c += 4) logits4(c, key + c);
+    for (int c = 0; c < EPL; c += 4) {
+      logits4(c, key + c);
+      lo = nan_min3(nan_min3(lo, key[c], key[c + 1]), key[c + 2], key[c + 3]);
+      if (SOFTMAX || !BIAS) hi = max3(max3(hi, key[c], key[c + 1]), key[c + 2], key[c + 3]);
+    }
+    bool unsure = nan_bias || lo != lo;      // a NaN among the logits
     if (SOFTMAX) {
-#pragma unroll
-      for (int c = 0; c < EPL; c += 2) hi = max3(hi, key[c], key[c + 1]);
       top = row_max(hi);
       top = top == kNegInf ? 0.f : top;   // nothing left: every e^(l - top) is 0
       if (BIAS || !a.renorm) {
@@ -476,16 +484,28 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
         sum = row_sum(sum);
         inv = __builtin_amdgcn_rcpf(sum);
       }
-      hi = kNegInf;
     }
-    bool unsure = nan_bias;
+    if (BIAS) {
+      const bool masked = lo == kNegInf;
+      unsure |= SOFTMAX && top == -kNegInf;
 #pragma unroll
-    for (int c = 0; c < EPL; c += 4) {
-      keys4(c, key + c);
+      for (int c = 0; c < EPL; c += 4) keys4(c, key + c);
+      if (__any(masked)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) unsure |= key[c + i] != key[c + i];
-      hi = max3(max3(hi, key[c], key[c + 1]), key[c + 2], key[c + 3]);
-      lo = min3(min3(lo, key[c], key[c + 1]), key[c + 2], key[c + 3]);
+        for (int c = 0; c < EPL; c += 4) {
+          float l[4];
+          logits4(c, l);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) key[c + i] = l[i] == kNegInf ? kNegInf : key[c + i];
+        }
+      }
+      hi = kNegInf;
+      lo = -kNegInf;
+#pragma unroll
+      for (int c = 0; c < EPL; c += 4) {
+        hi = max3(max3(hi, key[c], key[c + 1]), key[c + 2], key[c + 3]);
+        lo = min3(min3(lo, key[c], key[c + 1]), key[c + 2], key[c + 3]);
+      }
     }
     unsure |= hi == -kNegInf;
     if (__any(lo == kNegInf)) {     // masked experts: the lowest of the others
@@ -649,7 +669,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
         for (int i = 0; i < 4; ++i) k[i] = l[i];
         keys4(c, k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f(fix(k[i]), l[i], e0 + c + i);
+        for (int i = 0; i < 4; ++i) f(fix(l[i] == kNegInf ? kNegInf : k[i]), l[i], e0 + c + i);
       }
     };
     // experts that did not make the list but are as near to the last chosen one
