@@ -862,7 +862,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteB
       gate[h] = id[h] >= 0 ? a.gates[g * a.K + k] : 0.f;
       d[h] = gate[h] != 0.f ? a.dgates[g * a.K + k] : 0.f;   // a gate of 0 has no gradient
     }
-    mean += gate[h] * d[h];
+    // q exactly 1 for a lone choice, whose gradient is then exactly 0
+    mean += (a.renorm ? gate[h] / a.scale : gate[h]) * d[h];
   }
   mean = row_sum(mean);
   if (DENSE) {
@@ -900,7 +901,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteB
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (id[h] < 0) continue;
-    float v = gate[h] * (a.renorm ? d[h] - mean / a.scale : d[h]);
+    float v = gate[h] * (a.renorm ? d[h] - mean : d[h]);
     if (!a.softmax && gate[h] != 0.f) {
       const float l = a.bf16 ? load_logit<true>(a.logits, g * a.E + id[h])
                              : load_logit<false>(a.logits, g * a.E + id[h]);

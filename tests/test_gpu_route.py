@@ -370,6 +370,21 @@ def test_backward_skips_bad_ids_and_adds_repeated_ones():
     assert torch.equal(d.cpu(), want)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_lone_choice_has_no_gradient(score):
+    """K = 1 with renormalised gates: the gate is the scale whatever the logits are."""
+    say("route lone choice", score)
+    cfg = cfg_of(50, 12, 1)
+    rng = np.random.default_rng(9)
+    for scale in (1.0, 2.5, 0.3):
+        rt = MoERouter(cfg, score=score, scale=scale, backward=True)
+        l = torch.from_numpy(rng.standard_normal((50, 12)).astype(np.float32)).cuda()
+        _, gates = rt.forward(l)
+        d = rt.backward(l, torch.from_numpy(rng.standard_normal((50, 1)).astype(np.float32)).cuda())
+        torch.cuda.synchronize()
+        assert bool((gates == np.float32(scale)).all()) and not d.any()
+
+
 @pytest.mark.parametrize("dtype,width,K", [("fp32", 64, 1), ("fp32", 76, 3), ("bf16", 8, 2),
                                            ("bf16", 1408, 8), ("fp32", 1028, 9), ("bf16", 7168, 8),
                                            ("bf16", 264, 32)])
