@@ -244,8 +244,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
 // 91 us; route_kernel 535, 1000 and 690 us.
 constexpr int kHeads = 8;            // best experts that a lane lists
 constexpr int kTokens = 4;           // per wavefront
-// Tokens per launch of the kernels of four tokens per wavefront, which do not loop (a loop's invariants took 40
-// registers): a launch holds at most 2^32 threads.
+// Tokens per launch of the kernels of four tokens per wavefront, which do not loop (a loop's
+// invariants took 40 registers): a launch holds at most 2^32 threads.
 constexpr int kLaunchTokens = 1 << 26;
 constexpr uint32_t kIdMask = 1023;
 constexpr uint32_t kNearMax = 4096;  // a wider band of doubt sends the token to route_token
