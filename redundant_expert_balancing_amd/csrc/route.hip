@@ -518,16 +518,23 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
     // float32 keys are off by at most `err`: sigmoid 2^-22, softmax 2^-18 (EPL > 32: 2^-17) of
     // the largest score (at most EPL + 4 roundings of the sum, 6 of the rest, in units of
     // 2^-24), the sum with the bias 2^-23 of itself; logits are exact
-    const float err = !BIAS ? 0.f
-                            : (SOFTMAX ? (EPL > 32 ? 7.6293945e-6f : 3.8146973e-6f) * inv : 2.3841858e-7f) +
-                                  1.1920929e-7f * max2(fabsf(hi), fabsf(lo));
+    auto key_error = [&](float low) {
+      if (!BIAS) return 0.f;
+      return (SOFTMAX ? (EPL > 32 ? 7.6293945e-6f : 3.8146973e-6f) * inv : 2.3841858e-7f) +
+             1.1920929e-7f * max2(fabsf(hi), fabsf(low));
+    };
+    const float err = key_error(lo);
     // a long tail of low keys would take the range's resolution: keys more than 64 below the
     // highest get the number of masked ones
     const bool tail = lo < hi - 64.f;
     if (tail) lo = hi - 64.f;
     float f = hi > lo ? kQMax * 0.9999995f * __builtin_amdgcn_rcpf(hi - lo) : 0.f;
-    const uint32_t near = BIAS ? saturating_uint(2.f * err * f) + 3 : 0;
-    unsure |= near > kNearMax;
+    // The error in fixed-point steps, of keys inside the range: where it is too wide, and where
+    // the spread is so small that f is not finite, the token goes to route_token. Compared as a
+    // float: as a number it would wrap.
+    const float steps = BIAS && f > 0.f ? 2.f * key_error(lo) * f : 0.f;
+    unsure |= BIAS ? !(steps <= float(kNearMax - 3)) : f == -kNegInf;
+    const uint32_t near = BIAS ? saturating_uint(min2(steps, float(kNearMax))) + 3 : 0;
 
     // groups: runs of the token's lanes; an empty one ranks behind every expert's
     bool kept = true;

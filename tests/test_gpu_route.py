@@ -492,3 +492,49 @@ def test_router_graph_capture_and_stream():
         torch.cuda.synchronize()
         got = (rt.topk_idx, rt.gates, rt.dlogits, layer.dgates)
         assert all(torch.equal(a, b) for a, b in zip(want, got)), rep
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_keys_that_hardly_differ(score, dtype):
+    """Keys whose spread is too small for the packed range: scores of very low logits with a
+    bias of zeros, logits that differ by subnormals, and ordinary and masked rows between."""
+    say("route tiny spread", score, dtype)
+    rng = np.random.default_rng(12)
+    E, N = 64, 32
+    l = rng.standard_normal((N, E))
+    for g, at in enumerate((-22.0, -25.0, -40.0, -60.0, -75.0, -80.0, -86.0)):
+        l[g] += at
+    l[8:12] = 0.0
+    l[8, 37] = 1e-35
+    l[9] = rng.integers(0, 4, E) * 1e-35
+    l[10] = rng.integers(0, 5, E) * 2.0 ** -133         # subnormal in both types
+    l[11] = rng.integers(-3, 3, E) * 1e-33
+    l[12] = 1e-3 + 2.0 ** -30 * rng.integers(0, 4, E)
+    l[13] = -80.0 + rng.standard_normal(E)
+    l[13, 5:] = -np.inf
+    l[14] = -np.inf
+    l[15, 9:] = -80.0
+    same = np.full(E, 1e-35)
+    for renorm in (True, False):
+        for g in (dict(), dict(groups=4, top_groups=2, group_top=2), dict(groups=8, top_groups=5)):
+            for bias in (None, np.zeros(E), same):
+                for K in (8, 12):
+                    check(cfg_of(N, E, K), l, bias, dtype, score=score, renorm=renorm, **g)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_of_the_lowest_value(score):
+    """Experts put last by a bias of float32's lowest value, which masks nothing: near ties
+    among the others, and rows that need some of them."""
+    say("route lowest bias", score)
+    rng = np.random.default_rng(13)
+    E, N = 64, 33
+    l = rng.standard_normal((N, E)).astype(np.float32)
+    l[::3] = 1.5 + 2.0 ** -23 * rng.integers(0, 4, (len(l[::3]), E))
+    for left in (40, 20, 6):
+        b = np.full(E, np.finfo(np.float32).min)
+        b[rng.permutation(E)[:left]] = 0.0
+        for g in (dict(), dict(groups=8, top_groups=5, group_top=2), dict(groups=4, top_groups=3)):
+            for K in (8, 12):
+                check(cfg_of(N, E, K), l, b, score=score, **g)
