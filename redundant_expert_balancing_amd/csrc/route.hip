@@ -525,7 +525,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
     };
     const float err = key_error(lo);
     // a long tail of low keys would take the range's resolution: keys more than 64 below the
-    // highest get the number of masked ones
+    // highest get the number of masked ones (where the choice comes down to them, route_token
+    // makes it)
     const bool tail = lo < hi - 64.f;
     if (tail) lo = hi - 64.f;
     float f = hi > lo ? kQMax * 0.9999995f * __builtin_amdgcn_rcpf(hi - lo) : 0.f;
@@ -652,7 +653,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
     // (a list of fewer than 8 experts ends in zeros, whose id is cut to a place in the row)
     auto place_of = [&](uint32_t x) { return min(int(kIdMask - (x & kIdMask)), kRow - 1); };
     const uint32_t wl = s_list[w][t][a.K - 1], last = wl >> 10;      // the last chosen
-    unsure |= tail && last == 0;
+    // the last choice, or a rival within the error below it, may lie under the range
+    unsure |= tail && last <= near;
     const uint32_t least = s_list[w][t][KL - 1];
     // a lane has more of the best KL than its list holds
     if (KL > kHeads) unsure |= lost > least && (lost > kIdMask || last == 0);

@@ -538,3 +538,19 @@ def test_biases_of_the_lowest_value(score):
         for g in (dict(), dict(groups=8, top_groups=5, group_top=2), dict(groups=4, top_groups=3)):
             for K in (8, 12):
                 check(cfg_of(N, E, K), l, b, score=score, **g)
+
+
+def test_last_choice_at_the_end_of_the_packed_range():
+    """Biases of about -64 on all but one expert put the last choice 64 below the best, where
+    the packed range ends; its rivals' scores differ by less than a float32 sum resolves."""
+    say("route range end")
+    rng = np.random.default_rng(14)
+    E, N, K = 64, 1024, 2
+    step = 2.0 ** -18                          # of float32 numbers in [-64, -32)
+    b = -64.0 + step * rng.integers(0, 50000, E)
+    b[0] = 0.0
+    # sums just below the middle of two float32 numbers, 8 .. 23 steps below hi - 64 = -63.5
+    key = -63.5 - step * (8.5 + np.arange(N)[:, None] % 16) + 2e-8 * (rng.standard_normal((N, E)) - 3.0)
+    s = key - b
+    s[:, 0] = 0.5
+    check(cfg_of(N, E, K), np.log(s / (1.0 - s)), b, score="sigmoid")
