@@ -567,8 +567,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_packed_kernel(RouteArg
           score = score == kNegInf ? kNegInf : m1 + m2;
           tol = 3.8146973e-6f;
         } else {
-          score = m2 == kNegInf ? m1 : m1 + m2;
-          tol = 4.f * err + 2.3841858e-7f * (score == kNegInf ? 0.f : fabsf(score));
+          // half the sum: two biases of the largest value would pass float32's range
+          score = 0.5f * m1 + (m2 == kNegInf ? 0.f : 0.5f * m2);
+          tol = 2.f * err + 2.3841858e-7f * (score == kNegInf ? 0.f : fabsf(score));
         }
       }
       const int mine = i16 >> shift;

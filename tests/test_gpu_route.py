@@ -554,3 +554,20 @@ def test_last_choice_at_the_end_of_the_packed_range():
     s = key - b
     s[:, 0] = 0.5
     check(cfg_of(N, E, K), np.log(s / (1.0 - s)), b, score="sigmoid")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_scores_beyond_float32(score):
+    """Two biases of float32's lowest (or highest) value add up to more than float32 holds: such
+    a group still comes before one whose experts are all switched off, and ties to the lower."""
+    say("route group sums", score)
+    rng = np.random.default_rng(15)
+    E, N, per = 16, 13, 4
+    l = rng.standard_normal((N, E))
+    low, high = float(np.finfo(np.float32).min), float(np.finfo(np.float32).max)
+    for groups in ((-np.inf, low, 0.0, 0.0), (-np.inf, 0.0, low, low), (low, -np.inf, low, 0.0),
+                   (low, low, -np.inf, low), (0.75 * high, high, 0.0, high), (low, 0.6 * low, 0.0, -np.inf),
+                   (-np.inf, -np.inf, low, -np.inf)):
+        b = np.repeat(np.array(groups), per)
+        for top, K in ((3, 10), (2, 6), (1, 3)):
+            check(cfg_of(N, E, K), l, b, score=score, groups=4, top_groups=top, group_top=2)
