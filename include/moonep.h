@@ -386,7 +386,8 @@ int moonep_gate_grad(const moonep_shape* shape, int32_t width, const float* src,
  *           ceil(width/32) are written 0.
  * The scale of a block is the smallest power of two (at least 2^-127) that clips none of
  * its values, and values are rounded to nearest even: off by at most 2^-4 of the value,
- * or 2^-10 of the scale where that is more. A block that holds an Inf or a NaN becomes NaN.
+ * or 2^-10 of the scale where that is more. (Magnitudes above 240 * 2^120 become that value:
+ * rounded to 2^128 they would be Inf in float32.) A block that holds an Inf or a NaN becomes NaN.
  */
 
 /* Checkpoint of token rows: src dtype [N, width], width H or Hp. As all of the checkpoint

@@ -79,7 +79,11 @@ def dequantise(q, s, table, sign_bit):
 
 
 def checkpoint(x):
-    return quantise(np.asarray(x, dtype=np.float64), E4M3, 448.0, 128)
+    """Finite magnitudes above 240 * 2^120 become that value: rounded up they would be 2^128,
+    which float32 does not hold."""
+    x = np.asarray(x, dtype=np.float64)
+    top = 240.0 * 2.0 ** 120
+    return quantise(np.where(np.isfinite(x), np.clip(x, -top, top), x), E4M3, 448.0, 128)
 
 
 def checkpoint_values(q, s):

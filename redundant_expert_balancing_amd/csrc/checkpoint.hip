@@ -17,8 +17,8 @@ __device__ inline uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FF
 
 // 4 values scaled by inv as 4 e4m3 bytes
 __device__ inline uint32_t pack_e4m3(const float* v, float inv) {
-  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true));
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[0]) * inv, clamp_e4m3(v[1]) * inv, 0, false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[2]) * inv, clamp_e4m3(v[3]) * inv, w, true));
 }
 
 __device__ inline void unpack_e4m3(uint32_t w, float scale, float* v) {

@@ -97,6 +97,10 @@ __device__ inline uint32_t scale_byte(uint32_t amax_bits) {
   const int b = e - T::kTopExp + ((amax_bits & 0x7FFFFFu) > T::kTopMant ? 1 : 0);
   return uint32_t(b < 0 ? 0 : b);
 }
+// Largest magnitude that e4m3 with a float32 scale is rounded from: 240 * 2^120. What lies above
+// (up to float32's largest, 256 * 2^120 less a step) would round to 2^128.
+constexpr float kE4m3Max = 0x1.ep127f;
+__device__ inline float clamp_e4m3(float v) { return __builtin_amdgcn_fmed3f(v, -kE4m3Max, kE4m3Max); }
 // 2^-e of a scale byte (at most 254 for a finite block), exact
 __device__ inline float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 // 2^e of a scale byte: byte 0 is the subnormal 2^-127

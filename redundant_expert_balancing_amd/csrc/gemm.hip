@@ -807,7 +807,8 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64) void gemm_bf16_kernel(GemmA
                 const uint32_t sb = scale_byte<E4M3>(row16_max(
                     max(__float_as_uint(v0) & 0x7FFFFFFFu, __float_as_uint(v1) & 0x7FFFFFFFu)));
                 const float inv = scale_inverse(sb);
-                const int w = sb == 255 ? 0 : __builtin_amdgcn_cvt_pk_fp8_f32(v0 * inv, v1 * inv, 0, false);
+                const int w = sb == 255 ? 0 : __builtin_amdgcn_cvt_pk_fp8_f32(
+                    clamp_e4m3(v0) * inv, clamp_e4m3(v1) * inv, 0, false);
                 const uint32_t off = lq[b] + uint32_t(i * 16 + r) * g.Hp;
                 __builtin_amdgcn_raw_buffer_store_b8((unsigned char)w, qrs, off, 0, 0);
                 __builtin_amdgcn_raw_buffer_store_b8((unsigned char)(w >> 8), qrs, off + 16, 0, 0);

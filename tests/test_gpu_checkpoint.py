@@ -316,3 +316,74 @@ def test_checkpoint_ffn_graph_replays_match_eager():
         torch.cuda.synchronize()
         for k, v in want.items():
             assert torch.equal(getattr(l, k), v), (rep, k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_values_at_the_end_of_the_range_stay_finite(dtype):
+    """Values next to the type's largest and lowest: rounded up they would pass float32's range."""
+    say("checkpoint range end", dtype)
+    N, width = 8, 96
+    big = float(torch.finfo(_dt(dtype)).max)
+    rng = np.random.default_rng(5)
+    x = (rng.uniform(0.85, 1.0, (N, width)) * big).astype(np.float32)
+    x *= rng.choice([-1.0, 1.0], (N, width)).astype(np.float32)
+    x[0] = big
+    x[1] = -big
+    x[2, ::2] = 1.0
+    x[3] = 240.0 * 2.0 ** 120
+    x[4] = np.float32(248.0 * 2.0 ** 120)
+    t = torch.from_numpy(x).cuda().to(_dt(dtype))
+    t.clamp_(-big, big)
+    sh = _shape(N, 1, width, 32, dtype)
+    q, s = C.buffers(N, width)
+    L.moonep_checkpoint_quantize(sh, width, t, q, s)
+    dst = torch.zeros_like(t)
+    L.moonep_checkpoint_dispatch(sh, width, q, s, torch.arange(N, dtype=torch.int32, device="cuda"), dst)
+    torch.cuda.synchronize()
+    _assert_bytes(q, s, t.double().cpu().numpy(), width)
+    got, want = dst.double(), t.double()
+    assert bool(torch.isfinite(got).all())
+    # 2^-4 of the value, or 2^-10 of the block's scale (2^120) where that is more
+    assert bool(((got - want).abs() <= torch.clamp(want.abs() * 2.0 ** -4, min=2.0 ** 110)).all())
+    # the pre-activation's checkpoint: gates this large (silu(g) = g), ups of zero
+    hp = 32
+    h = torch.zeros((N, 2 * hp), device="cuda")
+    h[:, :hp] = t[:, :hp].float()
+    hq, hs = C.buffers(N, 2 * hp)
+    act = torch.empty((N, hp), dtype=_dt(dtype), device="cuda")
+    L.moonep_swiglu_checkpoint(sh, h, act, hq, hs)
+    dh = torch.empty((N, 2 * hp), dtype=_dt(dtype), device="cuda")
+    a = torch.empty_like(act)
+    L.moonep_swiglu_backward_checkpoint(sh, hq, hs, torch.full((N, hp), 0.5, device="cuda"), None, None,
+                                        a, dh, None)
+    torch.cuda.synchronize()
+    _assert_bytes(hq, hs, h.double().cpu().numpy(), 2 * hp)
+    assert bool(torch.isfinite(dh).all()) and not a.any()
+
+
+def test_fused_gemm_at_the_end_of_the_range():
+    """The GEMM's checkpointing epilogue on the same values: one product per sum."""
+    say("checkpoint fused range end")
+    N, E, H, Hp = 70, 2, 64, 64
+    sh = L.Shape(1, N, E, 1, E, H, Hp, L.TRAIN, L.BF16)
+    big = float(torch.finfo(torch.bfloat16).max)
+    rng = np.random.default_rng(6)
+    w = torch.zeros((2 * E, H, 2 * Hp), dtype=torch.bfloat16, device="cuda")
+    row = rng.uniform(0.85, 1.0, (E, 2 * Hp)) * big * rng.choice([-1.0, 1.0], (E, 2 * Hp))
+    row[0, :40] = big
+    w[:E, 5] = torch.from_numpy(row).cuda().bfloat16()
+    x = torch.zeros((N, H), dtype=torch.bfloat16, device="cuda")
+    x[:, 5] = 1.0
+    x[1, 5] = 0.5
+    cu = torch.tensor([[0, 33, N, N, N]], dtype=torch.int32, device="cuda")
+    ws = torch.empty(L.moonep_workspace_bytes(L.Shape(1, N, E, 1, E, H, 2 * Hp, L.TRAIN, L.BF16)) // 4,
+                     dtype=torch.int32, device="cuda")
+    L.moonep_workspace_init(sh, ws)
+    act = torch.empty((N, Hp), dtype=torch.bfloat16, device="cuda")
+    q, s = C.buffers(N, 2 * Hp)
+    L.moonep_grouped_gemm_swiglu_checkpoint(sh, x, w, cu, act, q, s, ws)
+    torch.cuda.synchronize()
+    of = torch.tensor([0] * 33 + [1] * (N - 33), device="cuda")
+    h = (w[of, 5].double() * x[:, 5:6].double()).cpu().numpy()
+    _assert_bytes(q, s, h, 2 * Hp)
+    assert np.isfinite(F.checkpoint_values(q.cpu().numpy(), s.cpu().numpy())).all()

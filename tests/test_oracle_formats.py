@@ -37,3 +37,13 @@ def test_errors_stay_within_half_a_step():
         q, s = f(x)
         scale = np.repeat(2.0 ** (s.astype(float) - 127), 32, 1)
         assert (np.abs(val(q, s) - x) <= np.maximum(rel * np.abs(x), low * scale)).all()
+
+
+def test_checkpoints_of_the_largest_values_stay_finite():
+    """What rounds up to 256 * 2^120 = 2^128 is kept as 240 * 2^120, still within 2^-4."""
+    big = np.float32([np.finfo(np.float32).max, 248.0 * 2.0 ** 120, 247.99 * 2.0 ** 120, 240.0 * 2.0 ** 120])
+    x = np.concatenate([big, -big, np.ones(24, np.float32)])[None].astype(np.float64)
+    v = F.checkpoint_values(*F.checkpoint(x))
+    assert (np.abs(v[0, :8]) == 240.0 * 2.0 ** 120).all() and np.isfinite(v.astype(np.float32)).all()
+    assert (np.abs(v - x)[0, :8] <= 2.0 ** -4 * np.abs(x)[0, :8]).all()
+    assert F.checkpoint(np.array([[np.inf] * 32]))[1][0, 0] == 255
