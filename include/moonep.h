@@ -435,7 +435,9 @@ int moonep_grouped_gemm_swiglu_checkpoint(const moonep_shape* shape, const void*
  *   dgates[u] = <a, da> of the slot u at each position (src_index from moonep_plan);
  *   act  = gate_u * a   (WGRAD(W2) with the dY permuted without gates: the same product)
  *   dh   = gate_u * dh
- * A position whose src_index is not in [0, N*K) gets act = dh = 0 and writes no dgates.
+ * A position whose src_index is not in [0, N*K) gets act = dh = 0 and writes no dgates: the
+ * gradient of a slot that no position names (all of them, in an empty plan) is left as it was,
+ * so clear dgates before the call where ids can be invalid.
  *   da  in  float32 [R*SK, Hp]
  * Requires Hp a multiple of 32. Training layers only.
  */

@@ -47,6 +47,17 @@ def _shape(cfg, H, Hp):
                    L.BF16 if cfg.dtype == "bf16" else L.FP32)
 
 
+def _zero(t, stream):
+    """t = 0 on `stream` (None, a torch stream or a hipStream_t), by a fill kernel."""
+    if stream is None:
+        t.zero_()
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    with torch.cuda.stream(stream):
+        t.zero_()
+
+
 class MoEFFN:
     def __init__(self, cfg, device="cuda", backward: bool = False, w1_all=None, w2_all=None,
                  fused: bool = True, checkpoint: bool = False, scratch: "MoEFFN | None" = None):
@@ -179,6 +190,8 @@ class MoEFFN:
         L.moonep_dispatch(self.up, c.H, dy, self.slot_map, None, self.dyp, stream)
         L.moonep_grouped_gemm(self.down, L.DGRAD, self.dyp, self.w2_all, self.cu_seqlens, self.da,
                               None, None, self.ws, stream)
+        # it writes the gradients of the slots that the plan names: none where ids were rejected
+        _zero(self.dgates, stream)
         L.moonep_swiglu_backward_checkpoint(self.shape, self.hq, self.hscales, self.da,
                                             self.src_index, gates, self.act, self.dh, self.dgates,
                                             stream)

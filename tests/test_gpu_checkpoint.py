@@ -387,3 +387,29 @@ def test_fused_gemm_at_the_end_of_the_range():
     h = (w[of, 5].double() * x[:, 5:6].double()).cpu().numpy()
     _assert_bytes(q, s, h, 2 * Hp)
     assert np.isfinite(F.checkpoint_values(q.cpu().numpy(), s.cpu().numpy())).all()
+
+
+@pytest.mark.parametrize("stream", ["current", "side", "handle"])
+def test_gate_gradients_of_a_rejected_routing_are_zero(stream):
+    """After a step on valid ids, a step whose ids are out of range (the plan is empty) gives
+    gradients of zero, as the layer without checkpoints does, and not the last step's."""
+    say("checkpoint rejected routing", stream)
+    cfg = small_cfg(name="ck_reject", R=2, S=20, E=8, K=2, H=64, Hp=64)
+    r, d, topk, gates = _data(cfg)
+    bad = topk.clone()
+    bad[3, 1] = cfg.E + 2
+    own = torch.cuda.Stream()
+    side = {"current": None, "side": own, "handle": own.cuda_stream}[stream]
+    torch.cuda.synchronize()
+    for checkpoint in (False, True):
+        l = _ffn(cfg, checkpoint, d)
+        l.dgates.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for ids in (topk, bad):
+            l.forward(ids, d["x"], gates, side)
+            l.backward(d["dyH"], gates, side)
+            got = l.gate_grad(d["dyH"], side)
+            torch.cuda.synchronize()
+            assert bool(torch.isfinite(got).all())
+        assert not got.any() and not l.dx.any() and not l.y.any(), checkpoint
+        assert l.error_flags(True) == L.ERR_ID_RANGE
