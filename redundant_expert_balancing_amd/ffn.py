@@ -68,6 +68,7 @@ class MoEFFN:
             raise ValueError("scratch: only layers with checkpoints can share slot buffers")
         self.cfg = c
         self.checkpoint = checkpoint
+        self._dgates_formed = False       # with checkpoints: dgates belong to the last forward
         # the float32 gate/up GEMM has no checkpointing epilogue
         self.fused = fused = fused and not (checkpoint and c.dtype == "fp32")
         self.shape = _shape(c, c.H, c.Hp)
@@ -143,6 +144,7 @@ class MoEFFN:
         L.moonep_checkpoint_quantize(self.up, self.cfg.H, x, self.xq, self.xs, stream)
 
     def gate_up(self, stream=None):
+        self._dgates_formed = False       # those of an earlier forward
         if self.fused and self.checkpoint:
             L.moonep_grouped_gemm_swiglu_checkpoint(self.shape, self.xp, self.w1_all,
                                                     self.cu_seqlens, self.act, self.hq,
@@ -179,10 +181,15 @@ class MoEFFN:
 
     # ---- backward
     def gate_grad(self, dy, stream=None):
-        """Gradient of the gates [N,K]. With checkpoints, the one that the last backward
-        formed (the expert outputs are not kept); else from the forward's outputs and dy."""
+        """Gradient of the gates [N,K], from the forward's outputs and dy. With checkpoints the
+        outputs are not kept: it is the one that backward(dy, gates) formed, which has to have
+        been called after the last forward (replays of captured graphs are not seen here: they
+        leave it in .dgates)."""
         if not self.checkpoint:
             L.moonep_gate_grad(self.up, self.cfg.H, self.z, self.slot_map, dy, self.dgates, stream)
+        elif not self._dgates_formed:
+            raise RuntimeError("gate_grad: with checkpoints, backward forms the gates' gradient; "
+                               "it has not been called since the last forward")
         return self.dgates
 
     def _backward_checkpoint(self, dy, gates, stream):
@@ -199,6 +206,7 @@ class MoEFFN:
                               self.grad2, self.red2, self.ws, stream)
         L.moonep_grouped_gemm(self.up, L.DGRAD, self.dh, self.w1_all, self.cu_seqlens, self.dxp,
                               None, None, self.ws, stream)
+        self._dgates_formed = True
         L.moonep_checkpoint_dispatch(self.up, c.H, self.xq, self.xs, self.slot_map, self.xp, stream)
 
     def backward(self, dy, gates, stream=None):

@@ -413,3 +413,32 @@ def test_gate_gradients_of_a_rejected_routing_are_zero(stream):
             assert bool(torch.isfinite(got).all())
         assert not got.any() and not l.dx.any() and not l.y.any(), checkpoint
         assert l.error_flags(True) == L.ERR_ID_RANGE
+
+
+def test_gate_gradients_need_the_backward_of_their_forward():
+    """A checkpointing layer forms the gates' gradient in its backward: asked before the first
+    one, or after a later forward, it refuses instead of handing out what its buffer holds."""
+    say("checkpoint gate_grad order")
+    cfg = small_cfg(name="ck_order", R=2, S=20, E=8, K=2, H=64, Hp=64)
+    r, d, topk, gates = _data(cfg)
+    l = _ffn(cfg, True, d)
+    with pytest.raises(RuntimeError, match="backward"):
+        l.gate_grad(d["dyH"])
+    l.forward(topk, d["x"], gates)
+    with pytest.raises(RuntimeError, match="backward"):
+        l.gate_grad(d["dyH"])
+    l.backward(d["dyH"], gates)
+    want = l.gate_grad(d["dyH"]).clone()
+    assert torch.equal(l.gate_grad(d["dyH"]), want)
+    l.forward(topk, d["x"], gates)
+    with pytest.raises(RuntimeError, match="backward"):
+        l.gate_grad(d["dyH"])
+    l.backward(d["dyH"], gates)
+    assert torch.equal(l.gate_grad(d["dyH"]), want)
+    # the layer without checkpoints keeps its outputs, so there the order is free
+    plain = _ffn(cfg, False, d)
+    plain.forward(topk, d["x"], gates)
+    before = plain.gate_grad(d["dyH"]).clone()
+    plain.backward(d["dyH"], gates)
+    assert torch.equal(plain.gate_grad(d["dyH"]), before)
+    torch.cuda.synchronize()
