@@ -17,7 +17,8 @@ With checkpoint=True the forward keeps x and the gate/up pre-activation in 8 bit
   and dh times the gates, and dgates) -> wgrad(W2) -> dgrad(W1) -> permute of x
   from its checkpoint -> wgrad(W1) -> combine -> reduce_grad.
 The slot buffers then hold nothing between the two passes, so the layers of a
-model can share one set of them (scratch=another layer of the same shape): what
+model can share one set of them (scratch=another layer of the same shape on the
+same device; calls of layers that share them must be ordered on one stream): what
 each keeps per slot falls from 2H + 6H' bytes (bfloat16 xp, act, hs) to 2.0625 H'
 bytes, plus 1.03 H bytes per token.
 
@@ -102,10 +103,12 @@ class MoEFFN:
             self.h = None if fused else torch.empty((rows, 2 * c.Hp), **f32)
             self.z = torch.empty((rows, c.H), **f32)
         else:
-            mine = (c.R, c.S, c.K, c.H, c.Hp, c.dtype, fused, self.device.type)
+            mine = (c.R, c.S, c.K, c.H, c.Hp, c.dtype, fused)
             o = scratch.cfg
-            if mine != (o.R, o.S, o.K, o.H, o.Hp, o.dtype, scratch.fused, scratch.device.type):
+            if mine != (o.R, o.S, o.K, o.H, o.Hp, o.dtype, scratch.fused):
                 raise ValueError("scratch: a layer of another shape")
+            if scratch.xp.device != self.cu_seqlens.device:
+                raise ValueError(f"scratch: a layer on another device, {scratch.xp.device}")
             for name in ("xp", "act", "h", "z", "dyp", "da", "dh", "dxp"):
                 setattr(self, name, getattr(scratch, name))
         self.hs = torch.empty((rows, 2 * c.Hp), **dtd) if backward and not checkpoint else None
