@@ -612,8 +612,9 @@ extern "C" int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* 
   const int64_t held = int64_t(s.E) + s.R;      // a plan has at most this many segments
   const bool tiled = cus % 4 == 0 && a.NK >= 8 * held &&
                      (a.NK + MxTile::BM / 2 * held) / MxTile::BM * nt >= cus &&
-                     // 32-bit offsets of gathered rows and tile numbers
+                     // 32-bit offsets of gathered rows and of a tile's outputs, and tile numbers
                      (!src_index || a.xrows * a.KT * 64 < int64_t(kOffNone)) &&
+                     int64_t(MxTile::BM) * s.Hp * 4 <= int64_t(kOffNone) &&
                      (a.NK / MxTile::BM + int64_t(s.R) * (s.E + s.B)) * nt < INT32_MAX;
   if (tiled) {
     st = launch_tile_list(s, cu_seqlens, MxTile::BM, ws, strm, &a.tiles, &a.ntiles);

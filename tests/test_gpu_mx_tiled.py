@@ -270,3 +270,30 @@ def test_prefetched_experts_are_read():
         assert bool((topk.reshape(-1)[l.src_index[a:b].long()] == home).all())
         v, wv = xv[tok[a:b]], weight_of(l.wq[home], l.wscales[home], cfg.H)
         assert bool(((l.out[a:b].double() - v @ wv).abs() <= cfg.H * U * (v.abs() @ wv.abs())).all()), row
+
+
+def test_outputs_wider_than_a_tile_s_offsets():
+    """128 rows of H' floats that pass 2^31 bytes are left to the few-row form."""
+    say("mx wide outputs")
+    N, H, Hp = 128, 64, 4227392                    # 127 * 4 * H' is beyond 2^31
+    sh = L.Shape(1, N, 1, 1, 0, H, Hp, L.INFER, L.BF16)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn((N, H), generator=g, device="cuda").bfloat16()
+    w = torch.randn((1, H, Hp), generator=g, device="cuda", dtype=torch.float32).bfloat16()
+    xq, xs = mx.buffers(N, H)
+    wq, wsc = mx.weight_buffers(1, H, Hp)
+    ws = torch.empty(L.moonep_workspace_bytes(sh) // 4, dtype=torch.int32, device="cuda")
+    L.moonep_workspace_init(sh, ws)
+    L.moonep_mx_quantize(sh, N, H, x, xq, xs)
+    L.moonep_mx_quantize_weight(sh, w, wq, wsc)
+    c = torch.full((N, Hp), float("nan"), device="cuda")
+    L.moonep_mx_grouped_gemm(sh, xq, xs, None, wq, wsc,
+                             torch.tensor([[0, N]], dtype=torch.int32, device="cuda"), c, ws)
+    torch.cuda.synchronize()
+    xv = rows_of(xq, xs, H)
+    for n0 in (0, Hp - 4096):                      # the first columns and the last
+        tiles = slice(n0 // 16, n0 // 16 + 256)
+        wv = weight_of(wq[0][tiles], wsc[0][tiles], H)
+        err = (c[:, n0:n0 + 4096].double() - xv @ wv).abs()
+        assert bool((err <= H * U * (xv.abs() @ wv.abs())).all()), n0
+    assert bool(torch.isfinite(c).all())
