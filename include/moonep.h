@@ -483,9 +483,11 @@ int moonep_mx_prefetch_weight(const moonep_shape* shape, const int32_t* replica_
  *                     is needed); with src_index NULL one row per position, [R*SK, ..]
  *   wq, wscales  in   weights
  *   c            out  float32 [R*SK, Hp]
- * A position whose src_index is not in [0, N*K) gives a row of zeros. Requires H and Hp
+ * A position whose src_index is not in [0, N*K) counts as a row of zeros. Requires H and Hp
  * multiples of 64. shape->dtype plays no part. The workspace is shared with the layer's
- * other calls.
+ * other calls. Calls with many rows per expert are fast only where the gathered token rows
+ * (64*T bytes each) stay below 2 GiB in all and Hp is at most 4194304: beyond either they run
+ * on the form for few rows, which reads each weight once per 64 rows.
  */
 int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* xq, const uint8_t* xscales,
                            const int32_t* src_index, const uint8_t* wq, const uint8_t* wscales,

@@ -234,11 +234,13 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
 // bias (then the id decides, as it should). Where two are (0.1% of the tokens of a normal
 // sigmoid router), the experts in question are ranked by float64 keys, one per lane; so are
 // groups that are too close. Tokens with a NaN or +inf, with more than 16 experts in
-// question, or with more than 8 of the best 16 in one lane, are done again by route_token.
+// question, or with more than 8 of the best 16 in one lane, are done again by route_token; so
+// are those whose keys' spread or error the fixed-point range does not suit.
 //
-// Bound by the vector instructions: 999 per wavefront at E = 384 with sigmoid, bias and groups
-// (757 with softmax and no bias), which issue in 67000 of the 73000 cycles that a CU is busy
-// with 65536 tokens, 37 us (softmax bf16 25 us); reading the logits alone is 22 us (12).
+// Bound by the vector instructions: 1010 per wavefront at E = 384 with sigmoid, bias and groups
+// (759 with softmax and no bias), which issue in 68000 of the 73300 cycles that a CU is busy
+// with 65536 tokens. A call among others takes 37 us (softmax bf16 24 us); reading the logits
+// alone is 22 us (12).
 // Against one float64 wavefront per token (route_kernel): 470 us (410).
 // E = 376 in 8 groups, whose places lie apart: 43 us, E = 1024 in 8 groups 131 us, K = 16
 // 91 us; route_kernel 535, 1000 and 690 us.
