@@ -202,24 +202,24 @@ def _run_own(st):
     op, N = c["op"], c["N"]
     xq, xs = st["xq"], st["xs"]
     if op == "grad":
-        L.moonep_i8_quantize_grad(sh, st["x"], st["src_index"] if c["gather"] else None,
+        L.moonep_int_quantize_grad(sh, st["x"], st["src_index"] if c["gather"] else None,
                                   st["gates"] if c["gather"] else None, st["ws"], st["cu"], xq, xs)
-        L.moonep_i8_grouped_gemm(st["back"], xq, xs, None, st["wq"], None, st["cu"], st["c"],
+        L.moonep_int_grouped_gemm(st["back"], xq, xs, None, st["wq"], None, st["cu"], st["c"],
                                  st["work"])
         return st["c"]
-    L.moonep_i8_quantize(sh, N, c["H"], st["x"], xq, xs)
+    L.moonep_int_quantize(sh, N, c["H"], st["x"], xq, xs)
     if op == "grouped":
-        L.moonep_i8_grouped_gemm(sh, xq, xs, st["src_index"], st["wq"], st["ws"], st["cu"], st["c"],
+        L.moonep_int_grouped_gemm(sh, xq, xs, st["src_index"], st["wq"], st["ws"], st["cu"], st["c"],
                                  st["work"])
         return st["c"]
     if op == "dense":
-        L.moonep_i8_gemm(sh, N, xq, xs, st["wq"], st["ws"], st["add"], st["c"])
+        L.moonep_int_gemm(sh, N, xq, xs, st["wq"], st["ws"], st["add"], st["c"])
         return st["c"]
     if op == "swiglu":
-        L.moonep_i8_grouped_gemm_swiglu(sh, xq, xs, st["src_index"], st["wq"], st["ws"], st["cu"],
+        L.moonep_int_grouped_gemm_swiglu(sh, xq, xs, st["src_index"], st["wq"], st["ws"], st["cu"],
                                         st["act"], st["h"], st["work"])
     else:
-        L.moonep_i8_gemm_swiglu(sh, N, xq, xs, st["wq"], st["ws"], st["act"], st["h"])
+        L.moonep_int_gemm_swiglu(sh, N, xq, xs, st["wq"], st["ws"], st["act"], st["h"])
     return (st["act"], st["h"]) if c["saved"] else st["act"]
 
 
