@@ -495,6 +495,126 @@ int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* xq, const u
                            void* stream);
 
 /*
+ * ---- Experts in 8-bit integers ---------------------------------------------------
+ * Weights and token rows as whole numbers in [-127, 127], with one float32 scale per token
+ * row and one per weight column (output channel). The scale of a row or column is
+ *   max(amax / 127, 2^-126), rounded to float32,
+ * and a value x is held as the whole number nearest to the exact quotient x / scale, ties to
+ * even: off by at most half a scale. A row or column that holds an Inf or a NaN gets the
+ * scale NaN and values 0, so that all of its products are NaN. With T = ceil(H/128) (padding
+ * is zero):
+ *   token rows  q       int8 [rows, 128*T]: value k is byte k
+ *               scales  float32 [rows]
+ *   weights     q       int8 [E+R*B, ceil(Hp/16), 2*T, 64, 16]: value (k, n) is byte k % 16 of
+ *                       lane 16*((k/16)%4) + n%16 of block (n/16, k/64)
+ *               scales  float32 [E+R*B, 16*ceil(Hp/16)]
+ * rows as in W_all: E home experts, then every rank's prefetch slots. H and Hp need not be
+ * multiples of more than a shape's rule asks (8 for bfloat16, 4 for float32).
+ * The products are summed in int32, which is exact; a reduction longer than 131072 could
+ * overflow it and gives MOONEP_ELIMIT. A result is (sum * row scale) * column scale, in
+ * float32 in this order.
+ */
+
+/* Quantise `rows` rows of `width` values (dtype) to token rows; width a multiple of 8
+ * (bfloat16) or 4 (float32), at most 131072. */
+int moonep_int_quantize(const moonep_shape* shape, int64_t rows, int32_t width, const void* src,
+                        int8_t* q, float* scales, void* stream);
+
+/* Quantise the E home experts of w, dtype [E, H, Hp], to weights' rows 0..E-1 (a set-up call). */
+int moonep_int_quantize_weight(const moonep_shape* shape, const void* w, int8_t* wq,
+                               float* wscales, void* stream);
+
+/*
+ * The E home experts of weights [H, Hp] as weights of the product that runs back through
+ * them, [Hp, H] (a set-up call): the same whole numbers. Their scales stay with the
+ * reduction, where moonep_int_quantize_grad applies them.
+ *   wq   in   as of `shape`
+ *   wqt  out  as of `shape` with H and Hp exchanged, rows 0..E-1
+ */
+int moonep_int_transpose_weight(const moonep_shape* shape, const int8_t* wq, int8_t* wqt,
+                                void* stream);
+
+/* moonep_prefetch_weight on 8-bit weights; wscales NULL copies the values alone. */
+int moonep_int_prefetch_weight(const moonep_shape* shape, const int32_t* replica_expert,
+                               int8_t* wq, float* wscales, void* stream);
+
+/*
+ * Grouped GEMM on 8-bit operands:
+ *   c[position of (q,i)] = x[row of the position] @ view_q(i)
+ *   xq, xscales  in   token rows of width H: with src_index (from moonep_plan) one row per
+ *                     token, [N, ..], and position p reads row src_index[p] / K (no permute
+ *                     is needed); with src_index NULL one row per position, [R*SK, ..]
+ *   wq           in   weights
+ *   wscales      in   their scales, or NULL: all 1
+ *   c            out  float32 [R*SK, Hp]; positions behind a rank's last row are left as
+ *                     they were
+ * A position whose src_index is not in [0, N*K) counts as a row of zeros. The workspace is
+ * shared with the layer's other calls. Calls with many rows per expert are fast only where
+ * the gathered token rows (128*T bytes each) stay below 2 GiB in all and Hp is at most
+ * 2097152: beyond either they run on the form for few rows, which reads each weight once
+ * per 64 rows.
+ */
+int moonep_int_grouped_gemm(const moonep_shape* shape, const int8_t* xq, const float* xscales,
+                            const int32_t* src_index, const int8_t* wq, const float* wscales,
+                            const int32_t* cu_seqlens, float* c, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * Gate/up grouped GEMM on 8-bit operands with the SwiGLU in its epilogue: the same bits as
+ * moonep_int_grouped_gemm (up shape) followed by moonep_swiglu, without the float32 h in
+ * memory. shape is the ffn shape; operands as there, the weights [H, 2*Hp] with gate and up
+ * columns interleaved.
+ *   act      out  dtype [R*SK, Hp];  h_saved  out  NULL or dtype [R*SK, 2*Hp]
+ * Requires Hp a multiple of 32.
+ */
+int moonep_int_grouped_gemm_swiglu(const moonep_shape* shape, const int8_t* xq,
+                                   const float* xscales, const int32_t* src_index,
+                                   const int8_t* wq, const float* wscales,
+                                   const int32_t* cu_seqlens, void* act, void* h_saved, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/*
+ * Dense product on 8-bit operands, for what every token passes (a shared expert):
+ *   c = x @ W + add,  x `rows` token rows of width H, W row 0 of the weights [H, Hp]
+ *   add  in   NULL or float32 [rows, Hp]; may be c itself, and must not overlap it otherwise
+ *   c    out  float32 [rows, Hp]: the product as in moonep_int_grouped_gemm, then the sum,
+ *             rounded once more
+ * Only H, Hp and dtype of the shape play a part.
+ */
+int moonep_int_gemm(const moonep_shape* shape, int64_t rows, const int8_t* xq,
+                    const float* xscales, const int8_t* wq, const float* wscales,
+                    const float* add, float* c, void* stream);
+
+/* The same for a gate/up projection [H, 2*Hp] (ffn shape), with the SwiGLU in its epilogue:
+ * act dtype [rows, Hp], h_saved NULL or dtype [rows, 2*Hp]. Requires Hp a multiple of 32. */
+int moonep_int_gemm_swiglu(const moonep_shape* shape, int64_t rows, const int8_t* xq,
+                           const float* xscales, const int8_t* wq, const float* wscales, void* act,
+                           void* h_saved, void* stream);
+
+/*
+ * Gradient rows for the product back through 8-bit weights [H, Hp], which are constants of
+ * the backward pass (frozen experts; the rounding of x counts as the identity):
+ *   dx[p] = gate_p * sum_n dc[p][n] * wscales[row][n] * w[row][:, n]
+ * This call forms g[n] = dc[n] * wscales[row of p][n] in float32 and holds it as a token row
+ * of width Hp, whose scale is then multiplied by the position's gate. The product follows as
+ * moonep_int_grouped_gemm of the shape with H and Hp exchanged, on the weights of
+ * moonep_int_transpose_weight, with src_index and wscales NULL: float32 [R*SK, H].
+ *   src         in   dtype: with src_index the tokens' gradient [N, Hp], position p reading
+ *                    row src_index[p] / K; with src_index NULL one row per position,
+ *                    [R*SK, Hp]
+ *   gates       in   NULL (1) or float32 [N, K]; needs src_index
+ *   wscales     in   scales of the weights [H, Hp]
+ *   cu_seqlens  in   from moonep_plan, or NULL: every position belongs to weight row 0
+ *   q, scales   out  token rows [R*SK, 128*ceil(Hp/128)] and [R*SK]; positions behind a
+ *                    rank's last row are left as they were
+ * A position whose src_index is not in [0, N*K) gets values and a scale of 0. Hp at most
+ * 131072 (MOONEP_ELIMIT). Training layers only.
+ */
+int moonep_int_quantize_grad(const moonep_shape* shape, const void* src, const int32_t* src_index,
+                             const float* gates, const float* wscales, const int32_t* cu_seqlens,
+                             int8_t* q, float* scales, void* stream);
+
+/*
  * ---- Process-global prefetch-slot pool ----------------------------------------
  * The prefetch slots of every layer come from one process-global pool, so the
  * extra memory is R*B expert weights per projection in total, not per layer,

@@ -1,0 +1,758 @@
+// Experts in 8-bit integers on gfx950: token rows and weights as whole numbers with a scale per
+// row and per column, prefetch and transposition of such weights, the grouped and the dense
+// product on them (v_mfma_i32_16x16x64_i8), and the gradient rows for the product back through
+// frozen weights. Layouts: moonep.h, "Experts in 8-bit integers"; a 16-column x 64-k block of a
+// weight is 1 KiB in the order in which a wavefront's lanes take the operand.
+#include <type_traits>
+
+#include "common.h"
+#include "lds_dma.h"
+
+namespace moonep {
+
+constexpr int kIntThreads = 256;
+constexpr int kIntMaxK = 131072;             // 127 * 127 * 131072 < 2^31: sums stay exact
+constexpr float kIntLeast = 0x1p-126f;       // the smallest scale
+constexpr uint32_t kIntNan = 0x7FC00000u;
+typedef float v4f_t __attribute__((ext_vector_type(4)));
+
+// ---- rounding to 8 bits
+//
+// Scale of magnitudes up to amax_bits (as bits; integer order ranks Inf and NaN highest).
+__device__ inline float int_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return __uint_as_float(kIntNan);
+  return fmaxf(__uint_as_float(amax_bits) / 127.0f, kIntLeast);
+}
+
+// The whole number nearest to the exact x / s, ties to even; inv = 1 / s in float32. x * inv is
+// off by a few units in its last place, so its nearest whole number is at most one away. The
+// remainder x - q s is exact in one FMA: it is a multiple of both numbers' last places and at
+// most about s (and a multiple of 2^-149 at the low end). It decides, so the choice is that of
+// exact arithmetic and does not depend on how the quotient was formed.
+__device__ inline int int_round(float x, float s, float inv) {
+  float q = rintf(x * inv);
+  const float r = fmaf(-q, s, x), twice = 2.0f * fabsf(r);
+  int w = int(q);
+  if (twice > s || (twice == s && (w & 1))) w += r > 0.0f ? 1 : -1;
+  return max(-127, min(127, w));
+}
+
+__device__ inline uint32_t int_mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+__device__ inline uint32_t wave_max(uint32_t m) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = max(m, uint32_t(__shfl_xor(int(m), d, 64)));
+  return m;
+}
+
+// A row's 16-byte vector as floats: 8 bfloat16 or 4 float32.
+template <bool BF16>
+struct RowVec {
+  static constexpr int N = BF16 ? 8 : 4;
+  uint4 raw;
+  __device__ float at(int i) const {
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    if (BF16) return __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+    return __uint_as_float(u[i]);
+  }
+};
+
+// N whole numbers as bytes
+template <int N>
+__device__ inline void int_store(int8_t* at, const int* w) {
+  uint32_t p[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    p[i] = uint32_t(w[4 * i] & 255) | uint32_t(w[4 * i + 1] & 255) << 8 |
+           uint32_t(w[4 * i + 2] & 255) << 16 | uint32_t(w[4 * i + 3]) << 24;
+  if constexpr (N == 8) *reinterpret_cast<uint2*>(at) = make_uint2(p[0], p[1]);
+  else *reinterpret_cast<uint32_t*>(at) = p[0];
+}
+
+// One wavefront per row, which holds it in registers between the maximum and the rounding, VPL
+// vectors a lane; VPL 0: rows too wide for that are read twice.
+template <bool BF16, int VPL>
+__global__ __launch_bounds__(kIntThreads) void int_quantize_kernel(const uint4* __restrict__ src,
+                                                                   int64_t rows, int nvec, int nout,
+                                                                   int8_t* __restrict__ q,
+                                                                   float* __restrict__ scales) {
+  typedef RowVec<BF16> V;
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = blockIdx.x * int64_t(kIntThreads / 64) + (threadIdx.x >> 6); r < rows;
+       r += int64_t(gridDim.x) * (kIntThreads / 64)) {
+    const uint4* in = src + r * nvec;
+    int8_t* out = q + r * nout * V::N;
+    V held[VPL ? VPL : 1];
+    uint32_t m = 0;
+    auto take = [&](int c) { return V{c < nvec ? in[c] : make_uint4(0, 0, 0, 0)}; };
+    auto most = [&](const V& v) {
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) m = max(m, int_mag(v.at(i)));
+    };
+    if constexpr (VPL > 0) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) held[i] = take(lane + 64 * i);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) most(held[i]);
+    } else {
+      for (int c = lane; c < nvec; c += 64) most(take(c));
+    }
+    const float s = int_scale(wave_max(m));
+    const float inv = 1.0f / s;
+    const bool good = s == s;
+    auto put = [&](int c, const V& v) {
+      int w[V::N];
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) w[i] = good ? int_round(v.at(i), s, inv) : 0;
+      if (c < nout) int_store<V::N>(out + c * V::N, w);
+    };
+    if constexpr (VPL > 0) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i * 64 < nout) put(lane + 64 * i, held[i]);
+    } else {
+      for (int c = lane; c < nout; c += 64) put(c, take(c));
+    }
+    if (lane == 0) scales[r] = s;
+  }
+}
+
+// ---- gradient rows
+struct IntGradArgs {
+  const uint4* src;
+  const int32_t* src_index;
+  const float* gates;
+  const float* ws;
+  const int32_t* cu;
+  int8_t* q;
+  float* scales;
+  int R, E, B, SK, K, nvec, nout, wscols;
+  int64_t NK;
+};
+
+// The view row of position pos of a rank: the last i with cu[i] <= pos, or -1 behind the last
+// row. Each step looks at 64 entries at once.
+__device__ inline int segment_of(const int32_t* cu, int EB, int pos, int lane) {
+  int lo = 0, n = EB + 1;
+  while (n > 1) {
+    const int stride = (n + 63) / 64;
+    const int at = lane * stride;
+    const uint64_t le = __ballot(at < n && cu[min(lo + at, EB)] <= pos);
+    if (le == 0) return -1;       // not a plan's cu_seqlens, which begin at 0
+    const int c = 63 - __clzll(le);
+    lo += c * stride;
+    n = min(stride, n - c * stride);
+  }
+  return lo < EB ? lo : -1;
+}
+
+// One wavefront per position: the upstream row times the scales of its expert's columns,
+// rounded as int_quantize_kernel rounds.
+template <bool BF16, int VPL>
+__global__ __launch_bounds__(kIntThreads) void int_quantize_grad_kernel(IntGradArgs a) {
+  typedef RowVec<BF16> V;
+  const int lane = threadIdx.x & 63;
+  const int64_t stride = int64_t(gridDim.x) * (kIntThreads / 64);
+  for (int64_t p = blockIdx.x * int64_t(kIntThreads / 64) + (threadIdx.x >> 6); p < a.NK; p += stride) {
+    int wrow = 0;
+    if (a.cu) {
+      const int rank = int(p / a.SK), EB = a.E + a.B;
+      const int i = segment_of(a.cu + int64_t(rank) * (EB + 1), EB, int(p % a.SK), lane);
+      if (i < 0) continue;
+      wrow = i < a.E ? i : a.E + rank * a.B + (i - a.E);
+    }
+    int64_t row = p;
+    float gate = 1.0f;
+    bool there = true;
+    if (a.src_index) {
+      const int u = a.src_index[p];
+      there = u >= 0 && u < a.NK;
+      row = there ? u / a.K : 0;
+      if (a.gates && there) gate = a.gates[u];
+    }
+    const uint4* in = a.src + row * a.nvec;
+    const v4f_t* ws = reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.wscols);
+    int8_t* out = a.q + p * a.nout * V::N;
+    struct Held { float v[V::N]; } held[VPL ? VPL : 1];
+    uint32_t m = 0;
+    auto take = [&](int c) {
+      Held h;
+      const bool in_row = there && c < a.nvec;
+      const V v{in_row ? in[c] : make_uint4(0, 0, 0, 0)};
+#pragma unroll
+      for (int j = 0; j < V::N / 4; ++j) {
+        const v4f_t s = in_row ? ws[c * (V::N / 4) + j] : v4f_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h.v[4 * j + i] = v.at(4 * j + i) * s[i];
+      }
+      return h;
+    };
+    auto most = [&](const Held& h) {
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) m = max(m, int_mag(h.v[i]));
+    };
+    if constexpr (VPL > 0) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) held[i] = take(lane + 64 * i);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) most(held[i]);
+    } else {
+      for (int c = lane; c < a.nvec; c += 64) most(take(c));
+    }
+    const float s = int_scale(wave_max(m));
+    const float inv = 1.0f / s;
+    const bool good = s == s;
+    auto put = [&](int c, const Held& h) {
+      int w[V::N];
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) w[i] = good ? int_round(h.v[i], s, inv) : 0;
+      if (c < a.nout) int_store<V::N>(out + c * V::N, w);
+    };
+    if constexpr (VPL > 0) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i * 64 < a.nout) put(lane + 64 * i, held[i]);
+    } else {
+      for (int c = lane; c < a.nout; c += 64) put(c, take(c));
+    }
+    if (lane == 0) a.scales[p] = there ? gate * s : 0.0f;
+  }
+}
+
+// ---- weights (set-up)
+//
+// A workgroup has 64 columns of one expert: their maxima over k, then blocks of 64 lanes x 16 k.
+template <bool BF16>
+__global__ __launch_bounds__(kIntThreads) void int_quantize_weight_kernel(const void* __restrict__ w,
+                                                                          int H, int Hp, int KB, int NB,
+                                                                          int8_t* __restrict__ wq,
+                                                                          float* __restrict__ ws) {
+  __shared__ uint32_t s_max[4][64];
+  __shared__ float s_scale[64];
+  const int64_t e = blockIdx.y;
+  const int n0 = blockIdx.x * 64, t = threadIdx.x;
+  auto value = [&](int k, int n) {
+    if (k >= H || n >= Hp) return 0.0f;
+    const int64_t at = (e * H + k) * Hp + n;
+    return BF16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(w)[at]) << 16)
+                : static_cast<const float*>(w)[at];
+  };
+  uint32_t m = 0;
+  for (int k = t >> 6; k < H; k += 4) m = max(m, int_mag(value(k, n0 + (t & 63))));
+  s_max[t >> 6][t & 63] = m;
+  __syncthreads();
+  if (t < 64) {
+    const float s = int_scale(max(max(s_max[0][t], s_max[1][t]), max(s_max[2][t], s_max[3][t])));
+    s_scale[t] = s;
+    if (n0 + t < NB * 16) ws[e * NB * 16 + n0 + t] = n0 + t < Hp ? s : 0.0f;
+  }
+  __syncthreads();
+  const int j = t >> 6, lane = t & 63, nb = n0 / 16 + j;
+  if (nb >= NB) return;
+  const int n = nb * 16 + (lane & 15);
+  const float s = s_scale[n - n0], inv = 1.0f / s;
+  for (int kb = 0; kb < KB; ++kb) {
+    int v[16];
+#pragma unroll
+    for (int b = 0; b < 16; ++b)
+      v[b] = s == s ? int_round(value(kb * 64 + 16 * (lane >> 4) + b, n), s, inv) : 0;
+    int8_t* at = wq + ((e * NB + nb) * KB + kb) * 1024 + lane * 16;
+    int_store<8>(at, v);
+    int_store<8>(at + 8, v + 8);
+  }
+}
+
+// One thread per 16 bytes of the result: lane of block (h / 16, n / 64) has column h of the
+// transposed weight and 16 consecutive n, which are byte h % 16 of 16 neighbouring lanes of one
+// block of the source.
+__global__ __launch_bounds__(kIntThreads) void int_transpose_weight_kernel(const int8_t* __restrict__ wq,
+                                                                           int KB, int NB, int KBt,
+                                                                           int NBt,
+                                                                           int8_t* __restrict__ wqt) {
+  const int64_t e = blockIdx.y;
+  const int64_t total = int64_t(NBt) * KBt * 64;
+  for (int64_t i = blockIdx.x * int64_t(kIntThreads) + threadIdx.x; i < total;
+       i += int64_t(gridDim.x) * kIntThreads) {
+    const int lane = int(i & 63), kb = int((i >> 6) % KBt), nb = int((i >> 6) / KBt);
+    const int h = nb * 16 + (lane & 15), n16 = kb * 4 + (lane >> 4);     // n = 16 * n16 + b
+    int v[16];
+    const int8_t* from = wq + ((e * NB + min(n16, NB - 1)) * KB + h / 64) * 1024 +
+                         ((h / 16) % 4) * 256 + h % 16;
+#pragma unroll
+    for (int b = 0; b < 16; ++b) v[b] = n16 < NB ? from[b * 16] : 0;
+    int8_t* at = wqt + (e * total + i) * 16;
+    int_store<8>(at, v);
+    int_store<8>(at + 8, v + 8);
+  }
+}
+
+// Copies of home rows into used prefetch slots, values and (svec > 0) scales in one launch.
+__global__ __launch_bounds__(kIntThreads) void int_prefetch_kernel(const int32_t* __restrict__ replica,
+                                                                   int RB, int E, uint4* wq,
+                                                                   int64_t qvec, uint4* ws,
+                                                                   int64_t svec) {
+  const int64_t stride = int64_t(gridDim.x) * kIntThreads;
+  const int64_t i0 = int64_t(blockIdx.x) * kIntThreads + threadIdx.x;
+  for (int s = 0; s < RB; ++s) {
+    const int e = replica[s];
+    if (e < 0 || e >= E) continue;
+    for (int64_t i = i0; i < qvec + svec; i += stride) {
+      if (i < qvec) wq[(int64_t(E) + s) * qvec + i] = wq[int64_t(e) * qvec + i];
+      else ws[(int64_t(E) + s) * svec + i - qvec] = ws[int64_t(e) * svec + i - qvec];
+    }
+  }
+}
+
+// ---- products
+struct IntArgs {
+  const int8_t* xq;
+  const float* xs;
+  const int32_t* src_index;
+  const int8_t* wq;
+  const float* ws;       // NULL: 1
+  const float* add;      // NULL: nothing added
+  float* c;
+  void* act;             // SwiGLU: dtype [., W/2], and c is not written
+  void* h_saved;         // SwiGLU: NULL or dtype [., W]
+  int K, W, NB, KB;      // columns of the weight, blocks of 16 of them, blocks of 64 k
+  int64_t NK;            // positions
+  const int32_t* cu;     // NULL: NK positions, all of weight row 0
+  int R, E, B, SK;
+};
+
+// What a product's epilogue makes of its sums.
+enum IntOut { kIntFloat, kIntSwigluBf16, kIntSwigluF32 };
+
+// (sum * row scale) * column scale, 4 columns of one row
+__device__ inline v4f_t int_scaled(v4i_t acc, float sa, v4f_t sw) {
+  v4f_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (float(acc[i]) * sa) * sw[i];
+  return r;
+}
+
+__device__ inline uint32_t bf16_pair(float a, float b) { return bf16_rne_any(a) | bf16_rne_any(b) << 16; }
+
+template <int OUT>
+__device__ inline void store4(void* base, int64_t at, v4f_t v) {
+  if constexpr (OUT == kIntSwigluBf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) =
+        make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+  else
+    *reinterpret_cast<v4f_t*>(static_cast<float*>(base) + at) = v;
+}
+
+// ---- few rows per expert: no list of work. Work items are (share of the rows, segment of the
+// view, J blocks of 16 columns), dealt out to the workgroups in turn; a workgroup's threads look
+// up one item's cu_seqlens each and list the ones that have rows. A workgroup's four
+// wavefronts take blocks of 16 rows; where there are fewer than three, the wavefronts of a block
+// share its k-blocks in turn and their sums are added. Operands go straight to registers,
+// U blocks of 64 k at a time.
+constexpr int kIntRows = 64;      // rows at a time
+constexpr int kIntItems = 256;    // items looked up at a time
+
+// Block j of item t: with SwiGLU and J = 2 a gate block and its up block, 32 columns further.
+template <int J, int OUT>
+__device__ inline int item_block(int t, int j) {
+  return OUT != kIntFloat && J == 2 ? 4 * (t >> 1) + (t & 1) + 2 * j : J * t + j;
+}
+
+template <int J, int U, int OUT>
+__device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v, int m0_v, int n,
+                                    int t_v, v4i_t (*s_part)[J][64]) {
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kb = lane >> 4, r16 = lane & 15;
+  const int rowbase = __builtin_amdgcn_readfirstlane(rowbase_v);
+  const int wrow = __builtin_amdgcn_readfirstlane(wrow_v);
+  const int m0 = __builtin_amdgcn_readfirstlane(m0_v), t = __builtin_amdgcn_readfirstlane(t_v);
+  const int rows = __builtin_amdgcn_readfirstlane(min(kIntRows, n - m0));
+  const int split = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;   // wavefronts per block of rows
+  const int part = w % split, r0 = w / split * 16;
+  const bool work = r0 < rows;    // uniform
+  const int64_t pos = int64_t(rowbase) + m0 + r0 + r16;
+  bool in = work && r0 + r16 < rows;
+  const bool store = in;
+  int64_t arow = pos;
+  v4i_t acc[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) acc[j] = v4i_t{0, 0, 0, 0};
+  if (work) {
+    if (a.src_index) {
+      const int u = in ? a.src_index[pos] : -1;
+      in = u >= 0 && u < a.NK;
+      arow = in ? u / a.K : 0;
+    }
+    const v4i_t* xq = reinterpret_cast<const v4i_t*>(a.xq) + arow * a.KB * 4 + kb;
+    const v4i_t* wq[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      wq[j] = reinterpret_cast<const v4i_t*>(a.wq) + lane +
+              (int64_t(wrow) * a.NB + min(item_block<J, OUT>(t, j), a.NB - 1)) * a.KB * 64;
+    // KB is even; a wavefront takes runs of U blocks
+    for (int c0 = part * U; c0 < a.KB; c0 += split * U) {
+      v4i_t fa[U], fb[U][J];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const bool there = c0 + k < a.KB;   // uniform
+        fa[k] = there && in ? xq[(c0 + k) * 4] : v4i_t{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < J; ++j) fb[k][j] = there ? wq[j][(c0 + k) * 64] : v4i_t{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int j = 0; j < J; ++j)      // operands swapped: a lane holds 4 columns of one row
+          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[k][j], fa[k], acc[j], 0, 0, 0);
+    }
+  }
+  if (split > 1) {       // uniform
+    if (part > 0)
+#pragma unroll
+      for (int j = 0; j < J; ++j) s_part[w - 1][j][lane] = acc[j];
+    __syncthreads();
+    if (part == 0)
+      for (int o = 1; o < split; ++o)
+#pragma unroll
+        for (int j = 0; j < J; ++j) acc[j] += s_part[w + o - 1][j][lane];
+    __syncthreads();     // read before the next entry's sums
+  }
+  if (!store || part != 0) return;
+  const float sa = in ? a.xs[arow] : 0.0f;
+  v4f_t v[J];
+  int col[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int blk = item_block<J, OUT>(t, j);
+    col[j] = blk * 16 + 4 * kb;
+    const v4f_t sw = a.ws ? *reinterpret_cast<const v4f_t*>(a.ws + (int64_t(wrow) * a.NB + min(blk, a.NB - 1)) * 16 + 4 * kb)
+                          : v4f_t{1.f, 1.f, 1.f, 1.f};
+    v[j] = int_scaled(acc[j], sa, sw);
+  }
+  if constexpr (OUT == kIntFloat) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (col[j] < a.W) {
+        const int64_t at = pos * a.W + col[j];
+        if (a.add) v[j] += *reinterpret_cast<const v4f_t*>(a.add + at);
+        *reinterpret_cast<v4f_t*>(a.c + at) = v[j];
+      }
+  } else {
+    if (a.h_saved)
+#pragma unroll
+      for (int j = 0; j < J; ++j) store4<OUT>(a.h_saved, pos * a.W + col[j], v[j]);
+#pragma unroll
+    for (int j = 0; j < J / 2; ++j) {
+      v4f_t s;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = swiglu_f32(v[j][i], v[j + J / 2][i]);
+      // gate column c stands for intermediate column 32 * (c / 64) + c % 32
+      store4<OUT>(a.act, pos * (a.W / 2) + col[j] / 64 * 32 + col[j] % 32, s);
+    }
+  }
+}
+
+struct IntItem {
+  int32_t rowbase, wrow, m0, n;
+};
+
+template <int J, int U, int OUT>
+__global__ __launch_bounds__(256) void int_gemm_kernel(IntArgs a, int shares) {
+  __shared__ __align__(16) v4i_t s_part[3][J][64];
+  __shared__ IntItem s_item[kIntItems];
+  __shared__ int s_t[kIntItems];
+  __shared__ int s_wave[4];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int NT = (a.NB + J - 1) / J, EB = a.E + a.B;
+  const int64_t segs = a.cu ? int64_t(a.R) * EB : 1;
+  const int64_t total = segs * shares * NT;
+  for (int64_t t0 = blockIdx.x; t0 < total; t0 += int64_t(gridDim.x) * kIntItems) {
+    const int64_t t = t0 + int64_t(threadIdx.x) * gridDim.x;
+    IntItem it{0, 0, 0, 0};
+    int tn = 0;
+    if (t < total) {
+      // shares slowest: the empty ones of short segments lie together, over all CUs
+      const int64_t rest = t / NT;
+      const int seg = int(rest % segs), share = int(rest / segs);
+      tn = int(t % NT);
+      if (a.cu) {
+        const int rank = seg / EB, i = seg % EB;
+        const int c0 = a.cu[int64_t(rank) * (EB + 1) + i];
+        it = IntItem{rank * a.SK + c0, i < a.E ? i : a.E + rank * a.B + (i - a.E), share * kIntRows,
+                     a.cu[int64_t(rank) * (EB + 1) + i + 1] - c0};
+      } else {
+        it = IntItem{0, 0, share * kIntRows, int(a.NK)};
+      }
+    }
+    const bool some = it.m0 < it.n;
+    const uint64_t have = __ballot(some);
+    if (lane == 0) s_wave[w] = __popcll(have);
+    __syncthreads();
+    int at = __popcll(have & ((uint64_t(1) << lane) - 1)), count = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < w) at += s_wave[i];
+      count += s_wave[i];
+    }
+    if (some) {
+      s_item[at] = it;
+      s_t[at] = tn;
+    }
+    __syncthreads();
+    for (int i = 0; i < count; ++i) {
+      const IntItem te = s_item[i];
+      for (int m0 = te.m0; m0 < te.n; m0 += shares * kIntRows)
+        int_few_rows<J, U, OUT>(a, te.rowbase, te.wrow, m0, te.n, s_t[i], s_part);
+    }
+    __syncthreads();     // the list is read before the next one
+  }
+}
+
+static int int_grid(int64_t work, int64_t cap) {
+  const int64_t blocks = (work + kIntThreads - 1) / kIntThreads;
+  return int(blocks < 1 ? 1 : (blocks > cap ? cap : blocks));
+}
+
+inline int64_t int_kb(int width) { return 2 * k_tiles(width); }      // blocks of 64 k
+inline int64_t int_nb(int width) { return (int64_t(width) + 15) / 16; }
+
+template <int OUT>
+static int int_product(const IntArgs& a, hipStream_t strm) {
+  const int cus = device_cus();
+  if (cus <= 0) return MOONEP_EHIP;
+  // a segment's rows are shared out twice as finely as an even plan would need
+  const int64_t held = a.cu ? int64_t(a.E) + a.R : 1;      // a plan has at most this many segments
+  const int64_t share = (2 * a.NK + held * kIntRows - 1) / (held * kIntRows);
+  const int shares = int(share < 64 ? share : 64);
+  int_gemm_kernel<4, 4, OUT><<<cus * 8, 256, 0, strm>>>(a, shares);
+  return launch_status();
+}
+
+// Vectors per lane that hold `nout` vectors of a row, as an argument of f (0: too many)
+template <typename F>
+static void with_vectors(int64_t nout, F f) {
+  const int64_t per = (nout + 63) / 64;
+  if (per <= 1) f(std::integral_constant<int, 1>());
+  else if (per <= 2) f(std::integral_constant<int, 2>());
+  else if (per <= 4) f(std::integral_constant<int, 4>());
+  else if (per <= 8) f(std::integral_constant<int, 8>());
+  else if (per <= 16) f(std::integral_constant<int, 16>());
+  else f(std::integral_constant<int, 0>());
+}
+
+static int int_row_grid(int64_t rows) {
+  const int64_t blocks = (rows + kIntThreads / 64 - 1) / (kIntThreads / 64);
+  return int(blocks < 65536 ? blocks : 65536);
+}
+
+// The rules all products share; W the weight's columns. MOONEP_OK leaves *a filled but for the
+// outputs, the plan and the add.
+static int int_operands(const moonep_shape& s, int64_t W, const int8_t* xq, const float* xscales,
+                        const int32_t* src_index, const int8_t* wq, const float* wscales,
+                        IntArgs* a) {
+  if (!aligned16(xq) || !aligned16(xscales) || !aligned16(wq) ||
+      (wscales && !aligned16(wscales)) || (src_index && !aligned16(src_index)))
+    return MOONEP_EINVAL;
+  *a = IntArgs{};
+  a->xq = xq;
+  a->xs = xscales;
+  a->src_index = src_index;
+  a->wq = wq;
+  a->ws = wscales;
+  a->K = s.K;
+  a->W = int(W);
+  a->NB = int(int_nb(int(W)));
+  a->KB = int(int_kb(s.H));
+  return MOONEP_OK;
+}
+
+static void int_plan(const moonep_shape& s, const int32_t* cu, IntArgs* a) {
+  a->NK = int64_t(s.R) * s.S * s.K;
+  a->cu = cu;
+  a->R = s.R;
+  a->E = s.E;
+  a->B = s.B;
+  a->SK = s.S * s.K;
+}
+
+}  // namespace moonep
+
+using namespace moonep;
+
+extern "C" int moonep_int_quantize(const moonep_shape* shape, int64_t rows, int32_t width,
+                                   const void* src, int8_t* q, float* scales, void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const bool bf16 = shape->dtype == MOONEP_BF16;
+  const int vec = bf16 ? 8 : 4;
+  if (rows < 0 || rows > INT32_MAX || width < vec || width % vec) return MOONEP_EINVAL;
+  if (width > kIntMaxK) return MOONEP_ELIMIT;
+  if (rows == 0) return MOONEP_OK;
+  if (!aligned16(src) || !aligned16(q) || !aligned16(scales)) return MOONEP_EINVAL;
+  const uint4* in = static_cast<const uint4*>(src);
+  const int nvec = width / vec, nout = int(k_tiles(width)) * 128 / vec;
+  with_vectors(nout, [&](auto v) {
+    constexpr int VPL = decltype(v)::value;
+    if (bf16)
+      int_quantize_kernel<true, VPL><<<int_row_grid(rows), kIntThreads, 0, as_stream(stream)>>>(in, rows, nvec, nout, q, scales);
+    else
+      int_quantize_kernel<false, VPL><<<int_row_grid(rows), kIntThreads, 0, as_stream(stream)>>>(in, rows, nvec, nout, q, scales);
+  });
+  return launch_status();
+}
+
+extern "C" int moonep_int_quantize_weight(const moonep_shape* shape, const void* w, int8_t* wq,
+                                          float* wscales, void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (!aligned16(w) || !aligned16(wq) || !aligned16(wscales)) return MOONEP_EINVAL;
+  const int KB = int(int_kb(s.H)), NB = int(int_nb(s.Hp));
+  const dim3 grid((NB + 3) / 4, s.E);
+  if (s.dtype == MOONEP_BF16)
+    int_quantize_weight_kernel<true><<<grid, kIntThreads, 0, as_stream(stream)>>>(w, s.H, s.Hp, KB, NB, wq, wscales);
+  else
+    int_quantize_weight_kernel<false><<<grid, kIntThreads, 0, as_stream(stream)>>>(w, s.H, s.Hp, KB, NB, wq, wscales);
+  return launch_status();
+}
+
+extern "C" int moonep_int_transpose_weight(const moonep_shape* shape, const int8_t* wq, int8_t* wqt,
+                                           void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (s.H > kIntMaxK || s.Hp > kIntMaxK) return MOONEP_ELIMIT;
+  if (!aligned16(wq) || !aligned16(wqt)) return MOONEP_EINVAL;
+  const int KBt = int(int_kb(s.Hp)), NBt = int(int_nb(s.H));
+  const dim3 grid(int_grid(int64_t(KBt) * NBt * 64, 1024), s.E);
+  int_transpose_weight_kernel<<<grid, kIntThreads, 0, as_stream(stream)>>>(
+      wq, int(int_kb(s.H)), int(int_nb(s.Hp)), KBt, NBt, wqt);
+  return launch_status();
+}
+
+extern "C" int moonep_int_prefetch_weight(const moonep_shape* shape, const int32_t* replica_expert,
+                                          int8_t* wq, float* wscales, void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (s.B == 0) return MOONEP_OK;
+  if (!aligned16(replica_expert) || !aligned16(wq) || (wscales && !aligned16(wscales)))
+    return MOONEP_EINVAL;
+  const int64_t qvec = int_nb(s.Hp) * int_kb(s.H) * 64;
+  const int64_t svec = wscales ? int_nb(s.Hp) * 4 : 0;
+  int_prefetch_kernel<<<int_grid(qvec + svec, 2048), kIntThreads, 0, as_stream(stream)>>>(
+      replica_expert, s.R * s.B, s.E, reinterpret_cast<uint4*>(wq), qvec,
+      reinterpret_cast<uint4*>(wscales), svec);
+  return launch_status();
+}
+
+extern "C" int moonep_int_grouped_gemm(const moonep_shape* shape, const int8_t* xq,
+                                       const float* xscales, const int32_t* src_index,
+                                       const int8_t* wq, const float* wscales,
+                                       const int32_t* cu_seqlens, float* c, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (!aligned16(cu_seqlens) || !aligned16(ws)) return MOONEP_EINVAL;
+  if (ws_bytes < ws_layout(s).total) return MOONEP_EWORKSPACE;
+  if (s.S == 0) return MOONEP_OK;
+  IntArgs a;
+  st = int_operands(s, s.Hp, xq, xscales, src_index, wq, wscales, &a);
+  if (st || !aligned16(c)) return MOONEP_EINVAL;
+  int_plan(s, cu_seqlens, &a);
+  a.c = c;
+  return int_product<kIntFloat>(a, as_stream(stream));
+}
+
+extern "C" int moonep_int_grouped_gemm_swiglu(const moonep_shape* shape, const int8_t* xq,
+                                              const float* xscales, const int32_t* src_index,
+                                              const int8_t* wq, const float* wscales,
+                                              const int32_t* cu_seqlens, void* act, void* h_saved,
+                                              void* ws, size_t ws_bytes, void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (s.Hp % kSwigluBlock || s.Hp > INT32_MAX / 2) return MOONEP_EINVAL;
+  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (!aligned16(cu_seqlens) || !aligned16(ws)) return MOONEP_EINVAL;
+  if (ws_bytes < ws_layout(s).total) return MOONEP_EWORKSPACE;
+  if (s.S == 0) return MOONEP_OK;
+  IntArgs a;
+  st = int_operands(s, 2 * int64_t(s.Hp), xq, xscales, src_index, wq, wscales, &a);
+  if (st || !aligned16(act) || (h_saved && !aligned16(h_saved))) return MOONEP_EINVAL;
+  int_plan(s, cu_seqlens, &a);
+  a.act = act;
+  a.h_saved = h_saved;
+  return s.dtype == MOONEP_BF16 ? int_product<kIntSwigluBf16>(a, as_stream(stream))
+                                : int_product<kIntSwigluF32>(a, as_stream(stream));
+}
+
+extern "C" int moonep_int_gemm(const moonep_shape* shape, int64_t rows, const int8_t* xq,
+                               const float* xscales, const int8_t* wq, const float* wscales,
+                               const float* add, float* c, void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (rows < 0 || rows > INT32_MAX) return MOONEP_EINVAL;
+  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (rows == 0) return MOONEP_OK;
+  IntArgs a;
+  st = int_operands(s, s.Hp, xq, xscales, nullptr, wq, wscales, &a);
+  if (st || !aligned16(c) || (add && !aligned16(add))) return MOONEP_EINVAL;
+  a.NK = rows;
+  a.add = add;
+  a.c = c;
+  return int_product<kIntFloat>(a, as_stream(stream));
+}
+
+extern "C" int moonep_int_gemm_swiglu(const moonep_shape* shape, int64_t rows, const int8_t* xq,
+                                      const float* xscales, const int8_t* wq, const float* wscales,
+                                      void* act, void* h_saved, void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (rows < 0 || rows > INT32_MAX || s.Hp % kSwigluBlock || s.Hp > INT32_MAX / 2)
+    return MOONEP_EINVAL;
+  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (rows == 0) return MOONEP_OK;
+  IntArgs a;
+  st = int_operands(s, 2 * int64_t(s.Hp), xq, xscales, nullptr, wq, wscales, &a);
+  if (st || !aligned16(act) || (h_saved && !aligned16(h_saved))) return MOONEP_EINVAL;
+  a.NK = rows;
+  a.act = act;
+  a.h_saved = h_saved;
+  return s.dtype == MOONEP_BF16 ? int_product<kIntSwigluBf16>(a, as_stream(stream))
+                                : int_product<kIntSwigluF32>(a, as_stream(stream));
+}
+
+extern "C" int moonep_int_quantize_grad(const moonep_shape* shape, const void* src,
+                                        const int32_t* src_index, const float* gates,
+                                        const float* wscales, const int32_t* cu_seqlens, int8_t* q,
+                                        float* scales, void* stream) {
+  int st = validate(shape);
+  if (st) return st;
+  const moonep_shape& s = *shape;
+  if (s.mode != MOONEP_TRAIN) return MOONEP_EMODE;
+  if (s.Hp > kIntMaxK) return MOONEP_ELIMIT;
+  if (s.S == 0) return MOONEP_OK;
+  if (!aligned16(src) || !aligned16(wscales) || !aligned16(q) || !aligned16(scales) ||
+      (src_index && !aligned16(src_index)) || (gates && !aligned16(gates)) ||
+      (cu_seqlens && !aligned16(cu_seqlens)) || (gates && !src_index))
+    return MOONEP_EINVAL;
+  const bool bf16 = s.dtype == MOONEP_BF16;
+  const int vec = bf16 ? 8 : 4;
+  IntGradArgs a{static_cast<const uint4*>(src), src_index, gates, wscales, cu_seqlens, q, scales,
+                s.R, s.E, s.B, s.S * s.K, s.K, s.Hp / vec, int(k_tiles(s.Hp)) * 128 / vec,
+                int(int_nb(s.Hp)) * 16, int64_t(s.R) * s.S * s.K};
+  const int grid = int_row_grid(a.NK);
+  with_vectors(a.nout, [&](auto v) {
+    constexpr int VPL = decltype(v)::value;
+    if (bf16) int_quantize_grad_kernel<true, VPL><<<grid, kIntThreads, 0, as_stream(stream)>>>(a);
+    else int_quantize_grad_kernel<false, VPL><<<grid, kIntThreads, 0, as_stream(stream)>>>(a);
+  });
+  return launch_status();
+}
