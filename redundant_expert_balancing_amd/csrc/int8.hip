@@ -318,6 +318,11 @@ struct IntArgs {
   int64_t NK;            // positions
   const int32_t* cu;     // NULL: NK positions, all of weight row 0
   int R, E, B, SK;
+  // the tiled form
+  const TileEntry* tiles;   // NULL: 256-row tiles of NK positions, all of weight row 0
+  const int32_t* ntiles;
+  int32_t* qcnt;            // 8 per-XCD tile-queue counters, zero at launch (NULL: static order)
+  int64_t xrows;            // token rows
 };
 
 // What a product's epilogue makes of its sums.
@@ -509,6 +514,320 @@ __global__ __launch_bounds__(256) void int_gemm_kernel(IntArgs a, int shares) {
   }
 }
 
+// ---- tiled form: 256 x 256 output tiles, 8 wavefronts of 128 x 64, 128 k per step. Both operands
+// go to LDS by DMA, two stages: token rows (gathered by src_index) as 128-byte rows with
+// swizzled chunks, weights as the 1 KiB blocks they are stored in, which a wavefront reads back
+// lane by lane. A wavefront holds the fragments of half a step (64 k) and refills them behind
+// its MFMAs; the one barrier of a step comes after the last reads of its stage, so the DMAs of
+// the step after next run under half a step's and a whole step's products.
+constexpr int kNonTemporal = 2;   // buffer cache policy: the output is not read back here
+
+struct IntTile {
+  static constexpr int BM = 256, BN = 256, WAVES = 8, THREADS = 512;
+  static constexpr int FM = 8, FN = 4;                   // 16 x 16 blocks of a wavefront
+  static constexpr int STEPB = 128;                      // bytes of a row per step
+  static constexpr int A_BYTES = BM * STEPB, B_BYTES = BN * STEPB, STAGE = A_BYTES + B_BYTES;
+  static constexpr int ISSUERS = 4;                      // wavefronts that issue the DMAs
+  static constexpr int A_DMAS = A_BYTES / 1024 / ISSUERS, B_DMAS = B_BYTES / 1024 / ISSUERS;
+  static constexpr int kBlockE = 8, kBlockN = 4;         // tile-order block
+};
+
+template <bool GATHER, int OUT>
+__global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArgs a) {
+  typedef IntTile T;
+  constexpr int FM = T::FM, FN = T::FN;
+  __shared__ __align__(1024) char smem[2 * T::STAGE];
+  __shared__ uint32_t s_off[T::BM];                      // byte offsets of the tile's token rows
+  __shared__ float s_sa[T::BM];                          // their scales
+  __shared__ __align__(16) float s_sw[T::BN];            // scales of its columns
+  __shared__ int s_claim;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wid / 4, wn = wid % 4;
+  const int r16 = lane & 15, kb = lane >> 4;
+  const uint32_t lds0 = lds_addr(smem);
+  const int NT = (a.W + T::BN - 1) / T::BN;
+  const int nent = a.tiles ? *a.ntiles : int((a.NK + T::BM - 1) / T::BM);
+  const int total = nent * NT;      // below 2^31 (host)
+  const int nsteps = a.KB / 2;
+  const uint32_t qrow = uint32_t(a.KB) * 64;             // bytes of a token row
+  // The workgroups of one XCD take a contiguous run of tiles per round, from a list of the call
+  // first come first served (position q of XCD x is tile (q / per) * G + x * per + q % per).
+  const int G = gridDim.x, xcd = blockIdx.x % 8, per = G / 8;
+  const bool dyn = a.qcnt != nullptr;
+  auto claim = [&]() {
+    if (tid == 0) {
+      const int q = atomicAdd(a.qcnt + xcd, 1);
+      s_claim = (q / per) * G + xcd * per + q % per;
+    }
+  };
+
+  int rowbase = 0, wrow = 0, rows_valid = 0, n0 = 0;
+  auto place = [&](int tau) {
+    // blocks of kBlockE entries x kBlockN N-tiles
+    const int eb = tau / (T::kBlockE * NT), j = tau % (T::kBlockE * NT);
+    const int ge = min(T::kBlockE, nent - eb * T::kBlockE);
+    const int nb = j / (ge * T::kBlockN), jj = j % (ge * T::kBlockN);
+    const int wb = min(T::kBlockN, NT - nb * T::kBlockN);
+    const int ent = eb * T::kBlockE + jj / wb;
+    n0 = (nb * T::kBlockN + jj % wb) * T::BN;
+    const TileEntry e = a.tiles ? a.tiles[ent] : TileEntry{0, 0, ent * T::BM, int(a.NK)};
+    rowbase = __builtin_amdgcn_readfirstlane(e.rowbase + e.m0);
+    wrow = __builtin_amdgcn_readfirstlane(e.wrow);
+    rows_valid = __builtin_amdgcn_readfirstlane(min(T::BM, e.n - e.m0));
+  };
+  // threads 0..255: a row of the tile each, the others a column's scale
+  int next_u = -1;
+  float next_s = 0.f;
+  uint32_t next_off = kOffNone;
+  auto look_up = [&]() {
+    if (tid < T::BM) {
+      next_u = tid < rows_valid ? (GATHER ? a.src_index[rowbase + tid] : tid) : -1;
+    } else {
+      const int n = n0 + tid - T::BM;
+      next_s = n < a.W ? (a.ws ? a.ws[int64_t(wrow) * a.NB * 16 + n] : 1.0f) : 0.f;
+    }
+  };
+  auto look_up_row = [&]() {
+    if (tid < T::BM) {
+      next_off = kOffNone;
+      next_s = 0.f;
+      if (next_u >= 0 && (!GATHER || next_u < a.NK)) {
+        const uint32_t r = GATHER ? uint32_t(next_u) / uint32_t(a.K) : uint32_t(next_u);
+        next_off = r * qrow;
+        next_s = a.xs[(GATHER ? 0 : rowbase) + int64_t(r)];
+      }
+    }
+  };
+  auto keep = [&]() {
+    if (tid < T::BM) {
+      s_off[tid] = next_off;
+      s_sa[tid] = next_s;
+    } else {
+      s_sw[tid - T::BM] = next_s;
+    }
+  };
+
+  int tau = (G % 8 == 0) ? xcd * per + blockIdx.x / 8 : blockIdx.x;
+  if (dyn) {
+    claim();
+    __syncthreads();
+    tau = __builtin_amdgcn_readfirstlane(s_claim);
+  }
+  if (tau >= total) return;
+  place(tau);
+  look_up();
+  look_up_row();
+  keep();
+  while (true) {
+    __syncthreads();     // the tile's rows are known, and the previous tile's LDS is free
+    const int64_t first = GATHER ? 0 : rowbase;
+    const int64_t span = GATHER ? a.xrows : rows_valid;
+    const __amdgpu_buffer_rsrc_t ars = make_rsrc(a.xq + first * qrow, clamp_bytes(span * qrow));
+    const int nblocks = min(T::BN / 16, a.NB - n0 / 16);
+    const __amdgpu_buffer_rsrc_t brs =
+        make_rsrc(a.wq + (int64_t(wrow) * a.NB + n0 / 16) * a.KB * 1024, uint32_t(nblocks * a.KB) * 1024);
+    uint32_t va[T::A_DMAS];
+    if (wid < T::ISSUERS) {
+#pragma unroll
+      for (int i = 0; i < T::A_DMAS; ++i) {
+        const int row = (wid + T::ISSUERS * i) * 8 + (lane >> 3);
+        const uint32_t off = s_off[row];
+        va[i] = off == kOffNone ? kOffNone : off + ((lane & 7) ^ swz_k(row)) * 16;
+      }
+    }
+    auto issue = [&](int k) {     // step k into stage k % 2
+      if (wid >= T::ISSUERS) return;
+      const uint32_t st = lds0 + (k & 1) * T::STAGE;
+#pragma unroll
+      for (int i = 0; i < T::A_DMAS; ++i)
+        dma16(ars, va[i], uint32_t(k) * T::STEPB, st + (wid + T::ISSUERS * i) * 1024);
+#pragma unroll
+      for (int i = 0; i < T::B_DMAS; ++i) {
+        const int b = wid + T::ISSUERS * i, j = b >> 1;   // half b % 2 of the step, 16-column block j
+        dma16(brs, j < nblocks ? lane * 16 : kOffNone, uint32_t(j * a.KB + 2 * k + (b & 1)) * 1024,
+              st + T::A_BYTES + b * 1024);
+      }
+    };
+    const int row0 = wm * 128, col0 = wn * 64;
+    const bool idle = row0 >= rows_valid || n0 + col0 >= a.W;    // uniform
+    v4i_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = v4i_t{0, 0, 0, 0};
+    issue(0);
+    if (nsteps > 1) issue(1);
+    if (wid < T::ISSUERS) {
+      if (nsteps > 1) wait_vm<T::A_DMAS + T::B_DMAS>();
+      else wait_vm<0>();
+    }
+    __syncthreads();
+    if (dyn) claim();             // the next tile, read behind the loop's barriers
+    if (idle) {
+      for (int k = 0; k < nsteps; ++k) {
+        if (wid < T::ISSUERS) wait_vm<0>();
+        __syncthreads();
+        if (k + 2 < nsteps) issue(k + 2);
+      }
+    } else {
+      v4i_t fa[FM], fb[FN];
+      auto load = [&](int k, int ks) {
+        const char* st = smem + (k & 1) * T::STAGE;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const int row = row0 + i * 16 + r16;
+          fa[i] = *reinterpret_cast<const v4i_t*>(st + row * T::STEPB + (((ks * 4 + kb) ^ swz_k(row)) << 4));
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          fb[j] = *reinterpret_cast<const v4i_t*>(st + T::A_BYTES + ((wn * 4 + j) * 2 + ks) * 1024 + lane * 16);
+      };
+      // every row with the first two column blocks, then with the others: the first blocks'
+      // fragments are refilled under the second half
+      auto products = [&]() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 2 * h; j < 2 * h + 2; ++j)   // operands swapped: a lane holds 4 columns of one row
+              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      };
+      auto interleave = [&]() {
+        __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / 2, 0);
+#pragma unroll
+        for (int q = 0; q < FM + FN / 2; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / 2 - (FM + FN / 2), 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, FN / 2, 0);
+      };
+      load(0, 0);
+      for (int k = 0; k < nsteps; ++k) {
+        products();
+        load(k, 1);
+        interleave();
+        if (wid < T::ISSUERS) wait_vm<0>();     // step k + 1
+        __syncthreads();
+        if (k + 2 < nsteps) issue(k + 2);
+        products();
+        load(k + 1 < nsteps ? k + 1 : k, 0);    // behind the last step: in bounds, not used
+        interleave();
+      }
+    }
+    // ---- epilogue
+    float sa[FM];
+    v4f_t sw[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sa[i] = s_sa[row0 + i * 16 + r16];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sw[j] = *reinterpret_cast<const v4f_t*>(&s_sw[col0 + j * 16 + 4 * kb]);
+    const int rb = rowbase, rv = rows_valid, c0 = n0;
+    tau = dyn ? __builtin_amdgcn_readfirstlane(s_claim) : tau + G;
+    const bool more = tau < total;
+    if (more) {
+      place(tau);
+      look_up();
+    }
+    __syncthreads();     // every wavefront has read the last stage and the tile's scales
+    // The lanes' own 16 x 16 blocks would be stored as 16 pieces of 64 bytes; the wavefronts
+    // exchange 32 rows of each row group at a time through LDS and store whole rows.
+    // Row R of the 64 is row (R / 32) * 128 + 32 * p + R % 32 of the tile.
+    auto put = [&](char* buf, int chunks, int ii, int byte, auto v) {
+      const int R = wm * 32 + ii * 16 + r16;
+      *reinterpret_cast<decltype(v)*>(buf + R * chunks * 16 + (((byte >> 4) ^ r16) << 4) + (byte & 15)) = v;
+    };
+    auto flush = [&](const char* buf, auto chunks_c, int p, __amdgpu_buffer_rsrc_t rs, uint32_t ld,
+                     uint32_t left, auto policy_c, auto add) {
+      constexpr int C = decltype(chunks_c)::value;
+#pragma unroll
+      for (int h = 0; h < 64 * C / T::THREADS; ++h) {
+        const int id = h * T::THREADS + tid, R = id / C, c = id % C;
+        const uint32_t row = (R >> 5) * 128 + p * 32 + (R & 31);
+        const uint32_t off = uint32_t(c) * 16 < left ? row * ld + c * 16 : kOffNone;
+        v4i_t x = *reinterpret_cast<const v4i_t*>(buf + R * C * 16 + ((c ^ (R & 15)) << 4));
+        x = add(x, off);
+        __builtin_amdgcn_raw_buffer_store_b128(x, rs, off, 0, decltype(policy_c)::value);
+      }
+    };
+    auto as_is = [](v4i_t x, uint32_t) { return x; };
+    // rows of `width` elements of eb bytes from column `col`: descriptor, and bytes left in a row
+    auto out_rsrc = [&](void* base, int64_t width, int64_t col, int eb) {
+      return make_rsrc(static_cast<char*>(base) + (rb * width + col) * eb,
+                       clamp_bytes((rv * width - col) * eb));
+    };
+    if constexpr (OUT == kIntFloat) {
+      const __amdgpu_buffer_rsrc_t crs = out_rsrc(a.c, a.W, c0, 4);
+      const __amdgpu_buffer_rsrc_t drs = out_rsrc(const_cast<float*>(a.add ? a.add : a.c), a.W, c0, 4);
+#pragma unroll
+      for (int p = 0; p < FM / 2; ++p) {
+        char* buf = smem + (p & 1) * 65536;
+        if (!idle) {
+#pragma unroll
+          for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              put(buf, 64, ii, (col0 + j * 16 + 4 * kb) * 4, int_scaled(acc[2 * p + ii][j], sa[2 * p + ii], sw[j]));
+        }
+        __syncthreads();
+        if (more && p == 1) look_up_row();
+        if (a.add)
+          flush(buf, std::integral_constant<int, 64>(), p, crs, uint32_t(a.W) * 4, uint32_t(a.W - c0) * 4,
+                std::integral_constant<int, kNonTemporal>(), [&](v4i_t x, uint32_t off) {
+                  const v4i_t y = __builtin_bit_cast(v4i_t, __builtin_amdgcn_raw_buffer_load_b128(drs, off, 0, 0));
+                  return __builtin_bit_cast(v4i_t, __builtin_bit_cast(v4f_t, x) + __builtin_bit_cast(v4f_t, y));
+                });
+        else
+          flush(buf, std::integral_constant<int, 64>(), p, crs, uint32_t(a.W) * 4, uint32_t(a.W - c0) * 4,
+                std::integral_constant<int, kNonTemporal>(), as_is);
+      }
+    } else {
+      constexpr int EB = OUT == kIntSwigluBf16 ? 2 : 4;
+      const __amdgpu_buffer_rsrc_t ars2 = out_rsrc(a.act, a.W / 2, c0 / 2, EB);
+      const __amdgpu_buffer_rsrc_t hrs = out_rsrc(a.h_saved ? a.h_saved : a.act, a.W, c0, EB);
+      auto value = [&](v4f_t v) {
+        if constexpr (EB == 2) return uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+        else return v;
+      };
+      char* hbuf = smem + 64 * 128 * EB;
+#pragma unroll
+      for (int p = 0; p < FM / 2; ++p) {
+        if (!idle) {
+#pragma unroll
+          for (int ii = 0; ii < 2; ++ii) {
+            v4f_t v[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+              v[j] = int_scaled(acc[2 * p + ii][j], sa[2 * p + ii], sw[j]);
+              if (a.h_saved) put(hbuf, 16 * EB, ii, (col0 + j * 16 + 4 * kb) * EB, value(v[j]));
+            }
+            // blocks 0, 1 of the wavefront's 64 columns are gates, 2, 3 their up columns
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              v4f_t s;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[i] = swiglu_f32(v[j][i], v[j + 2][i]);
+              put(smem, 8 * EB, ii, (wn * 32 + j * 16 + 4 * kb) * EB, value(s));
+            }
+          }
+        }
+        __syncthreads();
+        if (more && p == 1) look_up_row();
+        flush(smem, std::integral_constant<int, 8 * EB>(), p, ars2, uint32_t(a.W / 2) * EB,
+              uint32_t(a.W - c0) / 2 * EB, std::integral_constant<int, 0>(), as_is);
+        if (a.h_saved)
+          flush(hbuf, std::integral_constant<int, 16 * EB>(), p, hrs, uint32_t(a.W) * EB,
+                uint32_t(a.W - c0) * EB, std::integral_constant<int, kNonTemporal>(), as_is);
+        if (p + 1 < FM / 2) __syncthreads();     // read before the next rows
+      }
+    }
+    if (!more) break;
+    keep();
+  }
+}
+
 static int int_grid(int64_t work, int64_t cap) {
   const int64_t blocks = (work + kIntThreads - 1) / kIntThreads;
   return int(blocks < 1 ? 1 : (blocks > cap ? cap : blocks));
@@ -517,13 +836,31 @@ static int int_grid(int64_t work, int64_t cap) {
 inline int64_t int_kb(int width) { return 2 * k_tiles(width); }      // blocks of 64 k
 inline int64_t int_nb(int width) { return (int64_t(width) + 15) / 16; }
 
+// ws: the layer's workspace, for a grouped product's tile list; s its shape.
 template <int OUT>
-static int int_product(const IntArgs& a, hipStream_t strm) {
+static int int_product(IntArgs a, const moonep_shape& s, void* ws, hipStream_t strm) {
   const int cus = device_cus();
   if (cus <= 0) return MOONEP_EHIP;
+  const int64_t nt = (int64_t(a.W) + IntTile::BN - 1) / IntTile::BN;
+  const int64_t segs = a.cu ? int64_t(a.E) + a.R : 1;      // a plan has at most this many segments
+  a.xrows = a.src_index ? int64_t(s.R) * s.S : a.NK;
+  const bool tiled = cus % 8 == 0 && a.NK >= 64 * segs &&
+                     // 32-bit offsets of gathered rows and of a tile's outputs, and tile numbers
+                     (!a.src_index || a.xrows * a.KB * 64 < int64_t(kOffNone)) &&
+                     int64_t(IntTile::BM) * a.W * 4 <= int64_t(kOffNone) &&
+                     (a.NK / IntTile::BM + 1 + (a.cu ? int64_t(a.R) * (a.E + a.B) : 0)) * nt < INT32_MAX;
+  if (tiled) {
+    if (a.cu) {
+      const int st = launch_tile_list(s, a.cu, IntTile::BM, ws, strm, &a.tiles, &a.ntiles);
+      if (st) return st;
+      a.qcnt = ws_ptr<int32_t>(ws, ws_layout(s).flags) + kFlagQueue;
+    }
+    if (a.src_index) int_gemm_tiled_kernel<true, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
+    else int_gemm_tiled_kernel<false, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
+    return launch_status();
+  }
   // a segment's rows are shared out twice as finely as an even plan would need
-  const int64_t held = a.cu ? int64_t(a.E) + a.R : 1;      // a plan has at most this many segments
-  const int64_t share = (2 * a.NK + held * kIntRows - 1) / (held * kIntRows);
+  const int64_t share = (2 * a.NK + segs * kIntRows - 1) / (segs * kIntRows);
   const int shares = int(share < 64 ? share : 64);
   int_gemm_kernel<4, 4, OUT><<<cus * 8, 256, 0, strm>>>(a, shares);
   return launch_status();
@@ -665,7 +1002,7 @@ extern "C" int moonep_int_grouped_gemm(const moonep_shape* shape, const int8_t* 
   if (st || !aligned16(c)) return MOONEP_EINVAL;
   int_plan(s, cu_seqlens, &a);
   a.c = c;
-  return int_product<kIntFloat>(a, as_stream(stream));
+  return int_product<kIntFloat>(a, s, ws, as_stream(stream));
 }
 
 extern "C" int moonep_int_grouped_gemm_swiglu(const moonep_shape* shape, const int8_t* xq,
@@ -687,8 +1024,8 @@ extern "C" int moonep_int_grouped_gemm_swiglu(const moonep_shape* shape, const i
   int_plan(s, cu_seqlens, &a);
   a.act = act;
   a.h_saved = h_saved;
-  return s.dtype == MOONEP_BF16 ? int_product<kIntSwigluBf16>(a, as_stream(stream))
-                                : int_product<kIntSwigluF32>(a, as_stream(stream));
+  return s.dtype == MOONEP_BF16 ? int_product<kIntSwigluBf16>(a, s, ws, as_stream(stream))
+                                : int_product<kIntSwigluF32>(a, s, ws, as_stream(stream));
 }
 
 extern "C" int moonep_int_gemm(const moonep_shape* shape, int64_t rows, const int8_t* xq,
@@ -706,7 +1043,7 @@ extern "C" int moonep_int_gemm(const moonep_shape* shape, int64_t rows, const in
   a.NK = rows;
   a.add = add;
   a.c = c;
-  return int_product<kIntFloat>(a, as_stream(stream));
+  return int_product<kIntFloat>(a, s, nullptr, as_stream(stream));
 }
 
 extern "C" int moonep_int_gemm_swiglu(const moonep_shape* shape, int64_t rows, const int8_t* xq,
@@ -725,8 +1062,8 @@ extern "C" int moonep_int_gemm_swiglu(const moonep_shape* shape, int64_t rows, c
   a.NK = rows;
   a.act = act;
   a.h_saved = h_saved;
-  return s.dtype == MOONEP_BF16 ? int_product<kIntSwigluBf16>(a, as_stream(stream))
-                                : int_product<kIntSwigluF32>(a, as_stream(stream));
+  return s.dtype == MOONEP_BF16 ? int_product<kIntSwigluBf16>(a, s, nullptr, as_stream(stream))
+                                : int_product<kIntSwigluF32>(a, s, nullptr, as_stream(stream));
 }
 
 extern "C" int moonep_int_quantize_grad(const moonep_shape* shape, const void* src,
