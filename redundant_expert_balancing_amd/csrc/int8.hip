@@ -14,6 +14,8 @@ constexpr int kIntThreads = 256;
 constexpr int kIntMaxK = 131072;             // 127 * 127 * 131072 < 2^31: sums stay exact
 constexpr float kIntLeast = 0x1p-126f;       // the smallest scale
 constexpr uint32_t kIntNan = 0x7FC00000u;
+constexpr int kIntFewRows = 2048;            // fewer rows share a workgroup or more each
+constexpr int kIntChunk = 16;                // positions in a row of the gradient's rounding
 typedef float v4f_t __attribute__((ext_vector_type(4)));
 
 // ---- rounding to 8 bits
@@ -30,22 +32,73 @@ __device__ inline float int_scale(uint32_t amax_bits) {
 // most about s (and a multiple of 2^-149 at the low end). It decides, so the choice is that of
 // exact arithmetic and does not depend on how the quotient was formed.
 __device__ inline int int_round(float x, float s, float inv) {
-  float q = rintf(x * inv);
-  const float r = fmaf(-q, s, x), twice = 2.0f * fabsf(r);
+  const float q = rintf(x * inv), r = fmaf(-q, s, x), twice = 2.0f * fabsf(r);
   int w = int(q);
   if (twice > s || (twice == s && (w & 1))) w += r > 0.0f ? 1 : -1;
-  return max(-127, min(127, w));
+  return w;
 }
 
 __device__ inline uint32_t int_mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-__device__ inline uint32_t wave_max(uint32_t m) {
+// The low bytes of four words
+__device__ inline uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(b, a, 0x0c0c0400u) | __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+}
+
+// N whole numbers as bytes
+template <int N>
+__device__ inline void int_store(int8_t* at, const int* w) {
+  uint32_t p[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) p[i] = low_bytes(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  if constexpr (N == 8) *reinterpret_cast<uint2*>(at) = make_uint2(p[0], p[1]);
+  else *reinterpret_cast<uint32_t*>(at) = p[0];
+}
+
+// N values of a row with scale s, rounded and stored. Adding 1.5 * 2^23 to the quotient leaves
+// the whole number in the sum's low bits, so a value takes three more operations than its
+// packing: the sum, the whole number back, and the remainder, whose largest magnitude tells
+// whether any value of the lane is so near a border that the sum may have chosen the wrong side
+// (then, rarely, all of them are rounded the long way). 65536 bfloat16 rows of 4096: with
+// every value the long way the kernel was bound by its instructions (146 us).
+template <int N>
+__device__ inline void int_round_store(int8_t* at, const float* v, float s, float inv) {
+  constexpr float kMagic = 0x1.8p23f;
+  int w[N];
+  float most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float t = fmaf(v[i], inv, kMagic);
+    most = fmaxf(most, fabsf(fmaf(kMagic - t, s, v[i])));
+    w[i] = int(__float_as_uint(t));
+  }
+  if (2.0f * most >= s) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = int_round(v[i], s, inv);
+  }
+  if (s != s) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 0;
+  }
+  int_store<N>(at, w);
+}
+
+// The largest m of a row that WPR wavefronts share (a whole workgroup, unless it is one
+// wavefront); part: WPR words of LDS, not written again before every wavefront has read them.
+template <int WPR>
+__device__ inline uint32_t row_max(uint32_t m, uint32_t* part) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = max(m, uint32_t(__shfl_xor(int(m), d, 64)));
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) m = max(m, part[i]);
+  }
   return m;
 }
 
-// A row's 16-byte vector as floats: 8 bfloat16 or 4 float32.
+// A row's 16-byte vector: 8 bfloat16 or 4 float32.
 template <bool BF16>
 struct RowVec {
   static constexpr int N = BF16 ? 8 : 4;
@@ -57,29 +110,22 @@ struct RowVec {
   }
 };
 
-// N whole numbers as bytes
-template <int N>
-__device__ inline void int_store(int8_t* at, const int* w) {
-  uint32_t p[N / 4];
-#pragma unroll
-  for (int i = 0; i < N / 4; ++i)
-    p[i] = uint32_t(w[4 * i] & 255) | uint32_t(w[4 * i + 1] & 255) << 8 |
-           uint32_t(w[4 * i + 2] & 255) << 16 | uint32_t(w[4 * i + 3]) << 24;
-  if constexpr (N == 8) *reinterpret_cast<uint2*>(at) = make_uint2(p[0], p[1]);
-  else *reinterpret_cast<uint32_t*>(at) = p[0];
-}
+// Threads of a workgroup whose rows are shared by WPR wavefronts
+constexpr int int_threads(int wpr) { return wpr == 1 ? kIntThreads : 64 * wpr; }
 
-// One wavefront per row, which holds it in registers between the maximum and the rounding, VPL
+// A row is held in registers between the maximum and the rounding: WPR wavefronts per row, VPL
 // vectors a lane; VPL 0: rows too wide for that are read twice.
-template <bool BF16, int VPL>
-__global__ __launch_bounds__(kIntThreads) void int_quantize_kernel(const uint4* __restrict__ src,
-                                                                   int64_t rows, int nvec, int nout,
-                                                                   int8_t* __restrict__ q,
-                                                                   float* __restrict__ scales) {
+template <bool BF16, int WPR, int VPL>
+__global__ __launch_bounds__(int_threads(WPR)) void int_quantize_kernel(const uint4* __restrict__ src,
+                                                                        int64_t rows, int nvec, int nout,
+                                                                        int8_t* __restrict__ q,
+                                                                        float* __restrict__ scales) {
   typedef RowVec<BF16> V;
-  const int lane = threadIdx.x & 63;
-  for (int64_t r = blockIdx.x * int64_t(kIntThreads / 64) + (threadIdx.x >> 6); r < rows;
-       r += int64_t(gridDim.x) * (kIntThreads / 64)) {
+  constexpr int TPR = 64 * WPR, RPG = int_threads(WPR) / TPR;      // threads per row, rows per workgroup
+  __shared__ uint32_t part[2][WPR];
+  const int t = threadIdx.x % TPR;
+  int turn = 0;
+  for (int64_t r = blockIdx.x * int64_t(RPG) + threadIdx.x / TPR; r < rows; r += int64_t(gridDim.x) * RPG) {
     const uint4* in = src + r * nvec;
     int8_t* out = q + r * nout * V::N;
     V held[VPL ? VPL : 1];
@@ -91,29 +137,28 @@ __global__ __launch_bounds__(kIntThreads) void int_quantize_kernel(const uint4* 
     };
     if constexpr (VPL > 0) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) held[i] = take(lane + 64 * i);
+      for (int i = 0; i < VPL; ++i) held[i] = take(t + TPR * i);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) most(held[i]);
     } else {
-      for (int c = lane; c < nvec; c += 64) most(take(c));
+      for (int c = t; c < nvec; c += TPR) most(take(c));
     }
-    const float s = int_scale(wave_max(m));
+    const float s = int_scale(row_max<WPR>(m, part[turn]));
+    turn ^= 1;
     const float inv = 1.0f / s;
-    const bool good = s == s;
-    auto put = [&](int c, const V& v) {
-      int w[V::N];
+    auto put = [&](int c, const V& h) {
+      float v[V::N];
 #pragma unroll
-      for (int i = 0; i < V::N; ++i) w[i] = good ? int_round(v.at(i), s, inv) : 0;
-      if (c < nout) int_store<V::N>(out + c * V::N, w);
+      for (int i = 0; i < V::N; ++i) v[i] = h.at(i);
+      if (c < nout) int_round_store<V::N>(out + c * V::N, v, s, inv);
     };
     if constexpr (VPL > 0) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i * 64 < nout) put(lane + 64 * i, held[i]);
+      for (int i = 0; i < VPL; ++i) put(t + TPR * i, held[i]);
     } else {
-      for (int c = lane; c < nout; c += 64) put(c, take(c));
+      for (int c = t; c < nout; c += TPR) put(c, take(c));
     }
-    if (lane == 0) scales[r] = s;
+    if (t == 0) scales[r] = s;
   }
 }
 
@@ -128,6 +173,7 @@ struct IntGradArgs {
   float* scales;
   int R, E, B, SK, K, nvec, nout, wscols;
   int64_t NK;
+  int chunk;
 };
 
 // The view row of position pos of a rank: the last i with cu[i] <= pos, or -1 behind the last
@@ -146,76 +192,131 @@ __device__ inline int segment_of(const int32_t* cu, int EB, int pos, int lane) {
   return lo < EB ? lo : -1;
 }
 
-// One wavefront per position: the upstream row times the scales of its expert's columns,
-// rounded as int_quantize_kernel rounds.
-template <bool BF16, int VPL>
-__global__ __launch_bounds__(kIntThreads) void int_quantize_grad_kernel(IntGradArgs a) {
+// The upstream row of a position times the scales of its expert's columns, rounded as
+// int_quantize_kernel rounds. WPR wavefronts (or each wavefront alone) take a chunk of positions
+// in a row and hold the columns' scales while the expert stays the same; the next row is on
+// its way while one is rounded. VPL as there.
+template <bool BF16, int WPR, int VPL>
+__global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(IntGradArgs a) {
   typedef RowVec<BF16> V;
-  const int lane = threadIdx.x & 63;
-  const int64_t stride = int64_t(gridDim.x) * (kIntThreads / 64);
-  for (int64_t p = blockIdx.x * int64_t(kIntThreads / 64) + (threadIdx.x >> 6); p < a.NK; p += stride) {
-    int wrow = 0;
-    if (a.cu) {
-      const int rank = int(p / a.SK), EB = a.E + a.B;
-      const int i = segment_of(a.cu + int64_t(rank) * (EB + 1), EB, int(p % a.SK), lane);
-      if (i < 0) continue;
-      wrow = i < a.E ? i : a.E + rank * a.B + (i - a.E);
-    }
+  constexpr int TPR = 64 * WPR, RPG = int_threads(WPR) / TPR, HELD = VPL ? VPL : 1;
+  __shared__ uint32_t part[2][WPR];
+  const int lane = threadIdx.x & 63, t = threadIdx.x % TPR;
+  const int64_t p0 = (blockIdx.x * int64_t(RPG) + threadIdx.x / TPR) * a.chunk;
+  const int64_t p1 = min(p0 + a.chunk, a.NK);
+  int turn = 0;
+  int64_t until = p0;             // positions before it belong to weight row wrow (-1: none)
+  int wrow = 0;
+  float ws[HELD][V::N];
+  V next[HELD];
+  bool next_there = false;
+  float next_gate = 1.0f;
+  const uint4* next_in = nullptr;
+  auto fetch = [&](int64_t p) {
     int64_t row = p;
-    float gate = 1.0f;
-    bool there = true;
+    next_there = true;
+    next_gate = 1.0f;
     if (a.src_index) {
       const int u = a.src_index[p];
-      there = u >= 0 && u < a.NK;
-      row = there ? u / a.K : 0;
-      if (a.gates && there) gate = a.gates[u];
+      next_there = u >= 0 && u < a.NK;
+      row = next_there ? u / a.K : 0;
+      if (a.gates && next_there) next_gate = a.gates[u];
     }
-    const uint4* in = a.src + row * a.nvec;
-    const v4f_t* ws = reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.wscols);
-    int8_t* out = a.q + p * a.nout * V::N;
-    struct Held { float v[V::N]; } held[VPL ? VPL : 1];
-    uint32_t m = 0;
-    auto take = [&](int c) {
-      Held h;
-      const bool in_row = there && c < a.nvec;
-      const V v{in_row ? in[c] : make_uint4(0, 0, 0, 0)};
-#pragma unroll
-      for (int j = 0; j < V::N / 4; ++j) {
-        const v4f_t s = in_row ? ws[c * (V::N / 4) + j] : v4f_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h.v[4 * j + i] = v.at(4 * j + i) * s[i];
-      }
-      return h;
-    };
-    auto most = [&](const Held& h) {
-#pragma unroll
-      for (int i = 0; i < V::N; ++i) m = max(m, int_mag(h.v[i]));
-    };
+    next_in = a.src + row * a.nvec;
     if constexpr (VPL > 0) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) held[i] = take(lane + 64 * i);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) most(held[i]);
-    } else {
-      for (int c = lane; c < a.nvec; c += 64) most(take(c));
+      for (int i = 0; i < VPL; ++i) {
+        const int c = t + TPR * i;
+        next[i] = V{next_there && c < a.nvec ? next_in[c] : make_uint4(0, 0, 0, 0)};
+      }
     }
-    const float s = int_scale(wave_max(m));
-    const float inv = 1.0f / s;
-    const bool good = s == s;
-    auto put = [&](int c, const Held& h) {
-      int w[V::N];
+  };
+  if (p0 < p1) fetch(p0);
+  for (int64_t p = p0; p < p1; ++p) {
+    if (p >= until) {
+      wrow = 0;
+      until = a.NK;
+      if (a.cu) {
+        const int rank = int(p / a.SK), EB = a.E + a.B;
+        const int32_t* cu = a.cu + int64_t(rank) * (EB + 1);
+        const int i = segment_of(cu, EB, int(p % a.SK), lane);
+        wrow = i < 0 ? -1 : i < a.E ? i : a.E + rank * a.B + (i - a.E);
+        until = int64_t(rank) * a.SK + (i < 0 ? a.SK : cu[i + 1]);
+      }
+      if constexpr (VPL > 0) {
+        if (wrow >= 0)
 #pragma unroll
-      for (int i = 0; i < V::N; ++i) w[i] = good ? int_round(h.v[i], s, inv) : 0;
-      if (c < a.nout) int_store<V::N>(out + c * V::N, w);
-    };
+          for (int i = 0; i < VPL; ++i)
+#pragma unroll
+            for (int j = 0; j < V::N / 4; ++j) {
+              const int c = t + TPR * i;
+              const v4f_t s = c < a.nvec ? reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.wscols)[c * (V::N / 4) + j]
+                                         : v4f_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) ws[i][4 * j + k] = s[k];
+            }
+      }
+    }
+    const bool there = next_there;
+    const float gate = next_gate;
+    const uint4* in = next_in;
+    float v[HELD][V::N];
     if constexpr (VPL > 0) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (i * 64 < a.nout) put(lane + 64 * i, held[i]);
-    } else {
-      for (int c = lane; c < a.nout; c += 64) put(c, take(c));
+#pragma unroll
+        for (int k = 0; k < V::N; ++k) v[i][k] = next[i].at(k) * ws[i][k];
     }
-    if (lane == 0) a.scales[p] = there ? gate * s : 0.0f;
+    if (p + 1 < p1) fetch(p + 1);
+    if (wrow < 0) continue;       // behind the rank's last row; uniform for the row's wavefronts
+    uint32_t m = 0;
+    auto most = [&](const float* h) {
+#pragma unroll
+      for (int k = 0; k < V::N; ++k) m = max(m, int_mag(h[k]));
+    };
+    auto take = [&](int c, float* h) {       // VPL 0
+      const bool in_row = there && c < a.nvec;
+      const V x{in_row ? in[c] : make_uint4(0, 0, 0, 0)};
+#pragma unroll
+      for (int j = 0; j < V::N / 4; ++j) {
+        const v4f_t s = in_row ? reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.wscols)[c * (V::N / 4) + j]
+                               : v4f_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[4 * j + k] = x.at(4 * j + k) * s[k];
+      }
+    };
+    if constexpr (VPL > 0) {
+      // a position without a source is zeros, also where a column's scale is not a number
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (!there)
+#pragma unroll
+          for (int k = 0; k < V::N; ++k) v[i][k] = 0.0f;
+        most(v[i]);
+      }
+    } else {
+      for (int c = t; c < a.nvec; c += TPR) {
+        take(c, v[0]);
+        most(v[0]);
+      }
+    }
+    const float s = int_scale(row_max<WPR>(m, part[turn]));
+    turn ^= 1;
+    const float inv = 1.0f / s;
+    int8_t* out = a.q + p * a.nout * V::N;
+    if constexpr (VPL > 0) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int c = t + TPR * i;
+        if (c < a.nout) int_round_store<V::N>(out + c * V::N, v[i], s, inv);
+      }
+    } else {
+      for (int c = t; c < a.nout; c += TPR) {
+        take(c, v[0]);
+        int_round_store<V::N>(out + c * V::N, v[0], s, inv);
+      }
+    }
+    if (t == 0) a.scales[p] = there ? gate * s : 0.0f;
   }
 }
 
@@ -866,21 +967,24 @@ static int int_product(IntArgs a, const moonep_shape& s, void* ws, hipStream_t s
   return launch_status();
 }
 
-// Vectors per lane that hold `nout` vectors of a row, as an argument of f (0: too many)
+// How the `nout` vectors of a row are shared out, as arguments of f: wavefronts per row, and
+// vectors per lane (0: too many to hold). few: too few rows to fill the card with a wavefront
+// each, so that a row's latency counts.
 template <typename F>
-static void with_vectors(int64_t nout, F f) {
-  const int64_t per = (nout + 63) / 64;
-  if (per <= 1) f(std::integral_constant<int, 1>());
-  else if (per <= 2) f(std::integral_constant<int, 2>());
-  else if (per <= 4) f(std::integral_constant<int, 4>());
-  else if (per <= 8) f(std::integral_constant<int, 8>());
-  else if (per <= 16) f(std::integral_constant<int, 16>());
-  else f(std::integral_constant<int, 0>());
-}
-
-static int int_row_grid(int64_t rows) {
-  const int64_t blocks = (rows + kIntThreads / 64 - 1) / (kIntThreads / 64);
-  return int(blocks < 65536 ? blocks : 65536);
+static void with_row_split(int64_t nout, bool few, F f) {
+  const int64_t per = (nout + 63) / 64;       // vectors per lane of one wavefront
+#define MOONEP_SPLIT(W, V) f(std::integral_constant<int, W>(), std::integral_constant<int, V>())
+  if (per <= 1) MOONEP_SPLIT(1, 1);
+  else if (few && per <= 4) MOONEP_SPLIT(4, 1);
+  else if (few && per <= 8) MOONEP_SPLIT(8, 1);
+  else if (few && per <= 16) MOONEP_SPLIT(16, 1);
+  else if (per <= 2) MOONEP_SPLIT(1, 2);
+  else if (per <= 4) MOONEP_SPLIT(1, 4);
+  else if (per <= 8) MOONEP_SPLIT(4, 2);
+  else if (per <= 16) MOONEP_SPLIT(4, 4);
+  else if (per <= 64) MOONEP_SPLIT(16, 4);
+  else MOONEP_SPLIT(16, 0);
+#undef MOONEP_SPLIT
 }
 
 // The rules all products share; W the weight's columns. MOONEP_OK leaves *a filled but for the
@@ -929,12 +1033,14 @@ extern "C" int moonep_int_quantize(const moonep_shape* shape, int64_t rows, int3
   if (!aligned16(src) || !aligned16(q) || !aligned16(scales)) return MOONEP_EINVAL;
   const uint4* in = static_cast<const uint4*>(src);
   const int nvec = width / vec, nout = int(k_tiles(width)) * 128 / vec;
-  with_vectors(nout, [&](auto v) {
-    constexpr int VPL = decltype(v)::value;
+  with_row_split(nout, rows < kIntFewRows, [&](auto w, auto v) {
+    constexpr int WPR = decltype(w)::value, VPL = decltype(v)::value, RPG = int_threads(WPR) / (64 * WPR);
+    const int64_t groups = (rows + RPG - 1) / RPG;
+    const int grid = int(groups < 65536 ? groups : 65536);
     if (bf16)
-      int_quantize_kernel<true, VPL><<<int_row_grid(rows), kIntThreads, 0, as_stream(stream)>>>(in, rows, nvec, nout, q, scales);
+      int_quantize_kernel<true, WPR, VPL><<<grid, int_threads(WPR), 0, as_stream(stream)>>>(in, rows, nvec, nout, q, scales);
     else
-      int_quantize_kernel<false, VPL><<<int_row_grid(rows), kIntThreads, 0, as_stream(stream)>>>(in, rows, nvec, nout, q, scales);
+      int_quantize_kernel<false, WPR, VPL><<<grid, int_threads(WPR), 0, as_stream(stream)>>>(in, rows, nvec, nout, q, scales);
   });
   return launch_status();
 }
@@ -1084,12 +1190,16 @@ extern "C" int moonep_int_quantize_grad(const moonep_shape* shape, const void* s
   const int vec = bf16 ? 8 : 4;
   IntGradArgs a{static_cast<const uint4*>(src), src_index, gates, wscales, cu_seqlens, q, scales,
                 s.R, s.E, s.B, s.S * s.K, s.K, s.Hp / vec, int(k_tiles(s.Hp)) * 128 / vec,
-                int(int_nb(s.Hp)) * 16, int64_t(s.R) * s.S * s.K};
-  const int grid = int_row_grid(a.NK);
-  with_vectors(a.nout, [&](auto v) {
-    constexpr int VPL = decltype(v)::value;
-    if (bf16) int_quantize_grad_kernel<true, VPL><<<grid, kIntThreads, 0, as_stream(stream)>>>(a);
-    else int_quantize_grad_kernel<false, VPL><<<grid, kIntThreads, 0, as_stream(stream)>>>(a);
+                int(int_nb(s.Hp)) * 16, int64_t(s.R) * s.S * s.K, 0};
+  // chunks of at most kIntChunk positions, shorter where there are few
+  const int64_t chunk = a.NK / kIntFewRows;
+  a.chunk = int(chunk < 1 ? 1 : chunk < kIntChunk ? chunk : kIntChunk);
+  with_row_split(a.nout, a.NK < kIntFewRows, [&](auto w, auto v) {
+    constexpr int WPR = decltype(w)::value, VPL = decltype(v)::value, RPG = int_threads(WPR) / (64 * WPR);
+    const int64_t per = int64_t(RPG) * a.chunk;
+    const int grid = int((a.NK + per - 1) / per);      // below 2^31: NK is
+    if (bf16) int_quantize_grad_kernel<true, WPR, VPL><<<grid, int_threads(WPR), 0, as_stream(stream)>>>(a);
+    else int_quantize_grad_kernel<false, WPR, VPL><<<grid, int_threads(WPR), 0, as_stream(stream)>>>(a);
   });
   return launch_status();
 }
