@@ -427,7 +427,8 @@ struct IntArgs {
 };
 
 // What a product's epilogue makes of its sums.
-enum IntOut { kIntFloat, kIntSwigluBf16, kIntSwigluF32 };
+enum IntOut { kIntFloat, kIntFloatAdd, kIntSwigluBf16, kIntSwigluF32 };
+__host__ __device__ constexpr bool is_swiglu(int out) { return out == kIntSwigluBf16 || out == kIntSwigluF32; }
 
 // (sum * row scale) * column scale, 4 columns of one row
 __device__ inline v4f_t int_scaled(v4i_t acc, float sa, v4f_t sw) {
@@ -437,7 +438,29 @@ __device__ inline v4f_t int_scaled(v4i_t acc, float sa, v4f_t sw) {
   return r;
 }
 
-__device__ inline uint32_t bf16_pair(float a, float b) { return bf16_rne_any(a) | bf16_rne_any(b) << 16; }
+// A sum of its own, not contracted into an FMA with the product before it
+__device__ inline v4f_t added(v4f_t a, v4f_t b) {
+#pragma clang fp contract(off)
+  return a + b;
+}
+
+// The activation. float32 layers get swiglu_f32's bits. bfloat16 layers take the exponential and
+// the reciprocal from the hardware's instructions: off by at most (|g| + 8) * 2^-24 of the value
+// (g * log2(e) is rounded before the exponential), which the rounding to bfloat16 (2^-8) covers,
+// or |g u| * 2^-126 where the reciprocal falls below the normal numbers; and a third of swiglu_f32's instructions; with
+// those a tile's epilogue took half as long as its products at a reduction of 4096.
+template <int OUT>
+__device__ inline float int_swiglu(float g, float u) {
+  if constexpr (OUT == kIntSwigluF32) return swiglu_f32(g, u);
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -0x1.715476p0f)) * u;
+}
+
+// Two values rounded to bfloat16 (nearest even, a NaN stays one)
+typedef float v2f_t __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf_t __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t bf16_pair(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f_t{a, b}, v2bf_t));
+}
 
 template <int OUT>
 __device__ inline void store4(void* base, int64_t at, v4f_t v) {
@@ -460,7 +483,7 @@ constexpr int kIntItems = 256;    // items looked up at a time
 // Block j of item t: with SwiGLU and J = 2 a gate block and its up block, 32 columns further.
 template <int J, int OUT>
 __device__ inline int item_block(int t, int j) {
-  return OUT != kIntFloat && J == 2 ? 4 * (t >> 1) + (t & 1) + 2 * j : J * t + j;
+  return is_swiglu(OUT) && J == 2 ? 4 * (t >> 1) + (t & 1) + 2 * j : J * t + j;
 }
 
 template <int J, int U, int OUT>
@@ -535,12 +558,12 @@ __device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v,
                           : v4f_t{1.f, 1.f, 1.f, 1.f};
     v[j] = int_scaled(acc[j], sa, sw);
   }
-  if constexpr (OUT == kIntFloat) {
+  if constexpr (!is_swiglu(OUT)) {
 #pragma unroll
     for (int j = 0; j < J; ++j)
       if (col[j] < a.W) {
         const int64_t at = pos * a.W + col[j];
-        if (a.add) v[j] += *reinterpret_cast<const v4f_t*>(a.add + at);
+        if constexpr (OUT == kIntFloatAdd) v[j] = added(v[j], *reinterpret_cast<const v4f_t*>(a.add + at));
         *reinterpret_cast<v4f_t*>(a.c + at) = v[j];
       }
   } else {
@@ -551,7 +574,7 @@ __device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v,
     for (int j = 0; j < J / 2; ++j) {
       v4f_t s;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = swiglu_f32(v[j][i], v[j + J / 2][i]);
+      for (int i = 0; i < 4; ++i) s[i] = int_swiglu<OUT>(v[j][i], v[j + J / 2][i]);
       // gate column c stands for intermediate column 32 * (c / 64) + c % 32
       store4<OUT>(a.act, pos * (a.W / 2) + col[j] / 64 * 32 + col[j] % 32, s);
     }
@@ -619,8 +642,10 @@ __global__ __launch_bounds__(256) void int_gemm_kernel(IntArgs a, int shares) {
 // go to LDS by DMA, two stages: token rows (gathered by src_index) as 128-byte rows with
 // swizzled chunks, weights as the 1 KiB blocks they are stored in, which a wavefront reads back
 // lane by lane. A wavefront holds the fragments of half a step (64 k) and refills them behind
-// its MFMAs; the one barrier of a step comes after the last reads of its stage, so the DMAs of
-// the step after next run under half a step's and a whole step's products.
+// its MFMAs; the one barrier of a step comes under the MFMAs of its second half, when every read
+// of its stage is done, and the DMAs of the step after next are issued between the MFMAs behind
+// it (in one burst they held up the wavefront's MFMAs: 3% slower). The next tile's rows and
+// scales are looked up during a tile, and its first step is loaded under the tile's epilogue.
 constexpr int kNonTemporal = 2;   // buffer cache policy: the output is not read back here
 
 struct IntTile {
@@ -628,19 +653,29 @@ struct IntTile {
   static constexpr int FM = 8, FN = 4;                   // 16 x 16 blocks of a wavefront
   static constexpr int STEPB = 128;                      // bytes of a row per step
   static constexpr int A_BYTES = BM * STEPB, B_BYTES = BN * STEPB, STAGE = A_BYTES + B_BYTES;
-  static constexpr int ISSUERS = 4;                      // wavefronts that issue the DMAs
-  static constexpr int A_DMAS = A_BYTES / 1024 / ISSUERS, B_DMAS = B_BYTES / 1024 / ISSUERS;
+  static constexpr int A_DMAS = A_BYTES / 1024 / WAVES, B_DMAS = B_BYTES / 1024 / WAVES;
+  static constexpr int DMAS = A_DMAS + B_DMAS;           // per wavefront and step
   static constexpr int kBlockE = 8, kBlockN = 4;         // tile-order block
 };
+static_assert(IntTile::DMAS == IntTile::FM, "one DMA behind each row of the second half step");
+
+// One 4-byte-per-lane DMA into LDS, as dma16.
+__device__ inline void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(r), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
 
 template <bool GATHER, int OUT>
 __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArgs a) {
   typedef IntTile T;
   constexpr int FM = T::FM, FN = T::FN;
   __shared__ __align__(1024) char smem[2 * T::STAGE];
-  __shared__ uint32_t s_off[T::BM];                      // byte offsets of the tile's token rows
-  __shared__ float s_sa[T::BM];                          // their scales
-  __shared__ __align__(16) float s_sw[T::BN];            // scales of its columns
+  __shared__ __align__(256) float s_sw[2][T::BN];        // scales of the tile's columns, and of the next's
+  __shared__ __align__(256) float s_sa[2][T::BM];        // the same of its rows
+  __shared__ __align__(256) int s_u[T::BM];              // src_index of the next tile's rows
+  __shared__ uint32_t s_off[T::BM];                      // byte offsets of its token rows
   __shared__ int s_claim;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -652,18 +687,15 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
   const int total = nent * NT;      // below 2^31 (host)
   const int nsteps = a.KB / 2;
   const uint32_t qrow = uint32_t(a.KB) * 64;             // bytes of a token row
-  // The workgroups of one XCD take a contiguous run of tiles per round, from a list of the call
-  // first come first served (position q of XCD x is tile (q / per) * G + x * per + q % per).
+  // The workgroups of one XCD take a contiguous run of tiles per round, first come first
+  // served (position q of XCD x is tile (q / per) * G + x * per + q % per), a tile ahead;
+  // without a queue in turn.
   const int G = gridDim.x, xcd = blockIdx.x % 8, per = G / 8;
   const bool dyn = a.qcnt != nullptr;
-  auto claim = [&]() {
-    if (tid == 0) {
-      const int q = atomicAdd(a.qcnt + xcd, 1);
-      s_claim = (q / per) * G + xcd * per + q % per;
-    }
-  };
+  auto claim = [&]() { return tid == 0 ? atomicAdd(a.qcnt + xcd, 1) : 0; };
+  auto publish = [&](int q) { if (tid == 0) s_claim = (q / per) * G + xcd * per + q % per; };
 
-  int rowbase = 0, wrow = 0, rows_valid = 0, n0 = 0;
+  struct Place { int rowbase, wrow, rows, n0; };
   auto place = [&](int tau) {
     // blocks of kBlockE entries x kBlockN N-tiles
     const int eb = tau / (T::kBlockE * NT), j = tau % (T::kBlockE * NT);
@@ -671,261 +703,311 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
     const int nb = j / (ge * T::kBlockN), jj = j % (ge * T::kBlockN);
     const int wb = min(T::kBlockN, NT - nb * T::kBlockN);
     const int ent = eb * T::kBlockE + jj / wb;
-    n0 = (nb * T::kBlockN + jj % wb) * T::BN;
     const TileEntry e = a.tiles ? a.tiles[ent] : TileEntry{0, 0, ent * T::BM, int(a.NK)};
-    rowbase = __builtin_amdgcn_readfirstlane(e.rowbase + e.m0);
-    wrow = __builtin_amdgcn_readfirstlane(e.wrow);
-    rows_valid = __builtin_amdgcn_readfirstlane(min(T::BM, e.n - e.m0));
+    return Place{__builtin_amdgcn_readfirstlane(e.rowbase + e.m0), __builtin_amdgcn_readfirstlane(e.wrow),
+                 __builtin_amdgcn_readfirstlane(min(T::BM, e.n - e.m0)), (nb * T::kBlockN + jj % wb) * T::BN};
   };
-  // threads 0..255: a row of the tile each, the others a column's scale
-  int next_u = -1;
-  float next_s = 0.f;
-  uint32_t next_off = kOffNone;
-  auto look_up = [&]() {
-    if (tid < T::BM) {
-      next_u = tid < rows_valid ? (GATHER ? a.src_index[rowbase + tid] : tid) : -1;
-    } else {
-      const int n = n0 + tid - T::BM;
-      next_s = n < a.W ? (a.ws ? a.ws[int64_t(wrow) * a.NB * 16 + n] : 1.0f) : 0.f;
+  // Looking a tile up, in two goes of DMA. First the rows' src_index and the columns' scales ..
+  auto look_up = [&](const Place& p, int par) {
+    if (GATHER && wid < T::BM / 64)
+      dma4(make_rsrc(a.src_index + p.rowbase, uint32_t(p.rows) * 4), uint32_t(tid) * 4, lds_addr(s_u) + wid * 256);
+    if (wid == T::BM / 64) {
+      if (a.ws) dma16(make_rsrc(a.ws + int64_t(p.wrow) * a.NB * 16 + p.n0, clamp_bytes((int64_t(a.NB) * 16 - p.n0) * 4)),
+                      uint32_t(lane) * 16, lds_addr(s_sw[par]));
+      else *reinterpret_cast<v4f_t*>(&s_sw[par][lane * 4]) = v4f_t{1.f, 1.f, 1.f, 1.f};
     }
   };
-  auto look_up_row = [&]() {
-    if (tid < T::BM) {
-      next_off = kOffNone;
-      next_s = 0.f;
-      if (next_u >= 0 && (!GATHER || next_u < a.NK)) {
-        const uint32_t r = GATHER ? uint32_t(next_u) / uint32_t(a.K) : uint32_t(next_u);
-        next_off = r * qrow;
-        next_s = a.xs[(GATHER ? 0 : rowbase) + int64_t(r)];
-      }
+  // .. then, behind a barrier, each row's offset and scale.
+  auto look_up_rows = [&](const Place& p, int par) {
+    if (wid >= T::BM / 64) return;
+    uint32_t r = kOffNone;
+    if (tid < p.rows) {
+      const int u = GATHER ? s_u[tid] : 0;
+      if (!GATHER) r = tid;
+      else if (u >= 0 && u < a.NK) r = uint32_t(u) / uint32_t(a.K);
+    }
+    s_off[tid] = r == kOffNone ? kOffNone : r * qrow;
+    const int64_t first = GATHER ? 0 : p.rowbase;
+    dma4(make_rsrc(a.xs + first, clamp_bytes((GATHER ? a.xrows : p.rows) * 4)),
+         r == kOffNone ? kOffNone : r * 4, lds_addr(s_sa[par]) + wid * 256);
+  };
+  // the operands of the tile whose offsets are in s_off
+  __amdgpu_buffer_rsrc_t ars, brs;
+  uint32_t va[T::A_DMAS], vb[T::B_DMAS];
+  auto operands = [&](const Place& p) {
+    const int64_t first = GATHER ? 0 : p.rowbase;
+    ars = make_rsrc(a.xq + first * qrow, clamp_bytes((GATHER ? a.xrows : p.rows) * qrow));
+    const int nblocks = min(T::BN / 16, a.NB - p.n0 / 16);
+    brs = make_rsrc(a.wq + (int64_t(p.wrow) * a.NB + p.n0 / 16) * a.KB * 1024, uint32_t(nblocks * a.KB) * 1024);
+#pragma unroll
+    for (int i = 0; i < T::A_DMAS; ++i) {
+      const int row = (wid + T::WAVES * i) * 8 + (lane >> 3);
+      const uint32_t off = s_off[row];
+      va[i] = off == kOffNone ? kOffNone : off + ((lane & 7) ^ swz_k(row)) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < T::B_DMAS; ++i) {
+      const int b = wid + T::WAVES * i, j = b >> 1;     // half b % 2 of the step, 16-column block j
+      vb[i] = j < nblocks ? uint32_t((j * a.KB + (b & 1)) * 1024 + lane * 16) : kOffNone;
     }
   };
-  auto keep = [&]() {
-    if (tid < T::BM) {
-      s_off[tid] = next_off;
-      s_sa[tid] = next_s;
-    } else {
-      s_sw[tid - T::BM] = next_s;
-    }
+  // DMA i of this wavefront for step k, into stage k % 2
+  auto issue = [&](int k, int i) {
+    const uint32_t st = lds0 + (k & 1) * T::STAGE;
+    if (i < T::A_DMAS)
+      dma16(ars, va[i], uint32_t(k) * T::STEPB, st + (wid + T::WAVES * i) * 1024);
+    else
+      dma16(brs, vb[i - T::A_DMAS], uint32_t(k) * 2048, st + T::A_BYTES + (wid + T::WAVES * (i - T::A_DMAS)) * 1024);
+  };
+  auto issue_all = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < T::DMAS; ++i) issue(k, i);
   };
 
   int tau = (G % 8 == 0) ? xcd * per + blockIdx.x / 8 : blockIdx.x;
   if (dyn) {
-    claim();
+    publish(claim());
     __syncthreads();
     tau = __builtin_amdgcn_readfirstlane(s_claim);
   }
   if (tau >= total) return;
-  place(tau);
-  look_up();
-  look_up_row();
-  keep();
+  Place cur = place(tau);
+  int par = 0;
+  look_up(cur, par);
+  wait_vm<0>();
+  __syncthreads();
+  if (dyn) publish(claim());
+  look_up_rows(cur, par);
+  wait_vm<0>();
+  __syncthreads();
+  operands(cur);
+  issue_all(0);
   while (true) {
-    __syncthreads();     // the tile's rows are known, and the previous tile's LDS is free
-    const int64_t first = GATHER ? 0 : rowbase;
-    const int64_t span = GATHER ? a.xrows : rows_valid;
-    const __amdgpu_buffer_rsrc_t ars = make_rsrc(a.xq + first * qrow, clamp_bytes(span * qrow));
-    const int nblocks = min(T::BN / 16, a.NB - n0 / 16);
-    const __amdgpu_buffer_rsrc_t brs =
-        make_rsrc(a.wq + (int64_t(wrow) * a.NB + n0 / 16) * a.KB * 1024, uint32_t(nblocks * a.KB) * 1024);
-    uint32_t va[T::A_DMAS];
-    if (wid < T::ISSUERS) {
-#pragma unroll
-      for (int i = 0; i < T::A_DMAS; ++i) {
-        const int row = (wid + T::ISSUERS * i) * 8 + (lane >> 3);
-        const uint32_t off = s_off[row];
-        va[i] = off == kOffNone ? kOffNone : off + ((lane & 7) ^ swz_k(row)) * 16;
-      }
+    __syncthreads();     // the previous tile's LDS is free, and the claim is there
+    tau = dyn ? __builtin_amdgcn_readfirstlane(s_claim) : tau + G;
+    const bool more = tau < total;
+    if (nsteps > 1) {
+      issue_all(1);
+      wait_vm<T::DMAS>();     // step 0 (and whatever came before it)
+    } else {
+      wait_vm<0>();
     }
-    auto issue = [&](int k) {     // step k into stage k % 2
-      if (wid >= T::ISSUERS) return;
-      const uint32_t st = lds0 + (k & 1) * T::STAGE;
-#pragma unroll
-      for (int i = 0; i < T::A_DMAS; ++i)
-        dma16(ars, va[i], uint32_t(k) * T::STEPB, st + (wid + T::ISSUERS * i) * 1024);
-#pragma unroll
-      for (int i = 0; i < T::B_DMAS; ++i) {
-        const int b = wid + T::ISSUERS * i, j = b >> 1;   // half b % 2 of the step, 16-column block j
-        dma16(brs, j < nblocks ? lane * 16 : kOffNone, uint32_t(j * a.KB + 2 * k + (b & 1)) * 1024,
-              st + T::A_BYTES + b * 1024);
-      }
-    };
+    __syncthreads();
+    Place next = cur;
+    if (more) {
+      next = place(tau);
+      look_up(next, par ^ 1);
+    }
     const int row0 = wm * 128, col0 = wn * 64;
-    const bool idle = row0 >= rows_valid || n0 + col0 >= a.W;    // uniform
-    v4i_t acc[FM][FN];
+    const bool idle = row0 >= cur.rows || cur.n0 + col0 >= a.W;    // uniform
+    v4i_t acc[FM][FN], fa[FM], fb[FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = v4i_t{0, 0, 0, 0};
-    issue(0);
-    if (nsteps > 1) issue(1);
-    if (wid < T::ISSUERS) {
-      if (nsteps > 1) wait_vm<T::A_DMAS + T::B_DMAS>();
-      else wait_vm<0>();
-    }
-    __syncthreads();
-    if (dyn) claim();             // the next tile, read behind the loop's barriers
+    // fragments of half ks of the step in the stage at st; LDS rows 16 apart swizzle alike
+    auto frag_a = [&](const char* st, int ks, int i) {
+      return *reinterpret_cast<const v4i_t*>(st + (row0 + r16) * T::STEPB + (((ks * 4 + kb) ^ swz_k(r16)) << 4) +
+                                             i * 16 * T::STEPB);
+    };
+    auto frag_b = [&](const char* st, int ks, int j) {
+      return *reinterpret_cast<const v4i_t*>(st + T::A_BYTES + (wn * 8 + ks) * 1024 + lane * 16 + j * 2048);
+    };
+    // The products of the fragments held: of every row with the first two column blocks, then
+    // mid(), then with the other two, each row's fragments refilled from half ks of the
+    // stage at st behind its last product, and behind(i).
+    auto half = [&](const char* st, int ks, auto mid, auto behind) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)     // operands swapped: a lane holds 4 columns of one row
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      mid();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 2; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        fa[i] = frag_a(st, ks, i);
+        if (i < 2) fb[i] = frag_b(st, ks, i);
+        behind(i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int j = 2; j < 4; ++j) fb[j] = frag_b(st, ks, j);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // step k; the stage of step k + 1 has landed for every wavefront behind its barrier
+    auto land = [&]() {
+      wait_vm<0>();
+      __syncthreads();
+    };
+    auto step = [&](int k, auto fill_c) {
+      constexpr bool FILL = decltype(fill_c)::value;
+      half(smem + (k & 1) * T::STAGE, 1, []() {}, [](int) {});
+      // behind the last step its own stage is read again (not used)
+      half(smem + ((FILL || k + 1 < nsteps ? k + 1 : k) & 1) * T::STAGE, 0, land,
+           [&](int i) { if constexpr (FILL) issue(k + 2, i); });
+    };
     if (idle) {
       for (int k = 0; k < nsteps; ++k) {
-        if (wid < T::ISSUERS) wait_vm<0>();
-        __syncthreads();
-        if (k + 2 < nsteps) issue(k + 2);
+        if (k + 1 == nsteps && more) {
+          if (nsteps == 1) land();
+          look_up_rows(next, par ^ 1);
+        }
+        land();
+        if (k + 2 < nsteps) issue_all(k + 2);
       }
     } else {
-      v4i_t fa[FM], fb[FN];
-      auto load = [&](int k, int ks) {
-        const char* st = smem + (k & 1) * T::STAGE;
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          const int row = row0 + i * 16 + r16;
-          fa[i] = *reinterpret_cast<const v4i_t*>(st + row * T::STEPB + (((ks * 4 + kb) ^ swz_k(row)) << 4));
+      for (int i = 0; i < FM; ++i) fa[i] = frag_a(smem, 0, i);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j] = frag_b(smem, 0, j);
+      int k = 0;
+      for (; k + 2 < nsteps; ++k) step(k, std::true_type());
+      for (; k < nsteps; ++k) {
+        if (k + 1 == nsteps && more) {
+          if (nsteps == 1) land();      // what was looked up; longer loops have passed a barrier
+          look_up_rows(next, par ^ 1);
         }
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          fb[j] = *reinterpret_cast<const v4i_t*>(st + T::A_BYTES + ((wn * 4 + j) * 2 + ks) * 1024 + lane * 16);
-      };
-      // every row with the first two column blocks, then with the others: the first blocks'
-      // fragments are refilled under the second half
-      auto products = [&]() {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 2 * h; j < 2 * h + 2; ++j)   // operands swapped: a lane holds 4 columns of one row
-              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-      };
-      auto interleave = [&]() {
-        __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / 2, 0);
-#pragma unroll
-        for (int q = 0; q < FM + FN / 2; ++q) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / 2 - (FM + FN / 2), 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, FN / 2, 0);
-      };
-      load(0, 0);
-      for (int k = 0; k < nsteps; ++k) {
-        products();
-        load(k, 1);
-        interleave();
-        if (wid < T::ISSUERS) wait_vm<0>();     // step k + 1
-        __syncthreads();
-        if (k + 2 < nsteps) issue(k + 2);
-        products();
-        load(k + 1 < nsteps ? k + 1 : k, 0);    // behind the last step: in bounds, not used
-        interleave();
+        step(k, std::false_type());
       }
     }
-    // ---- epilogue
+    // ---- epilogue. Its addresses are formed from et, which hides them from the code ahead of the
+    // loop: kept in registers over the loop they made the accumulators spill.
+    int et = tid;
+    asm volatile("" : "+v"(et));
+    const int er = et & 15, ek = (et & 63) >> 4;
     float sa[FM];
     v4f_t sw[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = s_sa[row0 + i * 16 + r16];
+    for (int i = 0; i < FM; ++i) sa[i] = s_sa[par][row0 + i * 16 + er];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) sw[j] = *reinterpret_cast<const v4f_t*>(&s_sw[col0 + j * 16 + 4 * kb]);
-    const int rb = rowbase, rv = rows_valid, c0 = n0;
-    tau = dyn ? __builtin_amdgcn_readfirstlane(s_claim) : tau + G;
-    const bool more = tau < total;
-    if (more) {
-      place(tau);
-      look_up();
-    }
-    __syncthreads();     // every wavefront has read the last stage and the tile's scales
-    // The lanes' own 16 x 16 blocks would be stored as 16 pieces of 64 bytes; the wavefronts
-    // exchange 32 rows of each row group at a time through LDS and store whole rows.
-    // Row R of the 64 is row (R / 32) * 128 + 32 * p + R % 32 of the tile.
-    auto put = [&](char* buf, int chunks, int ii, int byte, auto v) {
-      const int R = wm * 32 + ii * 16 + r16;
-      *reinterpret_cast<decltype(v)*>(buf + R * chunks * 16 + (((byte >> 4) ^ r16) << 4) + (byte & 15)) = v;
+    for (int j = 0; j < FN; ++j) sw[j] = *reinterpret_cast<const v4f_t*>(&s_sw[par][col0 + j * 16 + 4 * ek]);
+    // rows of `width` elements of eb bytes from column `col`: descriptor
+    auto out_rsrc = [&](const void* base, int64_t width, int64_t col, int eb) {
+      return make_rsrc(static_cast<const char*>(base) + (cur.rowbase * width + col) * eb,
+                       clamp_bytes((cur.rows * width - col) * eb));
     };
-    auto flush = [&](const char* buf, auto chunks_c, int p, __amdgpu_buffer_rsrc_t rs, uint32_t ld,
-                     uint32_t left, auto policy_c, auto add) {
+    __syncthreads();     // every wavefront has read the last stage, the claim and the tile's scales
+    const int q = dyn ? claim() : 0;
+    if (more) {
+      operands(next);
+      issue_all(0);
+    }
+    // The lanes' own 16 x 16 blocks would be stored as 16 pieces of 64 bytes; the wavefronts
+    // exchange 16 rows of each row group at a time through the second stage and store whole
+    // rows. Row R of the 32 is row (R / 16) * 128 + 16 * i + R % 16 of the tile.
+    char* const ex = smem + T::STAGE;
+    auto put = [&](char* buf, int chunks, int byte, auto v) {
+      const int R = wm * 16 + er;
+      *reinterpret_cast<decltype(v)*>(buf + R * chunks * 16 + (((byte >> 4) ^ er) << 4) + (byte & 15)) = v;
+    };
+    // what thread et stores in go h of i: LDS address and offset in rows of ld bytes, of which
+    // `left` are left from the tile's first column
+    auto spot = [&](auto chunks_c, int h, int i, uint32_t ld, uint32_t left, uint32_t& at, uint32_t& off) {
       constexpr int C = decltype(chunks_c)::value;
+      const int id = h * T::THREADS + et, R = id / C, c = id % C;
+      at = R * C * 16 + ((c ^ (R & 15)) << 4);
+      off = uint32_t(c) * 16 < left ? uint32_t((R >> 4) * 128 + i * 16 + (R & 15)) * ld + c * 16 : kOffNone;
+    };
+    auto flush = [&](const char* buf, auto chunks_c, int i, __amdgpu_buffer_rsrc_t rs, uint32_t ld,
+                     uint32_t left, auto policy_c) {
 #pragma unroll
-      for (int h = 0; h < 64 * C / T::THREADS; ++h) {
-        const int id = h * T::THREADS + tid, R = id / C, c = id % C;
-        const uint32_t row = (R >> 5) * 128 + p * 32 + (R & 31);
-        const uint32_t off = uint32_t(c) * 16 < left ? row * ld + c * 16 : kOffNone;
-        v4i_t x = *reinterpret_cast<const v4i_t*>(buf + R * C * 16 + ((c ^ (R & 15)) << 4));
-        x = add(x, off);
-        __builtin_amdgcn_raw_buffer_store_b128(x, rs, off, 0, decltype(policy_c)::value);
+      for (int h = 0; h < 32 * decltype(chunks_c)::value / T::THREADS; ++h) {
+        uint32_t at, off;
+        spot(chunks_c, h, i, ld, left, at, off);
+        __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const v4i_t*>(buf + at), rs, off, 0,
+                                               decltype(policy_c)::value);
       }
     };
-    auto as_is = [](v4i_t x, uint32_t) { return x; };
-    // rows of `width` elements of eb bytes from column `col`: descriptor, and bytes left in a row
-    auto out_rsrc = [&](void* base, int64_t width, int64_t col, int eb) {
-      return make_rsrc(static_cast<char*>(base) + (rb * width + col) * eb,
-                       clamp_bytes((rv * width - col) * eb));
-    };
-    if constexpr (OUT == kIntFloat) {
-      const __amdgpu_buffer_rsrc_t crs = out_rsrc(a.c, a.W, c0, 4);
-      const __amdgpu_buffer_rsrc_t drs = out_rsrc(const_cast<float*>(a.add ? a.add : a.c), a.W, c0, 4);
+    const std::integral_constant<int, kNonTemporal> stream;
+    if constexpr (!is_swiglu(OUT)) {
+      const std::integral_constant<int, 64> chunks;
+      constexpr int GOES = 32 * 64 / T::THREADS;
+      const uint32_t ld = uint32_t(a.W) * 4, left = uint32_t(a.W - cur.n0) * 4;
+      const __amdgpu_buffer_rsrc_t crs = out_rsrc(a.c, a.W, cur.n0, 4);
+      const __amdgpu_buffer_rsrc_t drs = out_rsrc(OUT == kIntFloatAdd ? a.add : a.c, a.W, cur.n0, 4);
+      v4f_t add[GOES];       // of the next rows, on their way while these are exchanged
+      auto fetch = [&](int i) {
+        if constexpr (OUT == kIntFloatAdd) {
 #pragma unroll
-      for (int p = 0; p < FM / 2; ++p) {
-        char* buf = smem + (p & 1) * 65536;
+          for (int h = 0; h < GOES; ++h) {
+            uint32_t at, off;
+            spot(chunks, h, i, ld, left, at, off);
+            add[h] = __builtin_bit_cast(v4f_t, __builtin_amdgcn_raw_buffer_load_b128(drs, off, 0, 0));
+          }
+        }
+      };
+      fetch(0);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        char* buf = ex + (i & 1) * 32768;
         if (!idle) {
 #pragma unroll
-          for (int ii = 0; ii < 2; ++ii)
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-              put(buf, 64, ii, (col0 + j * 16 + 4 * kb) * 4, int_scaled(acc[2 * p + ii][j], sa[2 * p + ii], sw[j]));
+          for (int j = 0; j < FN; ++j) put(buf, 64, (col0 + j * 16 + 4 * ek) * 4, int_scaled(acc[i][j], sa[i], sw[j]));
         }
         __syncthreads();
-        if (more && p == 1) look_up_row();
-        if (a.add)
-          flush(buf, std::integral_constant<int, 64>(), p, crs, uint32_t(a.W) * 4, uint32_t(a.W - c0) * 4,
-                std::integral_constant<int, kNonTemporal>(), [&](v4i_t x, uint32_t off) {
-                  const v4i_t y = __builtin_bit_cast(v4i_t, __builtin_amdgcn_raw_buffer_load_b128(drs, off, 0, 0));
-                  return __builtin_bit_cast(v4i_t, __builtin_bit_cast(v4f_t, x) + __builtin_bit_cast(v4f_t, y));
-                });
-        else
-          flush(buf, std::integral_constant<int, 64>(), p, crs, uint32_t(a.W) * 4, uint32_t(a.W - c0) * 4,
-                std::integral_constant<int, kNonTemporal>(), as_is);
+        if constexpr (OUT == kIntFloatAdd) {
+          v4f_t out[GOES];
+          uint32_t at, off[GOES];
+#pragma unroll
+          for (int h = 0; h < GOES; ++h) {
+            spot(chunks, h, i, ld, left, at, off[h]);
+            out[h] = added(*reinterpret_cast<const v4f_t*>(buf + at), add[h]);
+          }
+          if (i + 1 < FM) fetch(i + 1);
+#pragma unroll
+          for (int h = 0; h < GOES; ++h)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i_t, out[h]), crs, off[h], 0, kNonTemporal);
+        } else {
+          flush(buf, chunks, i, crs, ld, left, stream);
+        }
       }
     } else {
       constexpr int EB = OUT == kIntSwigluBf16 ? 2 : 4;
-      const __amdgpu_buffer_rsrc_t ars2 = out_rsrc(a.act, a.W / 2, c0 / 2, EB);
-      const __amdgpu_buffer_rsrc_t hrs = out_rsrc(a.h_saved ? a.h_saved : a.act, a.W, c0, EB);
+      const std::integral_constant<int, 8 * EB> achunks;
+      const std::integral_constant<int, 16 * EB> hchunks;
+      const __amdgpu_buffer_rsrc_t ors = out_rsrc(a.act, a.W / 2, cur.n0 / 2, EB);
+      const __amdgpu_buffer_rsrc_t hrs = out_rsrc(a.h_saved ? a.h_saved : a.act, a.W, cur.n0, EB);
       auto value = [&](v4f_t v) {
         if constexpr (EB == 2) return uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         else return v;
       };
-      char* hbuf = smem + 64 * 128 * EB;
 #pragma unroll
-      for (int p = 0; p < FM / 2; ++p) {
+      for (int i = 0; i < FM; ++i) {
+        char* abuf = ex + (EB == 2 ? (i & 1) * 24576 : 0);
+        char* hbuf = abuf + 32 * 128 * EB;
         if (!idle) {
+          v4f_t v[FN];
 #pragma unroll
-          for (int ii = 0; ii < 2; ++ii) {
-            v4f_t v[FN];
+          for (int j = 0; j < FN; ++j) {
+            v[j] = int_scaled(acc[i][j], sa[i], sw[j]);
+            if (a.h_saved) put(hbuf, 16 * EB, (col0 + j * 16 + 4 * ek) * EB, value(v[j]));
+          }
+          // blocks 0, 1 of the wavefront's 64 columns are gates, 2, 3 their up columns
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-              v[j] = int_scaled(acc[2 * p + ii][j], sa[2 * p + ii], sw[j]);
-              if (a.h_saved) put(hbuf, 16 * EB, ii, (col0 + j * 16 + 4 * kb) * EB, value(v[j]));
-            }
-            // blocks 0, 1 of the wavefront's 64 columns are gates, 2, 3 their up columns
+          for (int j = 0; j < 2; ++j) {
+            v4f_t s;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              v4f_t s;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s[i] = swiglu_f32(v[j][i], v[j + 2][i]);
-              put(smem, 8 * EB, ii, (wn * 32 + j * 16 + 4 * kb) * EB, value(s));
-            }
+            for (int e = 0; e < 4; ++e) s[e] = int_swiglu<OUT>(v[j][e], v[j + 2][e]);
+            put(abuf, 8 * EB, (wn * 32 + j * 16 + 4 * ek) * EB, value(s));
           }
         }
         __syncthreads();
-        if (more && p == 1) look_up_row();
-        flush(smem, std::integral_constant<int, 8 * EB>(), p, ars2, uint32_t(a.W / 2) * EB,
-              uint32_t(a.W - c0) / 2 * EB, std::integral_constant<int, 0>(), as_is);
-        if (a.h_saved)
-          flush(hbuf, std::integral_constant<int, 16 * EB>(), p, hrs, uint32_t(a.W) * EB,
-                uint32_t(a.W - c0) * EB, std::integral_constant<int, kNonTemporal>(), as_is);
-        if (p + 1 < FM / 2) __syncthreads();     // read before the next rows
+        flush(abuf, achunks, i, ors, uint32_t(a.W / 2) * EB, uint32_t(a.W - cur.n0) / 2 * EB,
+              std::integral_constant<int, 0>());
+        if (a.h_saved) flush(hbuf, hchunks, i, hrs, uint32_t(a.W) * EB, uint32_t(a.W - cur.n0) * EB, stream);
+        if (EB == 4 && i + 1 < FM) __syncthreads();     // one buffer: read before the next rows
       }
     }
     if (!more) break;
-    keep();
+    if (dyn) publish(q);
+    cur = next;
+    par ^= 1;
   }
 }
 
@@ -956,8 +1038,10 @@ static int int_product(IntArgs a, const moonep_shape& s, void* ws, hipStream_t s
       if (st) return st;
       a.qcnt = ws_ptr<int32_t>(ws, ws_layout(s).flags) + kFlagQueue;
     }
-    if (a.src_index) int_gemm_tiled_kernel<true, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
-    else int_gemm_tiled_kernel<false, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
+    if (OUT != kIntFloatAdd && a.src_index)
+      int_gemm_tiled_kernel<OUT != kIntFloatAdd, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
+    else
+      int_gemm_tiled_kernel<false, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
     return launch_status();
   }
   // a segment's rows are shared out twice as finely as an even plan would need
@@ -1149,7 +1233,8 @@ extern "C" int moonep_int_gemm(const moonep_shape* shape, int64_t rows, const in
   a.NK = rows;
   a.add = add;
   a.c = c;
-  return int_product<kIntFloat>(a, s, nullptr, as_stream(stream));
+  return add ? int_product<kIntFloatAdd>(a, s, nullptr, as_stream(stream))
+             : int_product<kIntFloat>(a, s, nullptr, as_stream(stream));
 }
 
 extern "C" int moonep_int_gemm_swiglu(const moonep_shape* shape, int64_t rows, const int8_t* xq,
