@@ -472,23 +472,28 @@ __device__ inline void store4(void* base, int64_t at, v4f_t v) {
 }
 
 // ---- few rows per expert: no list of work. Work items are (share of the rows, segment of the
-// view, J blocks of 16 columns), dealt out to the workgroups in turn; a workgroup's threads look
-// up one item's cu_seqlens each and list the ones that have rows. A workgroup's four
-// wavefronts take blocks of 16 rows; where there are fewer than three, the wavefronts of a block
-// share its k-blocks in turn and their sums are added. Operands go straight to registers,
-// U blocks of 64 k at a time.
+// view, two blocks of 16 columns), dealt out to the workgroups in turn; a workgroup's threads
+// look up one item's cu_seqlens each and list the ones that have rows. A workgroup's eight
+// wavefronts take blocks of 16 rows; where there are fewer blocks, the wavefronts of a block
+// share its k-blocks in turn and their sums are added. Operands go straight to registers, four
+// blocks of 64 k at a time. The call is bound by reading each touched expert's weights once: 16
+// tokens, K = 8, 256 experts, H = 4096, H' = 1536: 114 us, 0.63 GB at 5.6 TB/s; 64 tokens, 128
+// experts, H = 4096, 2H' = 2816: 237 us, 6.1 TB/s. For one token (12 us, 50 MB) and dense products
+// (1 x 2048 x 7168: 4.4 us, 15 MB) its latency counts: two blocks and eight wavefronts took 12.1 and
+// 4.4 us, four and four 15.1 and 5.5, one and eight 13.2 and 4.4; 16 tokens 114, 112, 117.
 constexpr int kIntRows = 64;      // rows at a time
-constexpr int kIntItems = 256;    // items looked up at a time
+constexpr int kIntBlocks = 2, kIntDepth = 4, kIntWaves = 8;
 
-// Block j of item t: with SwiGLU and J = 2 a gate block and its up block, 32 columns further.
-template <int J, int OUT>
+// Block j of item t: with SwiGLU a gate block and its up block, 32 columns further.
+template <int OUT>
 __device__ inline int item_block(int t, int j) {
-  return is_swiglu(OUT) && J == 2 ? 4 * (t >> 1) + (t & 1) + 2 * j : J * t + j;
+  return is_swiglu(OUT) ? 4 * (t >> 1) + (t & 1) + 2 * j : 2 * t + j;
 }
 
-template <int J, int U, int OUT>
+template <int OUT>
 __device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v, int m0_v, int n,
-                                    int t_v, v4i_t (*s_part)[J][64]) {
+                                    int t_v, v4i_t (*s_part)[kIntBlocks][64]) {
+  constexpr int J = kIntBlocks, U = kIntDepth, WAVES = kIntWaves;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kb = lane >> 4, r16 = lane & 15;
@@ -496,43 +501,53 @@ __device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v,
   const int wrow = __builtin_amdgcn_readfirstlane(wrow_v);
   const int m0 = __builtin_amdgcn_readfirstlane(m0_v), t = __builtin_amdgcn_readfirstlane(t_v);
   const int rows = __builtin_amdgcn_readfirstlane(min(kIntRows, n - m0));
-  const int split = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;   // wavefronts per block of rows
+  const int split = rows <= 16 ? WAVES : rows <= 32 ? WAVES / 2 : WAVES / 4;   // wavefronts per block of rows
   const int part = w % split, r0 = w / split * 16;
   const bool work = r0 < rows;    // uniform
   const int64_t pos = int64_t(rowbase) + m0 + r0 + r16;
   bool in = work && r0 + r16 < rows;
-  const bool store = in;
+  const bool store = in && part == 0;
   int64_t arow = pos;
   v4i_t acc[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) acc[j] = v4i_t{0, 0, 0, 0};
+  float sa = 0.0f;
+  v4f_t sw[J];
   if (work) {
+    const v4i_t* wq[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int64_t blk = int64_t(wrow) * a.NB + min(item_block<OUT>(t, j), a.NB - 1);
+      wq[j] = reinterpret_cast<const v4i_t*>(a.wq) + lane + blk * a.KB * 64;
+      sw[j] = a.ws ? *reinterpret_cast<const v4f_t*>(a.ws + blk * 16 + 4 * kb) : v4f_t{1.f, 1.f, 1.f, 1.f};
+    }
+    // a wavefront takes runs of U blocks; weights first, whose addresses wait for nothing
+    v4i_t fa[U], fb[U][J];
+    auto weights = [&](int c0) {
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          fb[k][j] = c0 + k < a.KB ? wq[j][(c0 + k) * 64] : v4i_t{0, 0, 0, 0};    // uniform
+    };
+    if (part * U < a.KB) weights(part * U);
     if (a.src_index) {
       const int u = in ? a.src_index[pos] : -1;
       in = u >= 0 && u < a.NK;
       arow = in ? u / a.K : 0;
     }
+    if (in) sa = a.xs[arow];
     const v4i_t* xq = reinterpret_cast<const v4i_t*>(a.xq) + arow * a.KB * 4 + kb;
-    const v4i_t* wq[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      wq[j] = reinterpret_cast<const v4i_t*>(a.wq) + lane +
-              (int64_t(wrow) * a.NB + min(item_block<J, OUT>(t, j), a.NB - 1)) * a.KB * 64;
-    // KB is even; a wavefront takes runs of U blocks
     for (int c0 = part * U; c0 < a.KB; c0 += split * U) {
-      v4i_t fa[U], fb[U][J];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const bool there = c0 + k < a.KB;   // uniform
-        fa[k] = there && in ? xq[(c0 + k) * 4] : v4i_t{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < J; ++j) fb[k][j] = there ? wq[j][(c0 + k) * 64] : v4i_t{0, 0, 0, 0};
-      }
+      for (int k = 0; k < U; ++k)
+        fa[k] = c0 + k < a.KB && in ? xq[(c0 + k) * 4] : v4i_t{0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int j = 0; j < J; ++j)      // operands swapped: a lane holds 4 columns of one row
           acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[k][j], fa[k], acc[j], 0, 0, 0);
+      if (c0 + split * U < a.KB) weights(c0 + split * U);
     }
   }
   if (split > 1) {       // uniform
@@ -546,17 +561,13 @@ __device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v,
         for (int j = 0; j < J; ++j) acc[j] += s_part[w + o - 1][j][lane];
     __syncthreads();     // read before the next entry's sums
   }
-  if (!store || part != 0) return;
-  const float sa = in ? a.xs[arow] : 0.0f;
+  if (!store) return;
   v4f_t v[J];
   int col[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int blk = item_block<J, OUT>(t, j);
-    col[j] = blk * 16 + 4 * kb;
-    const v4f_t sw = a.ws ? *reinterpret_cast<const v4f_t*>(a.ws + (int64_t(wrow) * a.NB + min(blk, a.NB - 1)) * 16 + 4 * kb)
-                          : v4f_t{1.f, 1.f, 1.f, 1.f};
-    v[j] = int_scaled(acc[j], sa, sw);
+    col[j] = item_block<OUT>(t, j) * 16 + 4 * kb;
+    v[j] = int_scaled(acc[j], sa, sw[j]);
   }
   if constexpr (!is_swiglu(OUT)) {
 #pragma unroll
@@ -585,18 +596,20 @@ struct IntItem {
   int32_t rowbase, wrow, m0, n;
 };
 
-template <int J, int U, int OUT>
-__global__ __launch_bounds__(256) void int_gemm_kernel(IntArgs a, int shares) {
-  __shared__ __align__(16) v4i_t s_part[3][J][64];
-  __shared__ IntItem s_item[kIntItems];
-  __shared__ int s_t[kIntItems];
-  __shared__ int s_wave[4];
+template <int OUT>
+__global__ __launch_bounds__(kIntWaves * 64) void int_gemm_kernel(IntArgs a, int shares) {
+  constexpr int J = kIntBlocks, WAVES = kIntWaves;
+  constexpr int ITEMS = WAVES * 64;      // items looked up at a time
+  __shared__ __align__(16) v4i_t s_part[WAVES - 1][J][64];
+  __shared__ IntItem s_item[ITEMS];
+  __shared__ int s_t[ITEMS];
+  __shared__ int s_wave[WAVES];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int NT = (a.NB + J - 1) / J, EB = a.E + a.B;
   const int64_t segs = a.cu ? int64_t(a.R) * EB : 1;
   const int64_t total = segs * shares * NT;
-  for (int64_t t0 = blockIdx.x; t0 < total; t0 += int64_t(gridDim.x) * kIntItems) {
+  for (int64_t t0 = blockIdx.x; t0 < total; t0 += int64_t(gridDim.x) * ITEMS) {
     const int64_t t = t0 + int64_t(threadIdx.x) * gridDim.x;
     IntItem it{0, 0, 0, 0};
     int tn = 0;
@@ -620,7 +633,7 @@ __global__ __launch_bounds__(256) void int_gemm_kernel(IntArgs a, int shares) {
     __syncthreads();
     int at = __popcll(have & ((uint64_t(1) << lane) - 1)), count = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < WAVES; ++i) {
       if (i < w) at += s_wave[i];
       count += s_wave[i];
     }
@@ -632,7 +645,7 @@ __global__ __launch_bounds__(256) void int_gemm_kernel(IntArgs a, int shares) {
     for (int i = 0; i < count; ++i) {
       const IntItem te = s_item[i];
       for (int m0 = te.m0; m0 < te.n; m0 += shares * kIntRows)
-        int_few_rows<J, U, OUT>(a, te.rowbase, te.wrow, m0, te.n, s_t[i], s_part);
+        int_few_rows<OUT>(a, te.rowbase, te.wrow, m0, te.n, s_t[i], s_part);
     }
     __syncthreads();     // the list is read before the next one
   }
@@ -1011,6 +1024,227 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
   }
 }
 
+// ---- small tiles: where 256 x 256 tiles would leave CUs without one. BT x BT tiles by eight
+// wavefronts, both operands through LDS as in the tiled form, in a ring of four steps that is in
+// flight but for one: a tile's time is its loads' latency and what a step takes from barrier to
+// barrier. 64 x 64 tiles have two groups of wavefronts, which share a step's 256 k and add their
+// sums at the end: half the barriers per k.
+template <int BT>
+struct IntSmall {
+  static constexpr int THREADS = 512, STAGES = 4;
+  static constexpr int GROUPS = BT == 64 ? 2 : 1, WAVES_N = BT == 64 ? 2 : 4;   // 2 x WAVES_N wavefronts a group
+  static constexpr int FM = BT / 32, FN = 2;
+  static constexpr int OP_BYTES = BT * 128, PART = 2 * OP_BYTES, STAGE = GROUPS * PART;
+  static constexpr int A_DMAS = OP_BYTES / 1024 / (8 / GROUPS), DMAS = 2 * A_DMAS;   // per wavefront and step
+};
+
+template <int BT, bool GATHER, int OUT>
+__global__ __launch_bounds__(512) void int_gemm_small_kernel(IntArgs a) {
+  typedef IntSmall<BT> T;
+  constexpr int FM = T::FM, FN = T::FN, WPG = 8 / T::GROUPS;
+  __shared__ __align__(1024) char smem[T::STAGES * T::STAGE];
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = wid / WPG, w = wid % WPG;                // group, wavefront in it
+  const int wm = w / T::WAVES_N, wn = w % T::WAVES_N;
+  const int r16 = lane & 15, kb = lane >> 4;
+  const uint32_t lds0 = lds_addr(smem);
+  const int NT = (a.W + BT - 1) / BT;
+  // A plan's tiles, without a list of them and its launch: thread t counts those of its run of
+  // segments and s_upto[t] tells how many come before it.
+  __shared__ int s_upto[T::THREADS + 1];
+  __shared__ int s_waves[8];
+  const int EB = a.E + a.B, segs = a.R * EB, run = (segs + T::THREADS - 1) / T::THREADS;
+  auto length = [&](int seg, int& c0) {
+    const int32_t* at = a.cu + int64_t(seg / EB) * (EB + 1) + seg % EB;
+    c0 = at[0];
+    return at[1] - c0;
+  };
+  int nent = int((a.NK + BT - 1) / BT);
+  if (a.cu) {
+    int count = 0, c0;
+    for (int i = 0; i < run; ++i) {
+      const int seg = threadIdx.x * run + i;
+      if (seg < segs) count += (max(0, length(seg, c0)) + BT - 1) / BT;
+    }
+    int upto = count;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 63) s_waves[wid] = upto;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < wid) upto += s_waves[i];
+    s_upto[threadIdx.x + 1] = upto;
+    if (threadIdx.x == 0) s_upto[0] = 0;
+    __syncthreads();
+    nent = s_upto[T::THREADS];
+  }
+  auto entry = [&](int ent) {
+    int lo = 0, hi = T::THREADS;       // s_upto[lo] <= ent < s_upto[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (s_upto[mid] <= ent) lo = mid;
+      else hi = mid;
+    }
+    int before = s_upto[lo], seg = lo * run, c0, n = 0;
+    for (int i = 0; i < run; ++i, ++seg) {      // uniform
+      n = max(0, length(seg, c0));
+      const int t = (n + BT - 1) / BT;
+      if (ent < before + t) break;
+      before += t;
+    }
+    const int rank = seg / EB, i = seg % EB;
+    return TileEntry{rank * a.SK + c0, i < a.E ? i : a.E + rank * a.B + (i - a.E), (ent - before) * BT, n};
+  };
+  const int64_t total = int64_t(nent) * NT;
+  const int nparts = a.KB / 2, nsteps = (nparts + T::GROUPS - 1) / T::GROUPS;
+  const uint32_t qrow = uint32_t(a.KB) * 64;
+  // the workgroups of one XCD take a contiguous run of tiles per round: of one weight all its
+  // columns' rows, of a list all columns of its entries
+  const int G = gridDim.x, per = G / 8;
+  for (int64_t tau = (blockIdx.x % 8) * per + blockIdx.x / 8; tau < total; tau += G) {
+    const int ent = int(a.cu ? tau / NT : tau % nent), nt = int(a.cu ? tau % NT : tau / nent);
+    const TileEntry e = a.cu ? entry(ent) : TileEntry{0, 0, ent * BT, int(a.NK)};
+    const int rowbase = __builtin_amdgcn_readfirstlane(e.rowbase + e.m0);
+    const int wrow = __builtin_amdgcn_readfirstlane(e.wrow);
+    const int rows = __builtin_amdgcn_readfirstlane(min(BT, e.n - e.m0));
+    const int n0 = nt * BT;
+    const int nblocks = min(BT / 16, a.NB - n0 / 16);
+    auto row_of = [&](int row, bool& in) -> int64_t {      // token row of a row of the tile
+      in = row < rows;
+      if (!GATHER) return int64_t(rowbase) + row;
+      const int u = in ? a.src_index[rowbase + row] : -1;
+      in = u >= 0 && u < a.NK;
+      return in ? u / a.K : 0;
+    };
+    const int64_t first = GATHER ? 0 : rowbase;
+    const __amdgpu_buffer_rsrc_t ars =
+        make_rsrc(a.xq + first * qrow, clamp_bytes((GATHER ? a.xrows : rows) * qrow));
+    const __amdgpu_buffer_rsrc_t brs =
+        make_rsrc(a.wq + (int64_t(wrow) * a.NB + n0 / 16) * a.KB * 1024, uint32_t(nblocks * a.KB) * 1024);
+    uint32_t va[T::A_DMAS], vb[T::A_DMAS];
+#pragma unroll
+    for (int i = 0; i < T::A_DMAS; ++i) {
+      const int b = w + WPG * i, row = b * 8 + (lane >> 3), j = b >> 1;
+      bool in;
+      const int64_t r = row_of(row, in) - first;
+      va[i] = in ? uint32_t(r) * qrow + ((lane & 7) ^ swz_k(row)) * 16 : kOffNone;
+      vb[i] = j < nblocks ? uint32_t((j * a.KB + (b & 1)) * 1024 + lane * 16) : kOffNone;
+    }
+    // the group's part of step k; past the last part zeros, so that every step has its DMAs
+    auto issue = [&](int k, uint32_t stage) {
+      const int p = k * T::GROUPS + g;
+      const bool there = T::GROUPS == 1 || p < nparts;
+      const uint32_t st = lds0 + stage + g * T::PART;
+#pragma unroll
+      for (int i = 0; i < T::A_DMAS; ++i)
+        dma16(ars, there ? va[i] : kOffNone, uint32_t(p) * 128, st + (w + WPG * i) * 1024);
+#pragma unroll
+      for (int i = 0; i < T::A_DMAS; ++i)
+        dma16(brs, there ? vb[i] : kOffNone, uint32_t(p) * 2048, st + T::OP_BYTES + (w + WPG * i) * 1024);
+    };
+    auto wait_steps = [&](int n) {     // until at most n later steps are in flight
+      if (n >= 2) wait_vm<2 * T::DMAS>();
+      else if (n == 1) wait_vm<T::DMAS>();
+      else wait_vm<0>();
+    };
+    __syncthreads();     // every wavefront is done with the previous tile's LDS
+#pragma unroll
+    for (int k = 0; k < T::STAGES - 1; ++k)
+      if (k < nsteps) issue(k, k * T::STAGE);
+    v4i_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = v4i_t{0, 0, 0, 0};
+    const int row0 = wm * (BT / 2);
+    // the wavefront's two blocks of columns lie 32 apart: gate and up
+    auto block = [&](int j) { return (wn >> 1) * 4 + (wn & 1) + 2 * j; };
+    uint32_t cur = 0, fill = (T::STAGES - 1) * T::STAGE;
+    auto after = [](uint32_t s) { return s + T::STAGE == T::STAGES * T::STAGE ? 0u : s + T::STAGE; };
+    for (int k = 0; k < nsteps; ++k) {
+      wait_steps(min(T::STAGES - 2, nsteps - 1 - k));
+      __syncthreads();     // step k has landed, and every wavefront has read step k - 1
+      if (k + T::STAGES - 1 < nsteps) issue(k + T::STAGES - 1, fill);
+      const char* st = smem + cur + g * T::PART;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        v4i_t fa[FM], fb[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          fb[j] = *reinterpret_cast<const v4i_t*>(st + T::OP_BYTES + (block(j) * 2 + ks) * 1024 + lane * 16);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          fa[i] = *reinterpret_cast<const v4i_t*>(st + (row0 + i * 16 + r16) * 128 +
+                                                  (((ks * 4 + kb) ^ swz_k(r16)) << 4));
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      }
+      cur = after(cur);
+      fill = after(fill);
+    }
+    if constexpr (T::GROUPS == 2) {
+      // each group takes the other's sums of its row block (FM = 2: block i is group i's)
+      v4i_t(*part)[FN][64] = reinterpret_cast<v4i_t(*)[FN][64]>(smem);      // [8][FN][64]
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < FN; ++j) part[wid][j][lane] = g ? acc[0][j] : acc[1][j];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const v4i_t other = part[wid ^ WPG][j][lane];
+        acc[0][j] = (g ? acc[1][j] : acc[0][j]) + other;
+      }
+    }
+    constexpr int ROWS = FM / T::GROUPS;      // row blocks that a wavefront stores
+    int col[FN];
+    v4f_t sw[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      col[j] = n0 + block(j) * 16 + 4 * kb;
+      sw[j] = a.ws && col[j] < a.W ? *reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.NB * 16 + col[j])
+                                   : v4f_t{1.f, 1.f, 1.f, 1.f};
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int row = row0 + (i + g * ROWS) * 16 + r16;
+      if (row >= rows) continue;
+      bool in;
+      const int64_t r = row_of(row, in);
+      const float sa = in ? a.xs[r] : 0.0f;
+      const int64_t pos = int64_t(rowbase) + row;
+      v4f_t v[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) v[j] = int_scaled(acc[i][j], sa, sw[j]);
+      if constexpr (!is_swiglu(OUT)) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          if (col[j] < a.W) {
+            if constexpr (OUT == kIntFloatAdd)
+              v[j] = added(v[j], *reinterpret_cast<const v4f_t*>(a.add + pos * a.W + col[j]));
+            *reinterpret_cast<v4f_t*>(a.c + pos * a.W + col[j]) = v[j];
+          }
+      } else if (col[0] < a.W) {
+        v4f_t s;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] = int_swiglu<OUT>(v[0][x], v[1][x]);
+        store4<OUT>(a.act, pos * (a.W / 2) + col[0] / 64 * 32 + col[0] % 32, s);
+        if (a.h_saved) {
+          store4<OUT>(a.h_saved, pos * a.W + col[0], v[0]);
+          store4<OUT>(a.h_saved, pos * a.W + col[1], v[1]);
+        }
+      }
+    }
+  }
+}
+
 static int int_grid(int64_t work, int64_t cap) {
   const int64_t blocks = (work + kIntThreads - 1) / kIntThreads;
   return int(blocks < 1 ? 1 : (blocks > cap ? cap : blocks));
@@ -1019,35 +1253,64 @@ static int int_grid(int64_t work, int64_t cap) {
 inline int64_t int_kb(int width) { return 2 * k_tiles(width); }      // blocks of 64 k
 inline int64_t int_nb(int width) { return (int64_t(width) + 15) / 16; }
 
+template <int BT, int OUT>
+static int launch_small(const IntArgs& a, int grid, hipStream_t strm) {
+  if (OUT != kIntFloatAdd && a.src_index)      // an add comes with dense products alone
+    int_gemm_small_kernel<BT, OUT != kIntFloatAdd, OUT><<<grid, IntSmall<BT>::THREADS, 0, strm>>>(a);
+  else
+    int_gemm_small_kernel<BT, false, OUT><<<grid, IntSmall<BT>::THREADS, 0, strm>>>(a);
+  return launch_status();
+}
+
 // ws: the layer's workspace, for a grouped product's tile list; s its shape.
+//
+// Which form, by rows per weight row, and by how many tiles there are to hand out (counting half
+// a tile of padding per weight row). us, few rows / 64 x 64 / 128 x 128 / 256 x 256 tiles:
+//   grouped 256 x (4096, 1536), rows each: 4: 242/258/259/289, 8: 268/276/267/293, 16:
+//     334/289/276/295, 32: 466/317/290/298, 64: 803/416/325/312, 256: 2884/1260/714/509
+//   grouped 64 x (7168, 2048): 8: 162/165/166/185, 16: 206/171/168/185, 32: 302/193/174/187, 64:
+//     488/242/214/192, 256: 1664/709/388/294
+//   grouped 16 x (1024, 512): 8: 4.7/7.3/9.5/22, 32: 6.2/7.8/11/22, 128: 14/13/13/26, 512: 40/30/23/28
+//   dense (2048, 7168), rows: 16: 5.4/7.1/12/23, 32: 6.5/7.2/12/23, 48: 7.6/7.4/13/23, 128:
+//     16/8.4/17/24, 512: 45/27/19/36, 1024: 86/43/33/39, 2048: 167/93/61/45
+//   dense (7168, 4096): 32: 13/15/31/50, 48: 18/15/32/50, 512: 77/28/35/72, 1024: 151/61/38/74,
+//     2048: 299/134/74/83, 4096: 595/259/142/89
+//   dense (7168, 512): 32: 13/15/31/42, 64: 22/15/33/49, 2048: 43/22/36/71, 4096: 81/40/37/79, 16384:
+//     306/145/83/90
+// So: few rows up to 8 each (a dense product, which reads its one weight from the caches, up to
+// 32); 256-row tiles from 64 rows each on, if they are more than half as many as the CUs; below,
+// 128-row tiles if those are, else 64-row tiles.
 template <int OUT>
 static int int_product(IntArgs a, const moonep_shape& s, void* ws, hipStream_t strm) {
   const int cus = device_cus();
   if (cus <= 0) return MOONEP_EHIP;
-  const int64_t nt = (int64_t(a.W) + IntTile::BN - 1) / IntTile::BN;
-  const int64_t segs = a.cu ? int64_t(a.E) + a.R : 1;      // a plan has at most this many segments
+  const int64_t segs = a.cu ? int64_t(s.E) + s.R : 1;      // a plan has at most this many segments
   a.xrows = a.src_index ? int64_t(s.R) * s.S : a.NK;
-  const bool tiled = cus % 8 == 0 && a.NK >= 64 * segs &&
-                     // 32-bit offsets of gathered rows and of a tile's outputs, and tile numbers
-                     (!a.src_index || a.xrows * a.KB * 64 < int64_t(kOffNone)) &&
-                     int64_t(IntTile::BM) * a.W * 4 <= int64_t(kOffNone) &&
-                     (a.NK / IntTile::BM + 1 + (a.cu ? int64_t(a.R) * (a.E + a.B) : 0)) * nt < INT32_MAX;
-  if (tiled) {
-    if (a.cu) {
-      const int st = launch_tile_list(s, a.cu, IntTile::BM, ws, strm, &a.tiles, &a.ntiles);
-      if (st) return st;
-      a.qcnt = ws_ptr<int32_t>(ws, ws_layout(s).flags) + kFlagQueue;
+  auto tiles = [&](int64_t bt) { return (a.NK + bt / 2 * segs + bt - 1) / bt * ((int64_t(a.W) + bt - 1) / bt); };
+  // 32-bit offsets of gathered rows, and the order of tiles over the XCDs
+  const bool fits = cus % 8 == 0 && (!a.src_index || a.xrows * a.KB * 64 < int64_t(kOffNone));
+  if (fits && a.NK > (a.cu ? 8 : 32) * segs) {
+    if (a.NK >= 64 * segs && tiles(IntTile::BM) > cus / 2 &&
+        // 32-bit offsets of a tile's outputs, and tile numbers
+        int64_t(IntTile::BM) * a.W * 4 <= int64_t(kOffNone) &&
+        tiles(IntTile::BM) + int64_t(s.R) * (s.E + s.B) * ((a.W + IntTile::BN - 1) / IntTile::BN) < INT32_MAX) {
+      if (a.cu) {
+        const int st = launch_tile_list(s, a.cu, IntTile::BM, ws, strm, &a.tiles, &a.ntiles);
+        if (st) return st;
+        a.qcnt = ws_ptr<int32_t>(ws, ws_layout(s).flags) + kFlagQueue;
+      }
+      if (OUT != kIntFloatAdd && a.src_index)
+        int_gemm_tiled_kernel<OUT != kIntFloatAdd, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
+      else
+        int_gemm_tiled_kernel<false, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
+      return launch_status();
     }
-    if (OUT != kIntFloatAdd && a.src_index)
-      int_gemm_tiled_kernel<OUT != kIntFloatAdd, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
-    else
-      int_gemm_tiled_kernel<false, OUT><<<cus, IntTile::THREADS, 0, strm>>>(a);
-    return launch_status();
+    return tiles(128) > cus / 2 ? launch_small<128, OUT>(a, cus, strm) : launch_small<64, OUT>(a, cus, strm);
   }
   // a segment's rows are shared out twice as finely as an even plan would need
   const int64_t share = (2 * a.NK + segs * kIntRows - 1) / (segs * kIntRows);
   const int shares = int(share < 64 ? share : 64);
-  int_gemm_kernel<4, 4, OUT><<<cus * 8, 256, 0, strm>>>(a, shares);
+  int_gemm_kernel<OUT><<<cus * 4, kIntWaves * 64, 0, strm>>>(a, shares);
   return launch_status();
 }
 

@@ -144,6 +144,8 @@ def _check_layer(cfg, alpha, experts=None, seed=0):
     dict(R=4, S=64, E=8, K=2, B=1, H=1408, Hp=192),              # overflow rows
     dict(R=1, S=700, E=4, K=2, B=0, H=584, Hp=520),              # segments beyond a tile
     dict(R=2, S=512, E=8, K=4, B=4, H=320, Hp=600),
+    dict(R=2, S=2048, E=8, K=2, B=2, H=200, Hp=520),             # 128-row tiles
+    dict(R=8, S=600, E=16, K=2, B=2, H=1032, Hp=1096),           # 256-row tiles
 ])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_layer_against_the_oracle(kw, dtype):
@@ -233,7 +235,8 @@ def test_rows_in_place_and_bad_positions(S, cu, part):
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("rows,H,Hp", [(1, 64, 64), (1, 2048, 328), (5, 8, 8), (16, 200, 600), (17, 128, 64),
                                        (40, 136, 1000), (65, 1408, 80), (300, 72, 520),
-                                       (1000, 256, 264), (4100, 512, 2048), (5000, 64, 8200), (9000, 200, 2600)])
+                                       (1000, 256, 264), (4100, 512, 2048), (5000, 64, 8200), (9000, 200, 2600),
+                                       (1100, 328, 2056), (33, 128, 16)])
 def test_dense_product(rows, H, Hp, dtype):
     say("int dense", rows, H, Hp, dtype)
     sh, x, w, xq, xs, wq, ws = _operands(H, Hp, rows, dtype=dtype, seed=rows)
@@ -251,7 +254,7 @@ def test_dense_product(rows, H, Hp, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("rows,H,Hp,E", [(1, 64, 32, 1), (16, 200, 96, 1), (37, 136, 352, 4), (300, 72, 160, 3),
-                                         (900, 256, 128, 2), (5000, 320, 416, 4)])
+                                         (900, 256, 128, 2), (5000, 320, 416, 4), (20000, 136, 416, 4), (6000, 72, 992, 1)])
 def test_swiglu_against_the_two_steps(rows, H, Hp, E, dtype):
     """The fused product against the product followed by moonep_swiglu, dense and grouped: the same
     pre-activation, the same activation in float32, and in bfloat16 one whose exponential and
