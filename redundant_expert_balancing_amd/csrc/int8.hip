@@ -16,15 +16,26 @@ constexpr float kIntLeast = 0x1p-126f;       // the smallest scale
 constexpr uint32_t kIntNan = 0x7FC00000u;
 constexpr int kIntFewRows = 2048;            // fewer rows share a workgroup or more each
 constexpr int kIntChunk = 16;                // positions in a row of the gradient's rounding
+// Infinity Cache, 256 MiB: gradient rows beyond it are stored past the caches. 262144 rows of 4096
+// 504 -> 459 us, and the product that reads them loses nothing; in int_quantize_kernel 268 MB (65536
+// rows of 4096) made no difference, and 117 MB (16384 of 7168) cost the product 25 us.
+constexpr int64_t kIntCache = int64_t(1) << 28;
 typedef float v4f_t __attribute__((ext_vector_type(4)));
 
 // ---- rounding to 8 bits
 //
 // Scale of magnitudes up to amax_bits (as bits; integer order ranks Inf and NaN highest).
+// The quotient by 127 is the product with the rounded reciprocal and one correction by the exact
+// remainder: correctly rounded for every float32 whose quotient is a normal number (checked for
+// all mantissas).
 __device__ inline float int_scale(uint32_t amax_bits) {
-  if (amax_bits >= 0x7F800000u) return __uint_as_float(kIntNan);
-  return fmaxf(__uint_as_float(amax_bits) / 127.0f, kIntLeast);
+  constexpr float kInv = 1.0f / 127.0f;
+  const float m = __uint_as_float(amax_bits), q = m * kInv;
+  const float s = fmaxf(fmaf(fmaf(-q, 127.0f, m), kInv, q), kIntLeast);
+  return amax_bits >= 0x7F800000u ? __uint_as_float(kIntNan) : s;
 }
+// 1 / s, off by a unit in the last place (s is normal, and so is this)
+__device__ inline float int_inverse(float s) { return __builtin_amdgcn_rcpf(s); }
 
 // The whole number nearest to the exact x / s, ties to even; inv = 1 / s in float32. x * inv is
 // off by a few units in its last place, so its nearest whole number is at most one away. The
@@ -45,14 +56,17 @@ __device__ inline uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_
   return __builtin_amdgcn_perm(b, a, 0x0c0c0400u) | __builtin_amdgcn_perm(d, c, 0x04000c0cu);
 }
 
-// N whole numbers as bytes
-template <int N>
+// N whole numbers as bytes; STREAM: past the caches
+template <int N, bool STREAM = false>
 __device__ inline void int_store(int8_t* at, const int* w) {
   uint32_t p[N / 4];
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) p[i] = low_bytes(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  if constexpr (N == 8) *reinterpret_cast<uint2*>(at) = make_uint2(p[0], p[1]);
-  else *reinterpret_cast<uint32_t*>(at) = p[0];
+  typedef typename std::conditional<N == 8, uint64_t, uint32_t>::type word;
+  word all = p[0];
+  if constexpr (N == 8) all |= word(p[1]) << 32;
+  if constexpr (STREAM) __builtin_nontemporal_store(all, reinterpret_cast<word*>(at));
+  else *reinterpret_cast<word*>(at) = all;
 }
 
 // N values of a row with scale s, rounded and stored. Adding 1.5 * 2^23 to the quotient leaves
@@ -61,7 +75,7 @@ __device__ inline void int_store(int8_t* at, const int* w) {
 // whether any value of the lane is so near a border that the sum may have chosen the wrong side
 // (then, rarely, all of them are rounded the long way). 65536 bfloat16 rows of 4096: with
 // every value the long way the kernel was bound by its instructions (146 us).
-template <int N>
+template <int N, bool STREAM = false>
 __device__ inline void int_round_store(int8_t* at, const float* v, float s, float inv) {
   constexpr float kMagic = 0x1.8p23f;
   int w[N];
@@ -80,20 +94,33 @@ __device__ inline void int_round_store(int8_t* at, const float* v, float s, floa
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = 0;
   }
-  int_store<N>(at, w);
+  int_store<N, STREAM>(at, w);
+}
+
+// The largest of a wavefront's values, uniform: within rows of 16 lanes by DPP, then of the rows.
+__device__ inline uint32_t wave_max(uint32_t v) {
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false)));   // quad_perm 1,0,3,2
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, false)));   // quad_perm 2,3,0,1
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, false)));  // row_half_mirror
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x140, 0xF, 0xF, false)));  // row_mirror
+  const uint32_t a = __builtin_amdgcn_readlane(int(v), 0), b = __builtin_amdgcn_readlane(int(v), 16);
+  const uint32_t c = __builtin_amdgcn_readlane(int(v), 32), d = __builtin_amdgcn_readlane(int(v), 48);
+  return max(max(a, b), max(c, d));
 }
 
 // The largest m of a row that WPR wavefronts share (a whole workgroup, unless it is one
-// wavefront); part: WPR words of LDS, not written again before every wavefront has read them.
+// wavefront), uniform; part: WPR words of LDS, not written again before every wavefront has read
+// them.
 template <int WPR>
 __device__ inline uint32_t row_max(uint32_t m, uint32_t* part) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = max(m, uint32_t(__shfl_xor(int(m), d, 64)));
+  m = wave_max(m);
   if constexpr (WPR > 1) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
     __syncthreads();
+    m = 0;
 #pragma unroll
     for (int i = 0; i < WPR; ++i) m = max(m, part[i]);
+    m = __builtin_amdgcn_readfirstlane(int(m));
   }
   return m;
 }
@@ -145,7 +172,7 @@ __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_kernel(const ui
     }
     const float s = int_scale(row_max<WPR>(m, part[turn]));
     turn ^= 1;
-    const float inv = 1.0f / s;
+    const float inv = int_inverse(s);
     auto put = [&](int c, const V& h) {
       float v[V::N];
 #pragma unroll
@@ -194,106 +221,112 @@ __device__ inline int segment_of(const int32_t* cu, int EB, int pos, int lane) {
 
 // The upstream row of a position times the scales of its expert's columns, rounded as
 // int_quantize_kernel rounds. WPR wavefronts (or each wavefront alone) take a chunk of positions
-// in a row and hold the columns' scales while the expert stays the same; the next row is on
-// its way while one is rounded. VPL as there.
-template <bool BF16, int WPR, int VPL>
+// in a row: what is looked up per position is looked up by a lane each beforehand, the
+// columns' scales stay in registers while the expert is the same, and the next row is on its
+// way while one is rounded. VPL as there. 262144 positions of 32768 tokens, 4096 wide: 459 us,
+// 1.07 GB written and 2.1 GB of rows read (0.27 GB of them from HBM) at 7 TB/s; 504 us if the
+// output goes through the caches, 315 with every position on one token's row. Shares of all
+// experts at a time, so that the workgroups of an XCD read the same tokens: 502 us.
+template <bool BF16, int WPR, int VPL, bool STREAM>
 __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(IntGradArgs a) {
   typedef RowVec<BF16> V;
   constexpr int TPR = 64 * WPR, RPG = int_threads(WPR) / TPR, HELD = VPL ? VPL : 1;
+  static_assert(kIntChunk <= 64, "a lane per position of a chunk");
   __shared__ uint32_t part[2][WPR];
   const int lane = threadIdx.x & 63, t = threadIdx.x % TPR;
-  const int64_t p0 = (blockIdx.x * int64_t(RPG) + threadIdx.x / TPR) * a.chunk;
-  const int64_t p1 = min(p0 + a.chunk, a.NK);
-  int turn = 0;
+  const int64_t begin = (blockIdx.x * int64_t(RPG) + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR)) * a.chunk;
+  const int count = int(min(int64_t(a.chunk), a.NK - begin));      // uniform; below 1: nothing to do
+  if (count <= 0) return;                                          // all of a row's wavefronts
+  const int p0 = int(begin);
+  // lane i: source row of position p0 + i (-1: none), its gate, and in the end its scale
+  int my_row = p0 + lane;
+  float my_gate = 1.0f, my_scale = 0.0f;
+  bool my_live = false;
+  if (a.src_index) {
+    const int u = lane < count ? a.src_index[p0 + lane] : -1;
+    const bool there = u >= 0 && u < a.NK;
+    my_row = there ? u / a.K : -1;
+    if (a.gates && there) my_gate = a.gates[u];
+  }
+  int turn = 0, wrow = 0;
   int64_t until = p0;             // positions before it belong to weight row wrow (-1: none)
-  int wrow = 0;
   float ws[HELD][V::N];
   V next[HELD];
-  bool next_there = false;
-  float next_gate = 1.0f;
-  const uint4* next_in = nullptr;
-  auto fetch = [&](int64_t p) {
-    int64_t row = p;
-    next_there = true;
-    next_gate = 1.0f;
-    if (a.src_index) {
-      const int u = a.src_index[p];
-      next_there = u >= 0 && u < a.NK;
-      row = next_there ? u / a.K : 0;
-      if (a.gates && next_there) next_gate = a.gates[u];
-    }
-    next_in = a.src + row * a.nvec;
+  auto source = [&](int i) { return __builtin_amdgcn_readlane(my_row, i); };
+  auto fetch = [&](int row) {
     if constexpr (VPL > 0) {
+      const uint4* in = a.src + int64_t(row) * a.nvec;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const int c = t + TPR * i;
-        next[i] = V{next_there && c < a.nvec ? next_in[c] : make_uint4(0, 0, 0, 0)};
+        next[i] = V{row >= 0 && c < a.nvec ? in[c] : make_uint4(0, 0, 0, 0)};
       }
     }
   };
-  if (p0 < p1) fetch(p0);
-  for (int64_t p = p0; p < p1; ++p) {
+  int row = source(0);
+  fetch(row);
+  for (int i = 0; i < count; ++i) {
+    const int p = p0 + i;
     if (p >= until) {
       wrow = 0;
       until = a.NK;
       if (a.cu) {
-        const int rank = int(p / a.SK), EB = a.E + a.B;
+        const int rank = p / a.SK, EB = a.E + a.B;
         const int32_t* cu = a.cu + int64_t(rank) * (EB + 1);
-        const int i = segment_of(cu, EB, int(p % a.SK), lane);
-        wrow = i < 0 ? -1 : i < a.E ? i : a.E + rank * a.B + (i - a.E);
-        until = int64_t(rank) * a.SK + (i < 0 ? a.SK : cu[i + 1]);
+        const int seg = segment_of(cu, EB, p - rank * a.SK, lane);
+        wrow = __builtin_amdgcn_readfirstlane(seg < 0 ? -1 : seg < a.E ? seg : a.E + rank * a.B + (seg - a.E));
+        until = int64_t(rank) * a.SK + __builtin_amdgcn_readfirstlane(seg < 0 ? a.SK : cu[seg + 1]);
       }
       if constexpr (VPL > 0) {
-        if (wrow >= 0)
+        const v4f_t* from = reinterpret_cast<const v4f_t*>(a.ws + int64_t(max(wrow, 0)) * a.wscols);
 #pragma unroll
-          for (int i = 0; i < VPL; ++i)
+        for (int k = 0; k < VPL; ++k)
 #pragma unroll
-            for (int j = 0; j < V::N / 4; ++j) {
-              const int c = t + TPR * i;
-              const v4f_t s = c < a.nvec ? reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.wscols)[c * (V::N / 4) + j]
-                                         : v4f_t{0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < V::N / 4; ++j) {
+            const int c = t + TPR * k;
+            const v4f_t s = c < a.nvec ? from[c * (V::N / 4) + j] : v4f_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) ws[i][4 * j + k] = s[k];
-            }
+            for (int e = 0; e < 4; ++e) ws[k][4 * j + e] = s[e];
+          }
       }
     }
-    const bool there = next_there;
-    const float gate = next_gate;
-    const uint4* in = next_in;
+    const int from_row = row;
     float v[HELD][V::N];
     if constexpr (VPL > 0) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
+      for (int k = 0; k < VPL; ++k)
 #pragma unroll
-        for (int k = 0; k < V::N; ++k) v[i][k] = next[i].at(k) * ws[i][k];
+        for (int e = 0; e < V::N; ++e) v[k][e] = next[k].at(e) * ws[k][e];
     }
-    if (p + 1 < p1) fetch(p + 1);
+    if (i + 1 < count) {
+      row = source(i + 1);
+      fetch(row);
+    }
     if (wrow < 0) continue;       // behind the rank's last row; uniform for the row's wavefronts
     uint32_t m = 0;
     auto most = [&](const float* h) {
 #pragma unroll
-      for (int k = 0; k < V::N; ++k) m = max(m, int_mag(h[k]));
+      for (int e = 0; e < V::N; ++e) m = max(m, int_mag(h[e]));
     };
     auto take = [&](int c, float* h) {       // VPL 0
-      const bool in_row = there && c < a.nvec;
-      const V x{in_row ? in[c] : make_uint4(0, 0, 0, 0)};
+      const bool in_row = from_row >= 0 && c < a.nvec;
+      const V x{in_row ? (a.src + int64_t(from_row) * a.nvec)[c] : make_uint4(0, 0, 0, 0)};
 #pragma unroll
       for (int j = 0; j < V::N / 4; ++j) {
         const v4f_t s = in_row ? reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.wscols)[c * (V::N / 4) + j]
                                : v4f_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[4 * j + k] = x.at(4 * j + k) * s[k];
+        for (int e = 0; e < 4; ++e) h[4 * j + e] = x.at(4 * j + e) * s[e];
       }
     };
     if constexpr (VPL > 0) {
-      // a position without a source is zeros, also where a column's scale is not a number
+      if (from_row < 0)       // zeros, also where a column's scale is not a number
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (!there)
+        for (int k = 0; k < VPL; ++k)
 #pragma unroll
-          for (int k = 0; k < V::N; ++k) v[i][k] = 0.0f;
-        most(v[i]);
-      }
+          for (int e = 0; e < V::N; ++e) v[k][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) most(v[k]);
     } else {
       for (int c = t; c < a.nvec; c += TPR) {
         take(c, v[0]);
@@ -302,22 +335,26 @@ __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(Int
     }
     const float s = int_scale(row_max<WPR>(m, part[turn]));
     turn ^= 1;
-    const float inv = 1.0f / s;
-    int8_t* out = a.q + p * a.nout * V::N;
+    const float inv = int_inverse(s);
+    int8_t* out = a.q + int64_t(p) * a.nout * V::N;
     if constexpr (VPL > 0) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int c = t + TPR * i;
-        if (c < a.nout) int_round_store<V::N>(out + c * V::N, v[i], s, inv);
+      for (int k = 0; k < VPL; ++k) {
+        const int c = t + TPR * k;
+        if (c < a.nout) int_round_store<V::N, STREAM>(out + c * V::N, v[k], s, inv);
       }
     } else {
       for (int c = t; c < a.nout; c += TPR) {
         take(c, v[0]);
-        int_round_store<V::N>(out + c * V::N, v[0], s, inv);
+        int_round_store<V::N, STREAM>(out + c * V::N, v[0], s, inv);
       }
     }
-    if (t == 0) a.scales[p] = there ? gate * s : 0.0f;
+    if (lane == i) {
+      my_live = true;
+      my_scale = from_row < 0 ? 0.0f : my_gate * s;
+    }
   }
+  if (t < 64 && my_live) a.scales[p0 + lane] = my_scale;
 }
 
 // ---- weights (set-up)
@@ -351,7 +388,7 @@ __global__ __launch_bounds__(kIntThreads) void int_quantize_weight_kernel(const 
   const int j = t >> 6, lane = t & 63, nb = n0 / 16 + j;
   if (nb >= NB) return;
   const int n = nb * 16 + (lane & 15);
-  const float s = s_scale[n - n0], inv = 1.0f / s;
+  const float s = s_scale[n - n0], inv = int_inverse(s);
   for (int kb = 0; kb < KB; ++kb) {
     int v[16];
 #pragma unroll
@@ -1540,14 +1577,21 @@ extern "C" int moonep_int_quantize_grad(const moonep_shape* shape, const void* s
                 s.R, s.E, s.B, s.S * s.K, s.K, s.Hp / vec, int(k_tiles(s.Hp)) * 128 / vec,
                 int(int_nb(s.Hp)) * 16, int64_t(s.R) * s.S * s.K, 0};
   // chunks of at most kIntChunk positions, shorter where there are few
-  const int64_t chunk = a.NK / kIntFewRows;
+  const int64_t chunk = a.NK / (4 * kIntFewRows);
   a.chunk = int(chunk < 1 ? 1 : chunk < kIntChunk ? chunk : kIntChunk);
+  const bool stream_out = a.NK * a.nout * vec > kIntCache;
   with_row_split(a.nout, a.NK < kIntFewRows, [&](auto w, auto v) {
     constexpr int WPR = decltype(w)::value, VPL = decltype(v)::value, RPG = int_threads(WPR) / (64 * WPR);
     const int64_t per = int64_t(RPG) * a.chunk;
     const int grid = int((a.NK + per - 1) / per);      // below 2^31: NK is
-    if (bf16) int_quantize_grad_kernel<true, WPR, VPL><<<grid, int_threads(WPR), 0, as_stream(stream)>>>(a);
-    else int_quantize_grad_kernel<false, WPR, VPL><<<grid, int_threads(WPR), 0, as_stream(stream)>>>(a);
+    auto launch = [&](auto type, auto past) {
+      int_quantize_grad_kernel<decltype(type)::value, WPR, VPL, decltype(past)::value>
+          <<<grid, int_threads(WPR), 0, as_stream(stream)>>>(a);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    if (bf16) stream_out ? launch(yes, yes) : launch(yes, no);
+    else stream_out ? launch(no, yes) : launch(no, no);
   });
   return launch_status();
 }
