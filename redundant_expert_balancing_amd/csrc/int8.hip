@@ -12,6 +12,7 @@ namespace moonep {
 
 constexpr int kIntThreads = 256;
 constexpr int kIntMaxK = 131072;             // 127 * 127 * 131072 < 2^31: sums stay exact
+constexpr int kIntMaxCols = 1 << 24;
 constexpr float kIntLeast = 0x1p-126f;       // the smallest scale
 constexpr uint32_t kIntNan = 0x7FC00000u;
 constexpr int kIntFewRows = 2048;            // fewer rows share a workgroup or more each
@@ -234,127 +235,129 @@ __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(Int
   static_assert(kIntChunk <= 64, "a lane per position of a chunk");
   __shared__ uint32_t part[2][WPR];
   const int lane = threadIdx.x & 63, t = threadIdx.x % TPR;
-  const int64_t begin = (blockIdx.x * int64_t(RPG) + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR)) * a.chunk;
-  const int count = int(min(int64_t(a.chunk), a.NK - begin));      // uniform; below 1: nothing to do
-  if (count <= 0) return;                                          // all of a row's wavefronts
-  const int p0 = int(begin);
-  // lane i: source row of position p0 + i (-1: none), its gate, and in the end its scale
-  int my_row = p0 + lane;
-  float my_gate = 1.0f, my_scale = 0.0f;
-  bool my_live = false;
-  if (a.src_index) {
-    const int u = lane < count ? a.src_index[p0 + lane] : -1;
-    const bool there = u >= 0 && u < a.NK;
-    my_row = there ? u / a.K : -1;
-    if (a.gates && there) my_gate = a.gates[u];
-  }
-  int turn = 0, wrow = 0;
-  int64_t until = p0;             // positions before it belong to weight row wrow (-1: none)
-  float ws[HELD][V::N];
-  V next[HELD];
-  auto source = [&](int i) { return __builtin_amdgcn_readlane(my_row, i); };
-  auto fetch = [&](int row) {
-    if constexpr (VPL > 0) {
-      const uint4* in = a.src + int64_t(row) * a.nvec;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int c = t + TPR * i;
-        next[i] = V{row >= 0 && c < a.nvec ? in[c] : make_uint4(0, 0, 0, 0)};
-      }
+  int turn = 0;
+  for (int64_t begin = (blockIdx.x * int64_t(RPG) + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR)) * a.chunk;
+       begin < a.NK; begin += int64_t(gridDim.x) * RPG * a.chunk) {
+    const int count = int(min(int64_t(a.chunk), a.NK - begin));
+    const int p0 = int(begin);
+    // lane i: source row of position p0 + i (-1: none), its gate, and in the end its scale
+    int my_row = p0 + lane;
+    float my_gate = 1.0f, my_scale = 0.0f;
+    bool my_live = false;
+    if (a.src_index) {
+      const int u = lane < count ? a.src_index[p0 + lane] : -1;
+      const bool there = u >= 0 && u < a.NK;
+      my_row = there ? u / a.K : -1;
+      if (a.gates && there) my_gate = a.gates[u];
     }
-  };
-  int row = source(0);
-  fetch(row);
-  for (int i = 0; i < count; ++i) {
-    const int p = p0 + i;
-    if (p >= until) {
-      wrow = 0;
-      until = a.NK;
-      if (a.cu) {
-        const int rank = p / a.SK, EB = a.E + a.B;
-        const int32_t* cu = a.cu + int64_t(rank) * (EB + 1);
-        const int seg = segment_of(cu, EB, p - rank * a.SK, lane);
-        wrow = __builtin_amdgcn_readfirstlane(seg < 0 ? -1 : seg < a.E ? seg : a.E + rank * a.B + (seg - a.E));
-        until = int64_t(rank) * a.SK + __builtin_amdgcn_readfirstlane(seg < 0 ? a.SK : cu[seg + 1]);
-      }
+    int wrow = 0;
+    int64_t until = p0;             // positions before it belong to weight row wrow (-1: none)
+    float ws[HELD][V::N];
+    V next[HELD];
+    auto source = [&](int i) { return __builtin_amdgcn_readlane(my_row, i); };
+    auto fetch = [&](int row) {
       if constexpr (VPL > 0) {
-        const v4f_t* from = reinterpret_cast<const v4f_t*>(a.ws + int64_t(max(wrow, 0)) * a.wscols);
+        const uint4* in = a.src + int64_t(row) * a.nvec;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const int c = t + TPR * i;
+          next[i] = V{row >= 0 && c < a.nvec ? in[c] : make_uint4(0, 0, 0, 0)};
+        }
+      }
+    };
+    int row = source(0);
+    fetch(row);
+    for (int i = 0; i < count; ++i) {
+      const int p = p0 + i;
+      if (p >= until) {
+        wrow = 0;
+        until = a.NK;
+        if (a.cu) {
+          const int rank = p / a.SK, EB = a.E + a.B;
+          const int32_t* cu = a.cu + int64_t(rank) * (EB + 1);
+          const int seg = segment_of(cu, EB, p - rank * a.SK, lane);
+          wrow = __builtin_amdgcn_readfirstlane(seg < 0 ? -1 : seg < a.E ? seg : a.E + rank * a.B + (seg - a.E));
+          until = int64_t(rank) * a.SK + __builtin_amdgcn_readfirstlane(seg < 0 ? a.SK : cu[seg + 1]);
+        }
+        if constexpr (VPL > 0) {
+          const v4f_t* from = reinterpret_cast<const v4f_t*>(a.ws + int64_t(max(wrow, 0)) * a.wscols);
+#pragma unroll
+          for (int k = 0; k < VPL; ++k)
+#pragma unroll
+            for (int j = 0; j < V::N / 4; ++j) {
+              const int c = t + TPR * k;
+              const v4f_t s = c < a.nvec ? from[c * (V::N / 4) + j] : v4f_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) ws[k][4 * j + e] = s[e];
+            }
+        }
+      }
+      const int from_row = row;
+      float v[HELD][V::N];
+      if constexpr (VPL > 0) {
 #pragma unroll
         for (int k = 0; k < VPL; ++k)
 #pragma unroll
-          for (int j = 0; j < V::N / 4; ++j) {
-            const int c = t + TPR * k;
-            const v4f_t s = c < a.nvec ? from[c * (V::N / 4) + j] : v4f_t{0.f, 0.f, 0.f, 0.f};
+          for (int e = 0; e < V::N; ++e) v[k][e] = next[k].at(e) * ws[k][e];
+      }
+      if (i + 1 < count) {
+        row = source(i + 1);
+        fetch(row);
+      }
+      if (wrow < 0) continue;       // behind the rank's last row; uniform for the row's wavefronts
+      uint32_t m = 0;
+      auto most = [&](const float* h) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ws[k][4 * j + e] = s[e];
-          }
+        for (int e = 0; e < V::N; ++e) m = max(m, int_mag(h[e]));
+      };
+      auto take = [&](int c, float* h) {       // VPL 0
+        const bool in_row = from_row >= 0 && c < a.nvec;
+        const V x{in_row ? (a.src + int64_t(from_row) * a.nvec)[c] : make_uint4(0, 0, 0, 0)};
+#pragma unroll
+        for (int j = 0; j < V::N / 4; ++j) {
+          const v4f_t s = in_row ? reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.wscols)[c * (V::N / 4) + j]
+                                 : v4f_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[4 * j + e] = x.at(4 * j + e) * s[e];
+        }
+      };
+      if constexpr (VPL > 0) {
+        if (from_row < 0)       // zeros, also where a column's scale is not a number
+#pragma unroll
+          for (int k = 0; k < VPL; ++k)
+#pragma unroll
+            for (int e = 0; e < V::N; ++e) v[k][e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) most(v[k]);
+      } else {
+        for (int c = t; c < a.nvec; c += TPR) {
+          take(c, v[0]);
+          most(v[0]);
+        }
+      }
+      const float s = int_scale(row_max<WPR>(m, part[turn]));
+      turn ^= 1;
+      const float inv = int_inverse(s);
+      int8_t* out = a.q + int64_t(p) * a.nout * V::N;
+      if constexpr (VPL > 0) {
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+          const int c = t + TPR * k;
+          if (c < a.nout) int_round_store<V::N, STREAM>(out + c * V::N, v[k], s, inv);
+        }
+      } else {
+        for (int c = t; c < a.nout; c += TPR) {
+          take(c, v[0]);
+          int_round_store<V::N, STREAM>(out + c * V::N, v[0], s, inv);
+        }
+      }
+      if (lane == i) {
+        my_live = true;
+        my_scale = from_row < 0 ? 0.0f : my_gate * s;
       }
     }
-    const int from_row = row;
-    float v[HELD][V::N];
-    if constexpr (VPL > 0) {
-#pragma unroll
-      for (int k = 0; k < VPL; ++k)
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) v[k][e] = next[k].at(e) * ws[k][e];
-    }
-    if (i + 1 < count) {
-      row = source(i + 1);
-      fetch(row);
-    }
-    if (wrow < 0) continue;       // behind the rank's last row; uniform for the row's wavefronts
-    uint32_t m = 0;
-    auto most = [&](const float* h) {
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) m = max(m, int_mag(h[e]));
-    };
-    auto take = [&](int c, float* h) {       // VPL 0
-      const bool in_row = from_row >= 0 && c < a.nvec;
-      const V x{in_row ? (a.src + int64_t(from_row) * a.nvec)[c] : make_uint4(0, 0, 0, 0)};
-#pragma unroll
-      for (int j = 0; j < V::N / 4; ++j) {
-        const v4f_t s = in_row ? reinterpret_cast<const v4f_t*>(a.ws + int64_t(wrow) * a.wscols)[c * (V::N / 4) + j]
-                               : v4f_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[4 * j + e] = x.at(4 * j + e) * s[e];
-      }
-    };
-    if constexpr (VPL > 0) {
-      if (from_row < 0)       // zeros, also where a column's scale is not a number
-#pragma unroll
-        for (int k = 0; k < VPL; ++k)
-#pragma unroll
-          for (int e = 0; e < V::N; ++e) v[k][e] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < VPL; ++k) most(v[k]);
-    } else {
-      for (int c = t; c < a.nvec; c += TPR) {
-        take(c, v[0]);
-        most(v[0]);
-      }
-    }
-    const float s = int_scale(row_max<WPR>(m, part[turn]));
-    turn ^= 1;
-    const float inv = int_inverse(s);
-    int8_t* out = a.q + int64_t(p) * a.nout * V::N;
-    if constexpr (VPL > 0) {
-#pragma unroll
-      for (int k = 0; k < VPL; ++k) {
-        const int c = t + TPR * k;
-        if (c < a.nout) int_round_store<V::N, STREAM>(out + c * V::N, v[k], s, inv);
-      }
-    } else {
-      for (int c = t; c < a.nout; c += TPR) {
-        take(c, v[0]);
-        int_round_store<V::N, STREAM>(out + c * V::N, v[0], s, inv);
-      }
-    }
-    if (lane == i) {
-      my_live = true;
-      my_scale = from_row < 0 ? 0.0f : my_gate * s;
-    }
+    if (t < 64 && my_live) a.scales[p0 + lane] = my_scale;
   }
-  if (t < 64 && my_live) a.scales[p0 + lane] = my_scale;
 }
 
 // ---- weights (set-up)
@@ -681,8 +684,8 @@ __global__ __launch_bounds__(kIntWaves * 64) void int_gemm_kernel(IntArgs a, int
     __syncthreads();
     for (int i = 0; i < count; ++i) {
       const IntItem te = s_item[i];
-      for (int m0 = te.m0; m0 < te.n; m0 += shares * kIntRows)
-        int_few_rows<OUT>(a, te.rowbase, te.wrow, m0, te.n, s_t[i], s_part);
+      for (int64_t m0 = te.m0; m0 < te.n; m0 += shares * kIntRows)
+        int_few_rows<OUT>(a, te.rowbase, te.wrow, int(m0), te.n, s_t[i], s_part);
     }
     __syncthreads();     // the list is read before the next one
   }
@@ -729,7 +732,9 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
   __shared__ int s_claim;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wid / 4, wn = wid % 4;
+  // wavefronts w and w + 4 share a SIMD: of a tile whose last 128 rows or columns are empty each
+  // SIMD has one that works
+  const int wm = wid / 4, wn = (wid + 2 * wm) % 4;
   const int r16 = lane & 15, kb = lane >> 4;
   const uint32_t lds0 = lds_addr(smem);
   const int NT = (a.W + T::BN - 1) / T::BN;
@@ -988,7 +993,7 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
           for (int h = 0; h < GOES; ++h) {
             uint32_t at, off;
             spot(chunks, h, i, ld, left, at, off);
-            add[h] = __builtin_bit_cast(v4f_t, __builtin_amdgcn_raw_buffer_load_b128(drs, off, 0, 0));
+            add[h] = __builtin_bit_cast(v4f_t, __builtin_amdgcn_raw_buffer_load_b128(drs, off, 0, kNonTemporal));
           }
         }
       };
@@ -1434,7 +1439,7 @@ extern "C" int moonep_int_quantize_weight(const moonep_shape* shape, const void*
   int st = validate(shape);
   if (st) return st;
   const moonep_shape& s = *shape;
-  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (s.H > kIntMaxK || s.Hp > kIntMaxCols) return MOONEP_ELIMIT;
   if (!aligned16(w) || !aligned16(wq) || !aligned16(wscales)) return MOONEP_EINVAL;
   const int KB = int(int_kb(s.H)), NB = int(int_nb(s.Hp));
   const dim3 grid((NB + 3) / 4, s.E);
@@ -1464,6 +1469,7 @@ extern "C" int moonep_int_prefetch_weight(const moonep_shape* shape, const int32
   int st = validate(shape);
   if (st) return st;
   const moonep_shape& s = *shape;
+  if (s.H > kIntMaxK || s.Hp > kIntMaxCols) return MOONEP_ELIMIT;
   if (s.B == 0) return MOONEP_OK;
   if (!aligned16(replica_expert) || !aligned16(wq) || (wscales && !aligned16(wscales)))
     return MOONEP_EINVAL;
@@ -1483,7 +1489,7 @@ extern "C" int moonep_int_grouped_gemm(const moonep_shape* shape, const int8_t* 
   int st = validate(shape);
   if (st) return st;
   const moonep_shape& s = *shape;
-  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (s.H > kIntMaxK || s.Hp > kIntMaxCols) return MOONEP_ELIMIT;
   if (!aligned16(cu_seqlens) || !aligned16(ws)) return MOONEP_EINVAL;
   if (ws_bytes < ws_layout(s).total) return MOONEP_EWORKSPACE;
   if (s.S == 0) return MOONEP_OK;
@@ -1503,8 +1509,8 @@ extern "C" int moonep_int_grouped_gemm_swiglu(const moonep_shape* shape, const i
   int st = validate(shape);
   if (st) return st;
   const moonep_shape& s = *shape;
-  if (s.Hp % kSwigluBlock || s.Hp > INT32_MAX / 2) return MOONEP_EINVAL;
-  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (s.Hp % kSwigluBlock) return MOONEP_EINVAL;
+  if (s.H > kIntMaxK || s.Hp > kIntMaxCols / 2) return MOONEP_ELIMIT;
   if (!aligned16(cu_seqlens) || !aligned16(ws)) return MOONEP_EINVAL;
   if (ws_bytes < ws_layout(s).total) return MOONEP_EWORKSPACE;
   if (s.S == 0) return MOONEP_OK;
@@ -1525,7 +1531,7 @@ extern "C" int moonep_int_gemm(const moonep_shape* shape, int64_t rows, const in
   if (st) return st;
   const moonep_shape& s = *shape;
   if (rows < 0 || rows > INT32_MAX) return MOONEP_EINVAL;
-  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (s.H > kIntMaxK || s.Hp > kIntMaxCols) return MOONEP_ELIMIT;
   if (rows == 0) return MOONEP_OK;
   IntArgs a;
   st = int_operands(s, s.Hp, xq, xscales, nullptr, wq, wscales, &a);
@@ -1543,9 +1549,8 @@ extern "C" int moonep_int_gemm_swiglu(const moonep_shape* shape, int64_t rows, c
   int st = validate(shape);
   if (st) return st;
   const moonep_shape& s = *shape;
-  if (rows < 0 || rows > INT32_MAX || s.Hp % kSwigluBlock || s.Hp > INT32_MAX / 2)
-    return MOONEP_EINVAL;
-  if (s.H > kIntMaxK) return MOONEP_ELIMIT;
+  if (rows < 0 || rows > INT32_MAX || s.Hp % kSwigluBlock) return MOONEP_EINVAL;
+  if (s.H > kIntMaxK || s.Hp > kIntMaxCols / 2) return MOONEP_ELIMIT;
   if (rows == 0) return MOONEP_OK;
   IntArgs a;
   st = int_operands(s, 2 * int64_t(s.Hp), xq, xscales, nullptr, wq, wscales, &a);
@@ -1583,7 +1588,8 @@ extern "C" int moonep_int_quantize_grad(const moonep_shape* shape, const void* s
   with_row_split(a.nout, a.NK < kIntFewRows, [&](auto w, auto v) {
     constexpr int WPR = decltype(w)::value, VPL = decltype(v)::value, RPG = int_threads(WPR) / (64 * WPR);
     const int64_t per = int64_t(RPG) * a.chunk;
-    const int grid = int((a.NK + per - 1) / per);      // below 2^31: NK is
+    const int64_t groups = (a.NK + per - 1) / per;
+    const int grid = int(groups < (1 << 20) ? groups : (1 << 20));
     auto launch = [&](auto type, auto past) {
       int_quantize_grad_kernel<decltype(type)::value, WPR, VPL, decltype(past)::value>
           <<<grid, int_threads(WPR), 0, as_stream(stream)>>>(a);

@@ -12,6 +12,7 @@ P = ctypes.c_void_p(0x1000)       # aligned, never dereferenced
 BAD = ctypes.c_void_p(0x1008)
 BIG = 1 << 40
 LONG = 131080                     # a reduction that could overflow int32
+WIDE = (1 << 24) + 32             # more columns than a weight may have
 
 
 def S(**kw):
@@ -57,6 +58,8 @@ def test_weight_rules():
         assert call("prefetch_weight", sh, *p) == L.EINVAL
     assert call("prefetch_weight", sh, P, P, BAD) == L.EINVAL
     assert call("prefetch_weight", S(mode=L.INFER, B=0), None, None, None) == L.OK
+    assert call("quantize_weight", S(Hp=WIDE), P, P, P) == L.ELIMIT
+    assert call("prefetch_weight", S(Hp=WIDE), P, P, P) == L.ELIMIT
 
 
 def test_grouped_rules():
@@ -66,6 +69,7 @@ def test_grouped_rules():
         assert call("grouped_gemm", sh, *p, BIG) == L.EINVAL
     assert call("grouped_gemm", sh, *good, 16) == L.EWORKSPACE
     assert call("grouped_gemm", S(H=LONG), *good, BIG) == L.ELIMIT
+    assert call("grouped_gemm", S(Hp=WIDE), *good, BIG) == L.ELIMIT
     assert call("grouped_gemm", S(H=100), *good, BIG) == L.EINVAL
     empty = (None,) * 5 + (P, None, P)
     assert call("grouped_gemm", S(S=0), *empty, BIG) == L.OK
@@ -74,7 +78,7 @@ def test_grouped_rules():
         assert call("grouped_gemm_swiglu", sh, *p, BIG) == L.EINVAL
     assert call("grouped_gemm_swiglu", sh, *good, 16) == L.EWORKSPACE
     assert call("grouped_gemm_swiglu", S(Hp=48), *good, BIG) == L.EINVAL
-    assert call("grouped_gemm_swiglu", S(Hp=1 << 30), *good, BIG) == L.EINVAL    # 2 Hp past int32
+    assert call("grouped_gemm_swiglu", S(Hp=1 << 30), *good, BIG) == L.ELIMIT    # 2 Hp past int32
     assert call("grouped_gemm_swiglu", S(H=LONG), *good, BIG) == L.ELIMIT
     empty = (None,) * 5 + (P, None, None, P)
     assert call("grouped_gemm_swiglu", S(S=0), *empty, BIG) == L.OK
@@ -91,6 +95,7 @@ def test_dense_rules():
         assert call(name, sh, -1, *good) == L.EINVAL
         assert call(name, sh, 1 << 31, *good) == L.EINVAL
         assert call(name, S(H=LONG), 4, *good) == L.ELIMIT
+        assert call(name, S(Hp=WIDE), 4, *good) == L.ELIMIT
         assert call(name, sh, 0, *(None,) * 6) == L.OK
     assert call("gemm_swiglu", S(Hp=48), 4, *(P,) * 6) == L.EINVAL
 
