@@ -331,7 +331,7 @@ def moonep_swiglu_backward(shape, h_saved, da, dh, stream=None):
         _p(da, 4 * NK * Hp, "da", _f32()), _p(dh, NK * 2 * Hp * eb, "dh", a), _s(stream)))
 
 
-# ---- router, gates' gradient, 8-bit checkpoints, 4-bit and 8-bit integer experts
+# ---- router, gates' gradient, 8-bit checkpoints, 4-bit experts
 #
 # These calls serve single tokens too, so the checks of _p are made in one expression per
 # tensor and the stream is asked for as a handle (a whole call's marshalling: 4-6 us).
@@ -572,147 +572,91 @@ def moonep_mx_grouped_gemm(shape, xq, xscales, src_index, wq, wscales, cu_seqlen
         raise MoonepError("moonep_mx_grouped_gemm", st)
 
 
+# ---- 8-bit integer experts
+
 def int_row_bytes(width: int) -> int:
     """Bytes of one 8-bit token row's values."""
     return 128 * -(-width // 128)
 
 
-def int_weight_bytes(H: int, Hp: int):
-    """Bytes of one expert's 8-bit values and of its column scales."""
-    cols = 16 * -(-Hp // 16)
-    return cols * int_row_bytes(H), 4 * cols
+# The calls below are checked and marshalled by the compiled binding (csrc/binding.cpp).
+_fast = None
+_INT_CALLS = ("quantize", "quantize_weight", "transpose_weight", "prefetch_weight", "grouped_gemm",
+              "grouped_gemm_swiglu", "gemm", "gemm_swiglu", "quantize_grad")
+
+
+def _int():
+    global _fast
+    if _fast is None:
+        import torch        # its libraries have to be there before the binding's
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError(f"{e}: build the binding with "
+                              "`python -m redundant_expert_balancing_amd.build`") from e
+        _binding.bind(tuple(ctypes.cast(getattr(lib(), "moonep_int_" + n), _vp).value
+                            for n in _INT_CALLS),
+                      torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _fast = _binding
+    return _fast
 
 
 def moonep_int_quantize(shape, rows, width, src, q, scales, stream=None):
-    d = _device()
-    rows, w = int(rows), int(width)
-    act, eb = _types(shape)
-    st = lib().moonep_int_quantize(
-        shape, rows, w, _q(src, rows * w * eb, "src", act, d),
-        _q(q, rows * int_row_bytes(w), "q", _torch.int8, d),
-        _q(scales, 4 * rows, "scales", _torch.float32, d), _h(stream, d))
+    st = (_fast or _int()).quantize(shape, rows, width, src, q, scales, stream)
     if st:
         raise MoonepError("moonep_int_quantize", st)
 
 
 def moonep_int_quantize_weight(shape, w, wq, wscales, stream=None):
-    d = _device()
-    E = shape.E
-    act, eb = _types(shape)
-    qb, sb = int_weight_bytes(shape.H, shape.Hp)
-    st = lib().moonep_int_quantize_weight(
-        shape, _q(w, E * shape.H * shape.Hp * eb, "w", act, d),
-        _q(wq, E * qb, "wq", _torch.int8, d), _q(wscales, E * sb, "wscales", _torch.float32, d),
-        _h(stream, d))
+    st = (_fast or _int()).quantize_weight(shape, w, wq, wscales, stream)
     if st:
         raise MoonepError("moonep_int_quantize_weight", st)
 
 
 def moonep_int_transpose_weight(shape, wq, wqt, stream=None):
-    d = _device()
-    E = shape.E
-    st = lib().moonep_int_transpose_weight(
-        shape, _q(wq, E * int_weight_bytes(shape.H, shape.Hp)[0], "wq", _torch.int8, d),
-        _q(wqt, E * int_weight_bytes(shape.Hp, shape.H)[0], "wqt", _torch.int8, d), _h(stream, d))
+    st = (_fast or _int()).transpose_weight(shape, wq, wqt, stream)
     if st:
         raise MoonepError("moonep_int_transpose_weight", st)
 
 
-def _int_weights(rows, H, W, wq, wscales, d, optional=False):
-    qb, sb = int_weight_bytes(H, W)
-    return (_q(wq, rows * qb, "wq", _torch.int8, d),
-            _q(wscales, rows * sb, "wscales", _torch.float32, d, optional))
-
-
-def _int_rows(rows, H, xq, xscales, d):
-    return (_q(xq, rows * int_row_bytes(H), "xq", _torch.int8, d),
-            _q(xscales, 4 * rows, "xscales", _torch.float32, d))
-
-
 def moonep_int_prefetch_weight(shape, replica_expert, wq, wscales, stream=None):
-    d = _device()
-    st = lib().moonep_int_prefetch_weight(
-        shape, _q(replica_expert, 4 * shape.R * shape.B, "replica_expert", _torch.int32, d),
-        *_int_weights(shape.E + shape.R * shape.B, shape.H, shape.Hp, wq, wscales, d, True),
-        _h(stream, d))
+    st = (_fast or _int()).prefetch_weight(shape, replica_expert, wq, wscales, stream)
     if st:
         raise MoonepError("moonep_int_prefetch_weight", st)
 
 
 def moonep_int_grouped_gemm(shape, xq, xscales, src_index, wq, wscales, cu_seqlens, c, ws,
                             stream=None):
-    d = _device()
-    N, E, B = shape.R * shape.S, shape.E, shape.B
-    NK = N * shape.K
-    i32 = _torch.int32
-    st = lib().moonep_int_grouped_gemm(
-        shape, *_int_rows(NK if src_index is None else N, shape.H, xq, xscales, d),
-        _q(src_index, 4 * NK, "src_index", i32, d, True),
-        *_int_weights(E + shape.R * B, shape.H, shape.Hp, wq, wscales, d, True),
-        _q(cu_seqlens, 4 * shape.R * (E + B + 1), "cu_seqlens", i32, d),
-        _q(c, 4 * NK * shape.Hp, "c", _torch.float32, d), *_ws(ws, d), _h(stream, d))
+    st = (_fast or _int()).grouped_gemm(shape, xq, xscales, src_index, wq, wscales, cu_seqlens, c,
+                                        ws, stream)
     if st:
         raise MoonepError("moonep_int_grouped_gemm", st)
 
 
 def moonep_int_grouped_gemm_swiglu(shape, xq, xscales, src_index, wq, wscales, cu_seqlens, act,
                                    h_saved, ws, stream=None):
-    d = _device()
-    N, E, B, Hp = shape.R * shape.S, shape.E, shape.B, shape.Hp
-    NK = N * shape.K
-    i32 = _torch.int32
-    at, eb = _types(shape)
-    st = lib().moonep_int_grouped_gemm_swiglu(
-        shape, *_int_rows(NK if src_index is None else N, shape.H, xq, xscales, d),
-        _q(src_index, 4 * NK, "src_index", i32, d, True),
-        *_int_weights(E + shape.R * B, shape.H, 2 * Hp, wq, wscales, d, True),
-        _q(cu_seqlens, 4 * shape.R * (E + B + 1), "cu_seqlens", i32, d),
-        _q(act, NK * Hp * eb, "act", at, d), _q(h_saved, NK * 2 * Hp * eb, "h_saved", at, d, True),
-        *_ws(ws, d), _h(stream, d))
+    st = (_fast or _int()).grouped_gemm_swiglu(shape, xq, xscales, src_index, wq, wscales,
+                                               cu_seqlens, act, h_saved, ws, stream)
     if st:
         raise MoonepError("moonep_int_grouped_gemm_swiglu", st)
 
 
 def moonep_int_gemm(shape, rows, xq, xscales, wq, wscales, add, c, stream=None):
-    d = _device()
-    rows, H, Hp = int(rows), shape.H, shape.Hp
-    f32 = _torch.float32
-    st = lib().moonep_int_gemm(
-        shape, rows, *_int_rows(rows, H, xq, xscales, d),
-        *_int_weights(1, H, Hp, wq, wscales, d, True),
-        _q(add, 4 * rows * Hp, "add", f32, d, True), _q(c, 4 * rows * Hp, "c", f32, d), _h(stream, d))
+    st = (_fast or _int()).gemm(shape, rows, xq, xscales, wq, wscales, add, c, stream)
     if st:
         raise MoonepError("moonep_int_gemm", st)
 
 
 def moonep_int_gemm_swiglu(shape, rows, xq, xscales, wq, wscales, act, h_saved, stream=None):
-    d = _device()
-    rows, H, Hp = int(rows), shape.H, shape.Hp
-    at, eb = _types(shape)
-    st = lib().moonep_int_gemm_swiglu(
-        shape, rows, *_int_rows(rows, H, xq, xscales, d),
-        *_int_weights(1, H, 2 * Hp, wq, wscales, d, True),
-        _q(act, rows * Hp * eb, "act", at, d),
-        _q(h_saved, rows * 2 * Hp * eb, "h_saved", at, d, True), _h(stream, d))
+    st = (_fast or _int()).gemm_swiglu(shape, rows, xq, xscales, wq, wscales, act, h_saved, stream)
     if st:
         raise MoonepError("moonep_int_gemm_swiglu", st)
 
 
 def moonep_int_quantize_grad(shape, src, src_index, gates, wscales, cu_seqlens, q, scales,
                              stream=None):
-    d = _device()
-    N, E, B, Hp = shape.R * shape.S, shape.E, shape.B, shape.Hp
-    NK = N * shape.K
-    at, eb = _types(shape)
-    i32, f32 = _torch.int32, _torch.float32
-    rows = 1 if cu_seqlens is None else E + shape.R * B
-    st = lib().moonep_int_quantize_grad(
-        shape, _q(src, (NK if src_index is None else N) * Hp * eb, "src", at, d),
-        _q(src_index, 4 * NK, "src_index", i32, d, True), _q(gates, 4 * NK, "gates", f32, d, True),
-        _q(wscales, rows * int_weight_bytes(1, Hp)[1], "wscales", f32, d),
-        _q(cu_seqlens, 4 * shape.R * (E + B + 1), "cu_seqlens", i32, d, True),
-        _q(q, NK * int_row_bytes(Hp), "q", _torch.int8, d), _q(scales, 4 * NK, "scales", f32, d),
-        _h(stream, d))
+    st = (_fast or _int()).quantize_grad(shape, src, src_index, gates, wscales, cu_seqlens, q,
+                                         scales, stream)
     if st:
         raise MoonepError("moonep_int_quantize_grad", st)
 

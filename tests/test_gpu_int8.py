@@ -104,6 +104,43 @@ def test_weights_there_and_back(dtype, H, Hp):
         assert np.array_equal(wt[e].cpu().numpy(), I.pack_weight(q.T))
 
 
+def test_binding_refusals():
+    """What must not reach a kernel as an address is refused before the call."""
+    say("int refusals")
+    sh = _shape(128, 64, S=4, E=1)
+    x = torch.zeros((4, 128), device="cuda", dtype=torch.bfloat16)
+    q, s = int8.buffers(4, 128)
+    call = lambda **k: L.moonep_int_quantize(sh, *[{**dict(rows=4, width=128, src=x, q=q, scales=s), **k}[n]      # noqa: E731
+                                                   for n in ("rows", "width", "src", "q", "scales")])
+    call()
+    for k, why in ((dict(src=x.float()), "dtype"), (dict(src=x.cpu()), "GPU tensor"),
+                   (dict(src=x.t()), "contiguous"), (dict(rows=5), "bytes"), (dict(q=None), "required"),
+                   (dict(q=q[:, :64].contiguous()), "bytes"), (dict(scales=s.double()), "dtype")):
+        with pytest.raises(ValueError, match=why):
+            call(**k)
+    for k in (dict(rows=-1), dict(width=120 + 4), dict(width=1 << 40, src=None)):
+        with pytest.raises((ValueError, L.MoonepError)):
+            call(**k)
+    with pytest.raises(TypeError):
+        L.moonep_int_quantize(object(), 4, 128, x, q, s)
+    with pytest.raises(ValueError):
+        L.moonep_int_quantize(sh, "four", 128, x, q, s)
+    with pytest.raises(TypeError):
+        L.moonep_int_quantize(sh, 4, None, x, q, s)
+    c = torch.zeros((4, 64), device="cuda")
+    wq, ws = int8.weight_buffers(1, 128, 64)
+    wq.zero_(), ws.zero_()
+    L.moonep_int_gemm(sh, 4, q, s, wq, None, None, c)
+    with pytest.raises(ValueError, match="wq"):
+        L.moonep_int_gemm(sh, 4, q, s, wq[:, :2].contiguous(), None, None, c)
+    with pytest.raises(ValueError, match="add"):
+        L.moonep_int_gemm(sh, 4, q, s, wq, None, c[:3], c)
+    with pytest.raises(L.MoonepError) as e:
+        L.moonep_int_quantize_grad(sh, x[:, :64].contiguous(), None, None, ws, None, q, s)
+    assert e.value.status == L.EMODE
+    torch.cuda.synchronize()
+
+
 def _layer(cfg, alpha, seed=0):
     r = make_routing(cfg, 3.0, seed=seed, alpha=alpha)
     d = make_dense(cfg, "cuda", seed, which=("x", "W"))
