@@ -1319,8 +1319,11 @@ static int launch_small(const IntArgs& a, int grid, hipStream_t strm) {
 //     2048: 299/134/74/83, 4096: 595/259/142/89
 //   dense (7168, 512): 32: 13/15/31/42, 64: 22/15/33/49, 2048: 43/22/36/71, 4096: 81/40/37/79, 16384:
 //     306/145/83/90
+//   tiny: grouped 16 x (80, 104), 47 rows: 4.0/6.4, 16 x (64, 136), 32: 4.0/6.2, dense (512, 512), 64:
+//     4.8/4.8, 256: 5.2/5.1, 1024: 13/8.4
 // So: few rows up to 8 each (a dense product, which reads its one weight from the caches, up to
-// 32); 256-row tiles from 64 rows each on, if they are more than half as many as the CUs; below,
+// 32), and where the workgroups have at most one item each and a wavefront's share of one is
+// short (96 blocks of 16 rows by 64 k); 256-row tiles from 64 rows each on, if they are more than half as many as the CUs; below,
 // 128-row tiles if those are, else 64-row tiles.
 template <int OUT>
 static int int_product(IntArgs a, const moonep_shape& s, void* ws, hipStream_t strm) {
@@ -1331,7 +1334,11 @@ static int int_product(IntArgs a, const moonep_shape& s, void* ws, hipStream_t s
   auto tiles = [&](int64_t bt) { return (a.NK + bt / 2 * segs + bt - 1) / bt * ((int64_t(a.W) + bt - 1) / bt); };
   // 32-bit offsets of gathered rows, and the order of tiles over the XCDs
   const bool fits = cus % 8 == 0 && (!a.src_index || a.xrows * a.KB * 64 < int64_t(kOffNone));
-  if (fits && a.NK > (a.cu ? 8 : 32) * segs) {
+  const int64_t each = (a.NK + segs - 1) / segs;      // rows per weight row
+  const bool few = each <= (a.cu ? 8 : 32) ||
+                   (segs * ((a.NB + 1) / 2) * ((each + kIntRows - 1) / kIntRows) <= 4 * cus &&
+                    a.KB * ((each + 15) / 16) <= 96);
+  if (fits && !few) {
     if (a.NK >= 64 * segs && tiles(IntTile::BM) > cus / 2 &&
         // 32-bit offsets of a tile's outputs, and tile numbers
         int64_t(IntTile::BM) * a.W * 4 <= int64_t(kOffNone) &&
