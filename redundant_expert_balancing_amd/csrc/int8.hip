@@ -74,8 +74,8 @@ __device__ inline void int_store(int8_t* at, const int* w) {
 // the whole number in the sum's low bits, so a value takes three more operations than its
 // packing: the sum, the whole number back, and the remainder, whose largest magnitude tells
 // whether any value of the lane is so near a border that the sum may have chosen the wrong side
-// (then, rarely, all of them are rounded the long way). 65536 bfloat16 rows of 4096: with
-// every value the long way the kernel was bound by its instructions (146 us).
+// (then, rarely, all of them are rounded the long way). 65536 bfloat16 rows of 4096: 146 us with
+// every value the long way, bound by its instructions; 127 us so.
 template <int N, bool STREAM = false>
 __device__ inline void int_round_store(int8_t* at, const float* v, float s, float inv) {
   constexpr float kMagic = 0x1.8p23f;
@@ -142,7 +142,9 @@ struct RowVec {
 constexpr int int_threads(int wpr) { return wpr == 1 ? kIntThreads : 64 * wpr; }
 
 // A row is held in registers between the maximum and the rounding: WPR wavefronts per row, VPL
-// vectors a lane; VPL 0: rows too wide for that are read twice.
+// vectors a lane; VPL 0: rows too wide for that are read twice. Bound by HBM: 65536 bfloat16 rows of
+// 4096 123-127 us, 0.81 GB at 6.5 TB/s; 16384 of 7168 55-58 us, 6.3 TB/s (one wavefront a row, 16
+// vectors a lane: 116); one row of 4096 2-4 us, most of it the launch (one wavefront: 6.8).
 template <bool BF16, int WPR, int VPL>
 __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_kernel(const uint4* __restrict__ src,
                                                                         int64_t rows, int nvec, int nout,
@@ -699,6 +701,19 @@ __global__ __launch_bounds__(kIntWaves * 64) void int_gemm_kernel(IntArgs a, int
 // of its stage is done, and the DMAs of the step after next are issued between the MFMAs behind
 // it (in one burst they held up the wavefront's MFMAs: 3% slower). The next tile's rows and
 // scales are looked up during a tile, and its first step is loaded under the tile's epilogue.
+//
+// 524288 slots of 65536 tokens, 256 experts, H = 4096, H' = 1536: 2.93-3.0 ms, 2.2 Pop/s; gate/up
+// with SwiGLU, 262144 slots, H = 4096, 2H' = 2816, pre-activation kept: 2.62-2.67 ms, 2.3; dense
+// 16384 x 7168 x 4096 with SwiGLU 353 us, 2.7; 262144 x 4096 x 1408 1.40-1.44 ms, 2.1; dense 16384 x
+// 2048 x 7168 with an added tile 298 us, 1.6. (The library's dense int8 product with an int32
+// result reached 2.2 at 65536 x 4096 x 1536, 2.0 at 16384 x 7168 x 4096.) Bound by power and by the
+// operands' way into LDS together: the matrix pipes are busy 0.575 of the cycles at 1.78 GHz
+// (0.67 at 1.92 for the dense product); with operands of zeros the first case takes 8% less, with
+// no loads at all two thirds of the time. Short reductions are bound by the output, whose
+// stores all tiles of a round send at once: 16384 x 2048 x 7168 takes 235 us without stores.
+// No gain or slower: steps of 64 k in four stages (4%), 128 x 256 tiles in two workgroups a CU
+// (18%), L2 prefetch of either operand (7 to 12%), cache policies of the loads, other tile
+// orders (within 1%), staggered starts (dense with an add 4% faster, others slower).
 constexpr int kNonTemporal = 2;   // buffer cache policy: the output is not read back here
 
 struct IntTile {
