@@ -207,14 +207,14 @@ struct IntGradArgs {
 };
 
 // The view row of position pos of a rank: the last i with cu[i] <= pos, or -1 behind the last
-// row. Each step looks at 64 entries at once.
+// row and ahead of the first. Each step looks at 64 entries at once.
 __device__ inline int segment_of(const int32_t* cu, int EB, int pos, int lane) {
   int lo = 0, n = EB + 1;
   while (n > 1) {
     const int stride = (n + 63) / 64;
     const int at = lane * stride;
     const uint64_t le = __ballot(at < n && cu[min(lo + at, EB)] <= pos);
-    if (le == 0) return -1;       // not a plan's cu_seqlens, which begin at 0
+    if (le == 0) return -1;
     const int c = 63 - __clzll(le);
     lo += c * stride;
     n = min(stride, n - c * stride);
@@ -277,9 +277,11 @@ __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(Int
         if (a.cu) {
           const int rank = p / a.SK, EB = a.E + a.B;
           const int32_t* cu = a.cu + int64_t(rank) * (EB + 1);
-          const int seg = segment_of(cu, EB, p - rank * a.SK, lane);
+          const int pos = p - rank * a.SK, seg = segment_of(cu, EB, pos, lane);
           wrow = __builtin_amdgcn_readfirstlane(seg < 0 ? -1 : seg < a.E ? seg : a.E + rank * a.B + (seg - a.E));
-          until = int64_t(rank) * a.SK + __builtin_amdgcn_readfirstlane(seg < 0 ? a.SK : cu[seg + 1]);
+          // outside the rows: up to the first one, or to the end of the rank
+          const int end = seg >= 0 ? cu[seg + 1] : pos < cu[0] ? cu[0] : a.SK;
+          until = int64_t(rank) * a.SK + __builtin_amdgcn_readfirstlane(end);
         }
         if constexpr (VPL > 0) {
           const v4f_t* from = reinterpret_cast<const v4f_t*>(a.ws + int64_t(max(wrow, 0)) * a.wscols);

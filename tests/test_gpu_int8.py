@@ -419,6 +419,28 @@ def test_gradient_rows(R, S, E, K, Hp, dtype):
     check(q, s, _np(dh), np.float32(1), np.ones(NK, bool), None)
 
 
+@pytest.mark.parametrize("Hp", [200, 8200])
+def test_gradient_rows_ahead_of_the_first(Hp):
+    """Positions ahead of a rank's first row are left as they were, the ones behind it are not."""
+    say("int gradient rows ahead", Hp)
+    R, S, E = 2, 12, 4
+    sh = _shape(64, Hp, S=S, E=E, K=2, mode=L.TRAIN, R=R)
+    g = torch.Generator("cuda").manual_seed(Hp)
+    dh = torch.randn((R * S * 2, Hp), device="cuda", generator=g).bfloat16()
+    wsc = torch.ones((2 * E, 16 * -(-Hp // 16)), device="cuda")
+    cu = torch.tensor([[5, 5, 9, 9, 9, 20, 20], [0, 3, 7, 11, 15, 20, 24]], dtype=torch.int32, device="cuda")
+    q, s = int8.buffers(R * S * 2, Hp)
+    q0, s0 = int8.buffers(R * S * 2, Hp)
+    q.fill_(-86), s.fill_(NAN)
+    L.moonep_int_quantize(sh, R * S * 2, Hp, dh, q0, s0)      # scales of one: the same rows
+    L.moonep_int_quantize_grad(sh, dh, None, None, wsc, cu, q, s)
+    torch.cuda.synchronize()
+    out = torch.zeros(R * S * 2, dtype=torch.bool, device="cuda")
+    out[:5], out[20:24] = True, True
+    assert torch.equal(q[~out], q0[~out]) and torch.equal(s[~out], s0[~out])
+    assert bool((q[out] == -86).all()) and bool(torch.isnan(s[out]).all())
+
+
 def _ffn(cfg, shared=0, backward=False, seed=0):
     r = make_routing(cfg, 3.0, alpha=2.0, seed=seed)
     d = make_dense(cfg, "cuda", seed, which=("x", "W1", "W2"))
