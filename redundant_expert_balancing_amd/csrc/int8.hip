@@ -243,7 +243,7 @@ __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(Int
     const int count = int(min(int64_t(a.chunk), a.NK - begin));
     const int p0 = int(begin);
     // lane i: source row of position p0 + i (-1: none), its gate, and in the end its scale
-    int my_row = p0 + lane;
+    int my_row = int(uint32_t(p0) + uint32_t(lane));
     float my_gate = 1.0f, my_scale = 0.0f;
     bool my_live = false;
     if (a.src_index) {
