@@ -550,9 +550,8 @@ int moonep_int_prefetch_weight(const moonep_shape* shape, const int32_t* replica
  *                     they were
  * A position whose src_index is not in [0, N*K) counts as a row of zeros. The workspace is
  * shared with the layer's other calls. Calls with many rows per expert are fast only where
- * the gathered token rows (128*T bytes each) stay below 2 GiB in all and Hp is at most
- * 2097152: beyond either they run on the form for few rows, which reads each weight once
- * per 64 rows.
+ * the gathered token rows (128*T bytes each) stay below 2 GiB in all: beyond that they run on
+ * the form for few rows, which reads each weight once per 64 rows.
  */
 int moonep_int_grouped_gemm(const moonep_shape* shape, const int8_t* xq, const float* xscales,
                             const int32_t* src_index, const int8_t* wq, const float* wscales,

@@ -15,7 +15,7 @@ constexpr int kIntMaxK = 131072;             // 127 * 127 * 131072 < 2^31: sums 
 constexpr int kIntMaxCols = 1 << 24;
 constexpr float kIntLeast = 0x1p-126f;       // the smallest scale
 constexpr uint32_t kIntNan = 0x7FC00000u;
-constexpr int kIntFewRows = 2048;            // fewer rows share a workgroup or more each
+constexpr int kIntFewRows = 2048;            // fewer rows: as many wavefronts each as it takes
 constexpr int kIntChunk = 16;                // positions in a row of the gradient's rounding
 // Infinity Cache, 256 MiB: gradient rows beyond it are stored past the caches. 262144 rows of 4096
 // 504 -> 459 us, and the product that reads them loses nothing; in int_quantize_kernel 268 MB (65536
@@ -491,8 +491,9 @@ __device__ inline v4f_t added(v4f_t a, v4f_t b) {
 // The activation. float32 layers get swiglu_f32's bits. bfloat16 layers take the exponential and
 // the reciprocal from the hardware's instructions: off by at most (|g| + 8) * 2^-24 of the value
 // (g * log2(e) is rounded before the exponential), which the rounding to bfloat16 (2^-8) covers,
-// or |g u| * 2^-126 where the reciprocal falls below the normal numbers; and a third of swiglu_f32's instructions; with
-// those a tile's epilogue took half as long as its products at a reduction of 4096.
+// or |g u| * 2^-126 where the reciprocal falls below the normal numbers. It takes a third of
+// swiglu_f32's instructions, with which a tile's epilogue took half as long as its products
+// at a reduction of 4096.
 template <int OUT>
 __device__ inline float int_swiglu(float g, float u) {
   if constexpr (OUT == kIntSwigluF32) return swiglu_f32(g, u);
@@ -618,7 +619,8 @@ __device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v,
     for (int j = 0; j < J; ++j)
       if (col[j] < a.W) {
         const int64_t at = pos * a.W + col[j];
-        if constexpr (OUT == kIntFloatAdd) v[j] = added(v[j], *reinterpret_cast<const v4f_t*>(a.add + at));
+        if constexpr (OUT == kIntFloatAdd)
+          v[j] = added(v[j], *reinterpret_cast<const v4f_t*>(a.add + at));
         *reinterpret_cast<v4f_t*>(a.c + at) = v[j];
       }
   } else {
@@ -762,7 +764,7 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
   // The workgroups of one XCD take a contiguous run of tiles per round, first come first
   // served (position q of XCD x is tile (q / per) * G + x * per + q % per), a tile ahead;
   // without a queue in turn.
-  const int G = gridDim.x, xcd = blockIdx.x % 8, per = G / 8;
+  const int G = gridDim.x, xcd = blockIdx.x % 8, per = G / 8;      // a multiple of 8 (host)
   const bool dyn = a.qcnt != nullptr;
   auto claim = [&]() { return tid == 0 ? atomicAdd(a.qcnt + xcd, 1) : 0; };
   auto publish = [&](int q) { if (tid == 0) s_claim = (q / per) * G + xcd * per + q % per; };
@@ -782,11 +784,14 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
   // Looking a tile up, in two goes of DMA. First the rows' src_index and the columns' scales ..
   auto look_up = [&](const Place& p, int par) {
     if (GATHER && wid < T::BM / 64)
-      dma4(make_rsrc(a.src_index + p.rowbase, uint32_t(p.rows) * 4), uint32_t(tid) * 4, lds_addr(s_u) + wid * 256);
+      dma4(make_rsrc(a.src_index + p.rowbase, uint32_t(p.rows) * 4), uint32_t(tid) * 4,
+           lds_addr(s_u) + wid * 256);
     if (wid == T::BM / 64) {
-      if (a.ws) dma16(make_rsrc(a.ws + int64_t(p.wrow) * a.NB * 16 + p.n0, clamp_bytes((int64_t(a.NB) * 16 - p.n0) * 4)),
-                      uint32_t(lane) * 16, lds_addr(s_sw[par]));
-      else *reinterpret_cast<v4f_t*>(&s_sw[par][lane * 4]) = v4f_t{1.f, 1.f, 1.f, 1.f};
+      if (a.ws)
+        dma16(make_rsrc(a.ws + int64_t(p.wrow) * a.NB * 16 + p.n0, clamp_bytes((int64_t(a.NB) * 16 - p.n0) * 4)),
+              uint32_t(lane) * 16, lds_addr(s_sw[par]));
+      else
+        *reinterpret_cast<v4f_t*>(&s_sw[par][lane * 4]) = v4f_t{1.f, 1.f, 1.f, 1.f};
     }
   };
   // .. then, behind a barrier, each row's offset and scale.
@@ -829,14 +834,15 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
     if (i < T::A_DMAS)
       dma16(ars, va[i], uint32_t(k) * T::STEPB, st + (wid + T::WAVES * i) * 1024);
     else
-      dma16(brs, vb[i - T::A_DMAS], uint32_t(k) * 2048, st + T::A_BYTES + (wid + T::WAVES * (i - T::A_DMAS)) * 1024);
+      dma16(brs, vb[i - T::A_DMAS], uint32_t(k) * 2048,
+            st + T::A_BYTES + (wid + T::WAVES * (i - T::A_DMAS)) * 1024);
   };
   auto issue_all = [&](int k) {
 #pragma unroll
     for (int i = 0; i < T::DMAS; ++i) issue(k, i);
   };
 
-  int tau = (G % 8 == 0) ? xcd * per + blockIdx.x / 8 : blockIdx.x;
+  int tau = xcd * per + blockIdx.x / 8;
   if (dyn) {
     publish(claim());
     __syncthreads();
@@ -1010,7 +1016,8 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
           for (int h = 0; h < GOES; ++h) {
             uint32_t at, off;
             spot(chunks, h, i, ld, left, at, off);
-            add[h] = __builtin_bit_cast(v4f_t, __builtin_amdgcn_raw_buffer_load_b128(drs, off, 0, kNonTemporal));
+            add[h] = __builtin_bit_cast(v4f_t,
+                                        __builtin_amdgcn_raw_buffer_load_b128(drs, off, 0, kNonTemporal));
           }
         }
       };
@@ -1020,7 +1027,8 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
         char* buf = ex + (i & 1) * 32768;
         if (!idle) {
 #pragma unroll
-          for (int j = 0; j < FN; ++j) put(buf, 64, (col0 + j * 16 + 4 * ek) * 4, int_scaled(acc[i][j], sa[i], sw[j]));
+          for (int j = 0; j < FN; ++j)
+            put(buf, 64, (col0 + j * 16 + 4 * ek) * 4, int_scaled(acc[i][j], sa[i], sw[j]));
         }
         __syncthreads();
         if constexpr (OUT == kIntFloatAdd) {
@@ -1034,7 +1042,8 @@ __global__ __launch_bounds__(IntTile::THREADS) void int_gemm_tiled_kernel(IntArg
           if (i + 1 < FM) fetch(i + 1);
 #pragma unroll
           for (int h = 0; h < GOES; ++h)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i_t, out[h]), crs, off[h], 0, kNonTemporal);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i_t, out[h]), crs, off[h], 0,
+                                                   kNonTemporal);
         } else {
           flush(buf, chunks, i, crs, ld, left, stream);
         }
@@ -1340,15 +1349,17 @@ static int launch_small(const IntArgs& a, int grid, hipStream_t strm) {
 //     4.8/4.8, 256: 5.2/5.1, 1024: 13/8.4
 // So: few rows up to 8 each (a dense product, which reads its one weight from the caches, up to
 // 32), and where the workgroups have at most one item each and a wavefront's share of one is
-// short (96 blocks of 16 rows by 64 k); 256-row tiles from 64 rows each on, if they are more than half as many as the CUs; below,
-// 128-row tiles if those are, else 64-row tiles.
+// short (96 blocks of 16 rows by 64 k); 256-row tiles from 64 rows each on, if they are more than
+// half as many as the CUs; below, 128-row tiles if those are, else 64-row tiles.
 template <int OUT>
 static int int_product(IntArgs a, const moonep_shape& s, void* ws, hipStream_t strm) {
   const int cus = device_cus();
   if (cus <= 0) return MOONEP_EHIP;
   const int64_t segs = a.cu ? int64_t(s.E) + s.R : 1;      // a plan has at most this many segments
   a.xrows = a.src_index ? int64_t(s.R) * s.S : a.NK;
-  auto tiles = [&](int64_t bt) { return (a.NK + bt / 2 * segs + bt - 1) / bt * ((int64_t(a.W) + bt - 1) / bt); };
+  auto tiles = [&](int64_t bt) {
+    return (a.NK + bt / 2 * segs + bt - 1) / bt * ((int64_t(a.W) + bt - 1) / bt);
+  };
   // 32-bit offsets of gathered rows, and the order of tiles over the XCDs
   const bool fits = cus % 8 == 0 && (!a.src_index || a.xrows * a.KB * 64 < int64_t(kOffNone));
   const int64_t each = (a.NK + segs - 1) / segs;      // rows per weight row

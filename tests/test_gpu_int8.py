@@ -326,6 +326,17 @@ def test_swiglu_against_the_two_steps(rows, H, Hp, E, dtype):
     assert torch.equal(a1[:rows], a2[:rows]) and torch.equal(h1[:rows], h0[:rows])
     for got in (a1, a2, h1):
         assert bool(torch.isnan(got[rows:]).all())
+    # a row and a column whose scales are not numbers
+    hurt, part = xs.clone(), ws.clone()
+    hurt[rows // 2] = NAN
+    part[:, 33] = NAN                 # an up column, of intermediate column 1
+    L.moonep_int_grouped_gemm_swiglu(ffn, xq, hurt, None, wq, part, cu, a2, h1, work)
+    torch.cuda.synchronize()
+    want = torch.zeros((rows, Hp), dtype=torch.bool, device="cuda")
+    want[rows // 2], want[:, 1] = True, True
+    assert torch.equal(torch.isnan(a2[:rows]), want)
+    assert torch.equal(torch.where(want, 0, a2[:rows]), torch.where(want, 0, a1[:rows]))
+    L.moonep_int_grouped_gemm_swiglu(ffn, xq, xs, None, wq, ws, cu, a2, h1, work)
     if E > 1:
         return
     a1.fill_(NAN), h1.fill_(NAN)
