@@ -18,7 +18,7 @@ constexpr uint32_t kIntNan = 0x7FC00000u;
 constexpr int kIntFewRows = 2048;            // fewer rows: as many wavefronts each as it takes
 constexpr int kIntChunk = 16;                // positions in a row of the gradient's rounding
 // Infinity Cache, 256 MiB: gradient rows beyond it are stored past the caches. 262144 rows of 4096
-// 504 -> 459 us, and the product that reads them loses nothing; in int_quantize_kernel 268 MB (65536
+// 504 -> 456 us, and the product that reads them loses nothing; in int_quantize_kernel 268 MB (65536
 // rows of 4096) made no difference, and 117 MB (16384 of 7168) cost the product 25 us.
 constexpr int64_t kIntCache = int64_t(1) << 28;
 typedef float v4f_t __attribute__((ext_vector_type(4)));
@@ -226,10 +226,12 @@ __device__ inline int segment_of(const int32_t* cu, int EB, int pos, int lane) {
 // int_quantize_kernel rounds. WPR wavefronts (or each wavefront alone) take a chunk of positions
 // in a row: what is looked up per position is looked up by a lane each beforehand, the
 // columns' scales stay in registers while the expert is the same, and the next row is on its
-// way while one is rounded. VPL as there. 262144 positions of 32768 tokens, 4096 wide: 459 us,
+// way while one is rounded. VPL as there. 262144 positions of 32768 tokens, 4096 wide: 456 us,
 // 1.07 GB written and 2.1 GB of rows read (0.27 GB of them from HBM) at 7 TB/s; 504 us if the
-// output goes through the caches, 315 with every position on one token's row. Shares of all
-// experts at a time, so that the workgroups of an XCD read the same tokens: 502 us.
+// output goes through the caches, 302 with every position on one token's row (6.5 vector
+// instructions a value take 0.2 ms of it; the maximum of magnitudes as integers, one more: 318).
+// 128 shares of every expert in turn, so that the workgroups of an XCD read the same tokens:
+// 464 us, nine tenths of the requests still miss its L2.
 template <bool BF16, int WPR, int VPL, bool STREAM>
 __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(IntGradArgs a) {
   typedef RowVec<BF16> V;
@@ -309,10 +311,10 @@ __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(Int
         fetch(row);
       }
       if (wrow < 0) continue;       // behind the rank's last row; uniform for the row's wavefronts
-      uint32_t m = 0;
+      float largest = 0.0f;      // its maximum keeps a NaN
       auto most = [&](const float* h) {
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) m = max(m, int_mag(h[e]));
+        for (int e = 0; e < V::N; ++e) largest = __builtin_elementwise_maximum(largest, fabsf(h[e]));
       };
       auto take = [&](int c, float* h) {       // VPL 0
         const bool in_row = from_row >= 0 && c < a.nvec;
@@ -339,7 +341,7 @@ __global__ __launch_bounds__(int_threads(WPR)) void int_quantize_grad_kernel(Int
           most(v[0]);
         }
       }
-      const float s = int_scale(row_max<WPR>(m, part[turn]));
+      const float s = int_scale(row_max<WPR>(int_mag(largest), part[turn]));
       turn ^= 1;
       const float inv = int_inverse(s);
       int8_t* out = a.q + int64_t(p) * a.nout * V::N;
