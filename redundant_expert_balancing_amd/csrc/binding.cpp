@@ -60,9 +60,15 @@ struct Call {
     ok = false;
   }
 
-  int64_t integer(int i) {
+  // A whole number: anything with __index__ (numpy's among them), no float and no text.
+  int64_t integer(int i, const char* name) {
     if (!ok) return 0;
-    PyObject* v = PyNumber_Long(args[i]);
+    if (PyUnicode_Check(args[i]) || PyBytes_Check(args[i])) {
+      PyErr_Format(PyExc_ValueError, "%s: a whole number is required, got text", name);
+      ok = false;
+      return 0;
+    }
+    PyObject* v = PyNumber_Index(args[i]);
     const int64_t r = v ? PyLong_AsLongLong(v) : -1;
     Py_XDECREF(v);
     if (PyErr_Occurred()) ok = false;
@@ -167,7 +173,7 @@ PyObject* run(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, F body) {
 
 PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return run(args, n, 7, [](Call& c) {      // shape, rows, width, src, q, scales, stream
-    const int64_t rows = c.integer(1), width = c.integer(2);
+    const int64_t rows = c.integer(1, "rows"), width = c.integer(2, "width");
     void* src = c.tensor(3, "src", wide(rows) * width * c.element(), c.type());
     void* q = c.tensor(4, "q", rows * row_bytes(width), I8);
     void* scales = c.tensor(5, "scales", 4 * wide(rows), F32);
@@ -257,7 +263,7 @@ PyObject* grouped_gemm_swiglu(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return run(args, n, 9, [](Call& c) {      // shape, rows, xq, xscales, wq, wscales, add, c, stream
-    const int64_t rows = c.integer(1);
+    const int64_t rows = c.integer(1, "rows");
     const wide bytes = 4 * wide(rows) * c.sh.Hp;
     const Operands o(c, 2, false, rows, 1, c.sh.Hp);
     void* add = c.tensor(6, "add", bytes, F32, true);
@@ -271,7 +277,7 @@ PyObject* gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* gemm_swiglu(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return run(args, n, 9, [](Call& c) {      // shape, rows, xq, xscales, wq, wscales, act, h_saved, stream
-    const int64_t rows = c.integer(1);
+    const int64_t rows = c.integer(1, "rows");
     const wide bytes = wide(rows) * c.sh.Hp * c.element();
     const Operands o(c, 2, false, rows, 1, 2 * wide(c.sh.Hp));
     void* act = c.tensor(6, "act", bytes, c.type());

@@ -1,0 +1,36 @@
+"""The compiled binding of the 8-bit integer calls, on the CPU: what it takes as a number, and
+what it needs to be built."""
+import numpy as np
+import pytest
+import torch
+
+from redundant_expert_balancing_amd import _lib as L
+
+
+def _shape():
+    return L.Shape(4, 64, 16, 2, 4, 128, 64, L.TRAIN, L.BF16)
+
+
+CALLS = {
+    "quantize rows": lambda n: L.moonep_int_quantize(_shape(), n, 128, *(torch.zeros(4),) * 3),
+    "quantize width": lambda n: L.moonep_int_quantize(_shape(), 4, n, *(torch.zeros(4),) * 3),
+    "gemm": lambda n: L.moonep_int_gemm(_shape(), n, *(torch.zeros(4),) * 6),
+    "gemm_swiglu": lambda n: L.moonep_int_gemm_swiglu(_shape(), n, *(torch.zeros(4),) * 6),
+}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_numbers_are_whole_numbers(call):
+    """Nothing is cut to a whole number: a row count that came out as a float is refused."""
+    for bad in (4.0, 4.9, np.float32(4), torch.tensor(4.5), None, [4]):
+        with pytest.raises(TypeError):
+            CALLS[call](bad)
+    for bad in ("4", "four", b"4"):
+        with pytest.raises((TypeError, ValueError)) as e:
+            CALLS[call](bad)
+        assert "GPU tensor" not in str(e.value)
+    with pytest.raises(OverflowError):
+        CALLS[call](1 << 70)
+    for good in (4, True, np.int32(4), np.int64(4), torch.tensor(4)):        # on to the tensors
+        with pytest.raises(ValueError, match="GPU tensor"):
+            CALLS[call](good)
