@@ -562,8 +562,8 @@ int moonep_int_grouped_gemm(const moonep_shape* shape, const int8_t* xq, const f
  * Gate/up grouped GEMM on 8-bit operands with the SwiGLU in its epilogue: what
  * moonep_int_grouped_gemm (up shape) followed by moonep_swiglu gives, without the float32 h in
  * memory; the same bits but for a bfloat16 act, whose float32 value is off by at most
- * (|gate| + 8) * 2^-24 of itself, or |gate * up| * 2^-126, before it is rounded. shape is the ffn shape; operands as there, the weights [H, 2*Hp] with gate and up
- * columns interleaved.
+ * (1.25 |gate| + 8) * 2^-24 of itself, or |gate * up| * 2^-126, before it is rounded. shape is
+ * the ffn shape; operands as there, the weights [H, 2*Hp] with gate and up columns interleaved.
  *   act      out  dtype [R*SK, Hp];  h_saved  out  NULL or dtype [R*SK, 2*Hp]
  * Requires Hp a multiple of 32.
  */

@@ -109,7 +109,8 @@ __device__ inline float scale_value(uint32_t byte) {
 }
 
 // SwiGLU in float32: silu(g) * u with silu(g) = g / (1 + e^-g). Every kernel that
-// produces the activation calls this one function, so all of them agree bit for bit.
+// produces the activation calls this one function, so all of them agree bit for bit; but for
+// the bfloat16 activation of the 8-bit integer products (int_swiglu), which has a bound instead.
 __device__ inline float swiglu_f32(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 // Gate/up columns of the FFN's first projection are interleaved in blocks of

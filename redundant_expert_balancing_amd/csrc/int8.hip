@@ -491,11 +491,12 @@ __device__ inline v4f_t added(v4f_t a, v4f_t b) {
 }
 
 // The activation. float32 layers get swiglu_f32's bits. bfloat16 layers take the exponential and
-// the reciprocal from the hardware's instructions: off by at most (|g| + 8) * 2^-24 of the value
-// (g * log2(e) is rounded before the exponential), which the rounding to bfloat16 (2^-8) covers,
-// or |g u| * 2^-126 where the reciprocal falls below the normal numbers. It takes a third of
-// swiglu_f32's instructions, with which a tile's epilogue took half as long as its products
-// at a reduction of 4096.
+// the reciprocal from the hardware's instructions, each off by a unit in the last place: off by at
+// most (1.25 |g| + 8) * 2^-24 of the value, which the rounding to bfloat16 (2^-8) covers, or
+// |g u| * 2^-126 where the reciprocal falls below the normal numbers. The exponent's share is 1.23 |g|:
+// the product g * log2(e) is rounded (1) and the constant lies 0.224 * 2^-24 below log2(e). It takes a
+// third of swiglu_f32's instructions, with which a tile's epilogue took half as long as its
+// products at a reduction of 4096.
 template <int OUT>
 __device__ inline float int_swiglu(float g, float u) {
   if constexpr (OUT == kIntSwigluF32) return swiglu_f32(g, u);
