@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
@@ -23,9 +24,19 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")))
 
 
+def _hipcc() -> str:
+    return os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+
+
+def _host_compiler() -> str:
+    """CXX, or g++ where there is one, or the C++ compiler beside hipcc."""
+    return (os.environ.get("CXX") or shutil.which("g++")
+            or os.path.join(os.path.dirname(_hipcc()), "amdclang++"))
+
+
 def build_library(verbose: bool = False) -> str:
     """Compile every HIP source into libmoonep.so next to this file; return its path."""
-    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    hipcc = _hipcc()
     tmp = LIB + ".tmp"
     cmd = [hipcc, *HIP_FLAGS, "-I", os.path.join(ROOT, "include"), *sources(), "-o", tmp]
     if verbose:
@@ -49,7 +60,7 @@ def build_binding(verbose: bool = False) -> str:
     base = os.path.dirname(torch.__file__)
     inc = os.path.join(base, "include")
     tmp = BINDING + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+    cmd = [_host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-I", inc,
            "-I", os.path.join(inc, "torch", "csrc", "api", "include"),

@@ -34,3 +34,20 @@ def test_numbers_are_whole_numbers(call):
     for good in (4, True, np.int32(4), np.int64(4), torch.tensor(4)):        # on to the tensors
         with pytest.raises(ValueError, match="GPU tensor"):
             CALLS[call](good)
+
+
+@pytest.mark.slow
+def test_the_binding_builds_with_the_compiler_beside_hipcc(monkeypatch, tmp_path):
+    """No host compiler on the path: hipcc alone builds the library, so its own C++ compiler builds
+    the binding."""
+    import importlib.util
+
+    from redundant_expert_balancing_amd import build
+    monkeypatch.delenv("CXX", raising=False)
+    monkeypatch.setenv("PATH", str(tmp_path))
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    path = build.build_binding()
+    spec = importlib.util.spec_from_file_location("_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert all(hasattr(module, n) for n in ("bind", *L._INT_CALLS))
