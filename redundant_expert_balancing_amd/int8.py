@@ -167,7 +167,9 @@ class IntFFN(_IntBase):
 
     def quantise_weights(self, w1, w2, s1=None, s2=None, stream=None):
         """w1 dtype [E, H, 2H'], w2 dtype [E, H', H]: the home experts; s1 [H, 2*shared] and s2
-        [shared, H]: the shared expert."""
+        [shared, H]: the shared expert, of a layer that has one."""
+        if (s1 is None, s2 is None) != (not self.shared,) * 2:
+            raise ValueError("s1, s2: both, of a layer with a shared expert, and neither otherwise")
         L.moonep_int_quantize_weight(self.up, w1, self.w1q, self.w1s, stream)
         L.moonep_int_quantize_weight(self.down, w2, self.w2q, self.w2s, stream)
         if self.shared:

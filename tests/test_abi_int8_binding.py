@@ -51,3 +51,14 @@ def test_the_binding_builds_with_the_compiler_beside_hipcc(monkeypatch, tmp_path
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     assert all(hasattr(module, n) for n in ("bind", *L._INT_CALLS))
+
+
+def test_shared_weights_go_with_a_shared_expert():
+    """A layer without a shared expert does not drop its weights, one with it does not go without."""
+    from redundant_expert_balancing_amd.int8 import IntFFN
+    w = torch.zeros(4)
+    for shared, s1, s2 in ((0, w, w), (0, w, None), (0, None, w), (64, None, None), (64, w, None), (64, None, w)):
+        l = IntFFN.__new__(IntFFN)          # no GPU here: the rule comes before everything else
+        l.shared = shared
+        with pytest.raises(ValueError, match="shared expert"):
+            l.quantise_weights(w, w, s1, s2)
