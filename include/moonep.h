@@ -511,8 +511,9 @@ int moonep_mx_grouped_gemm(const moonep_shape* shape, const uint8_t* xq, const u
  * rows as in W_all: E home experts, then every rank's prefetch slots. H and Hp need not be
  * multiples of more than a shape's rule asks (8 for bfloat16, 4 for float32).
  * The products are summed in int32, which is exact; a reduction longer than 131072 could
- * overflow it and gives MOONEP_ELIMIT, as do more than 16777216 columns. A result is (sum * row scale) * column scale, in
- * float32 in this order.
+ * overflow it and gives MOONEP_ELIMIT, as do more than 16777216 columns. A byte of -128, which
+ * no call here writes, counts as -128; sums stay exact where one operand alone holds such bytes.
+ * A result is (sum * row scale) * column scale, in float32 in this order.
  */
 
 /* Quantise `rows` rows of `width` values (dtype) to token rows; width a multiple of 8

@@ -254,3 +254,30 @@ def test_token_rows_beyond_32_bit_offsets():
             want = (xq[at].double() @ q) * xs[at].double()[:, None] * ws[e].double()
             got = c[p:min(p + 2048, hi)].double()
             assert bool(((got - want).abs() <= 3.01 * U * want.abs() + TINY).all()), (e, p)
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_the_longest_sums_are_exact(rows):
+    """A reduction of 131072 whole numbers of the largest magnitude, -128 (which quantisation never
+    writes) in one of the operands: 127 * 128 * 131072 < 2^31."""
+    H, W = 131072, 16
+    say("int longest sums", rows)
+    sh = _shape(H, W, "fp32", rows, 1, 1)
+    xq = torch.full((rows, H), 127, dtype=torch.int8, device="cuda")
+    xq[1] = -127
+    xs = torch.ones(rows, device="cuda")
+    wq, _ = int8.weight_buffers(1, H, W)
+    wq.fill_(-128)
+    wq.view(H // 64, 64, 16)[:, 16:32] = 127            # a quarter of the k of every column
+    c = torch.full((rows, W), NAN, device="cuda")
+    L.moonep_int_gemm(sh, rows, xq, xs, wq, None, None, c)
+    torch.cuda.synchronize()
+    want = torch.full((rows, W), 127 * (127 - 3 * 128) * (H // 4), dtype=torch.float64).float().cuda()
+    want[1] *= -1
+    assert torch.equal(c, want)
+    wq.fill_(-128)
+    L.moonep_int_gemm(sh, rows, xq, xs, wq, None, None, c)
+    torch.cuda.synchronize()
+    want.fill_(float(np.float32(-127 * 128 * H)))
+    want[1] *= -1
+    assert torch.equal(c, want)
