@@ -549,7 +549,8 @@ __device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v,
   const int wrow = __builtin_amdgcn_readfirstlane(wrow_v);
   const int m0 = __builtin_amdgcn_readfirstlane(m0_v), t = __builtin_amdgcn_readfirstlane(t_v);
   const int rows = __builtin_amdgcn_readfirstlane(min(kIntRows, n - m0));
-  const int split = rows <= 16 ? WAVES : rows <= 32 ? WAVES / 2 : WAVES / 4;   // wavefronts per block of rows
+  // wavefronts per block of rows, at least two
+  const int split = rows <= 16 ? WAVES : rows <= 32 ? WAVES / 2 : WAVES / 4;
   const int part = w % split, r0 = w / split * 16;
   const bool work = r0 < rows;    // uniform
   const int64_t pos = int64_t(rowbase) + m0 + r0 + r16;
@@ -598,17 +599,15 @@ __device__ inline void int_few_rows(const IntArgs& a, int rowbase_v, int wrow_v,
       if (c0 + split * U < a.KB) weights(c0 + split * U);
     }
   }
-  if (split > 1) {       // uniform
-    if (part > 0)
+  if (part > 0)
 #pragma unroll
-      for (int j = 0; j < J; ++j) s_part[w - 1][j][lane] = acc[j];
-    __syncthreads();
-    if (part == 0)
-      for (int o = 1; o < split; ++o)
+    for (int j = 0; j < J; ++j) s_part[w - 1][j][lane] = acc[j];
+  __syncthreads();
+  if (part == 0)
+    for (int o = 1; o < split; ++o)
 #pragma unroll
-        for (int j = 0; j < J; ++j) acc[j] += s_part[w + o - 1][j][lane];
-    __syncthreads();     // read before the next entry's sums
-  }
+      for (int j = 0; j < J; ++j) acc[j] += s_part[w + o - 1][j][lane];
+  __syncthreads();     // read before the next entry's sums
   if (!store) return;
   v4f_t v[J];
   int col[J];
