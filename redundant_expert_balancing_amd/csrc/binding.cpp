@@ -1,7 +1,7 @@
 // Marshalling of the 8-bit integer experts' calls for Python: the checks of _lib.py's _q on every
 // tensor, the current stream's handle, and the call. These calls serve single tokens, where
-// the host's time counts: a call takes 3.1 us, nearly all of it the launch, against 5.2 (three
-// tensors) to 6.2 us (six) with the checks in Python; one token through a dense product 12.2 -> 8.2
+// the host's time counts: a call takes 3.1 us (3.7-3.9 on a slower host), nearly all of it the
+// launch, against 5.2 (three tensors) to 6.2 us (six) with the checks in Python; one token through a dense product 12.2 -> 8.2
 // us with the rounding of its row.
 //
 // bind(addresses, current_device, current_stream) hands over the loaded library's functions and

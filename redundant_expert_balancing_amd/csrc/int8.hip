@@ -708,14 +708,15 @@ __global__ __launch_bounds__(kIntWaves * 64) void int_gemm_kernel(IntArgs a, int
 // it (in one burst they held up the wavefront's MFMAs: 3% slower). The next tile's rows and
 // scales are looked up during a tile, and its first step is loaded under the tile's epilogue.
 //
-// 524288 slots of 65536 tokens, 256 experts, H = 4096, H' = 1536: 2.93-3.0 ms, 2.2 Pop/s; gate/up
-// with SwiGLU, 262144 slots, H = 4096, 2H' = 2816, pre-activation kept: 2.62-2.67 ms, 2.3; dense
-// 16384 x 7168 x 4096 with SwiGLU 353 us, 2.7; 262144 x 4096 x 1408 1.40-1.44 ms, 2.1; dense 16384 x
-// 2048 x 7168 with an added tile 298 us, 1.6. (The library's dense int8 product with an int32
-// result reached 2.2 at 65536 x 4096 x 1536, 2.0 at 16384 x 7168 x 4096.) Bound by power and by the
-// operands' way into LDS together: the matrix pipes are busy 0.575 of the cycles at 1.78 GHz
-// (0.67 at 1.92 for the dense product); with operands of zeros the first case takes 8% less, with
-// no loads at all two thirds of the time. Short reductions are bound by the output, whose
+// Fastest and median pass: 524288 slots of 65536 tokens, 256 experts, H = 4096, H' = 1536 2.93-2.99
+// ms, 2.2 Pop/s; gate/up with SwiGLU, 262144 slots, H = 4096, 2H' = 2816, pre-activation kept
+// 2.62-2.67 ms, 2.3; dense 16384 x 7168 x 4096 with SwiGLU 353-374 us, 2.6; 262144 x 4096 x 1408
+// 1.40-1.44 ms, 2.1; dense 16384 x 2048 x 7168 with an added tile 298-321 us, 1.5; 65536 rows of a
+// reduction of 64 to 256 to 2048 columns 90-98 us, 5.5-5.9 TB/s written. (The library's dense int8
+// product with an int32 result reached 2.2 at 65536 x 4096 x 1536, 2.0 at 16384 x 7168 x 4096.) Bound
+// by power and by the operands' way into LDS together: the matrix pipes are busy 0.575 of the
+// cycles at 1.78 GHz (0.67 at 1.92 for the dense product); with operands of zeros the first case
+// takes 8% less, with no loads at all two thirds of the time. Short reductions are bound by the output, whose
 // stores all tiles of a round send at once: 16384 x 2048 x 7168 takes 235 us without stores.
 // No gain or slower: steps of 64 k in four stages (4%), 128 x 256 tiles in two workgroups a CU
 // (18%), L2 prefetch of either operand (7 to 12%), cache policies of the loads, other tile
@@ -1349,6 +1350,9 @@ static int launch_small(const IntArgs& a, int grid, hipStream_t strm) {
 //     306/145/83/90
 //   tiny: grouped 16 x (80, 104), 47 rows: 4.0/6.4, 16 x (64, 136), 32: 4.0/6.2, dense (512, 512), 64:
 //     4.8/4.8, 256: 5.2/5.1, 1024: 13/8.4
+//   skewed, 256 x (4096, 1536), 8 rows each on average, few rows / 128 x 128: all alike 264/280, a
+//     tenth of the rows on one expert 303/285, half 340/288, all of them 367/28 (the rule sees the
+//     average alone: the longest segment is known on the device)
 // So: few rows up to 8 each (a dense product, which reads its one weight from the caches, up to
 // 32), and where the workgroups have at most one item each and a wavefront's share of one is
 // short (96 blocks of 16 rows by 64 k); 256-row tiles from 64 rows each on, if they are more than
