@@ -1,8 +1,8 @@
 // Marshalling of the 8-bit integer experts' calls for Python: the checks of _lib.py's _q on every
 // tensor, the current stream's handle, and the call. These calls serve single tokens, where
 // the host's time counts: a call takes 3.1 us (3.7-3.9 on a slower host), nearly all of it the
-// launch, against 5.2 (three tensors) to 6.2 us (six) with the checks in Python; one token through a dense product 12.2 -> 8.2
-// us with the rounding of its row.
+// launch, against 5.2 (three tensors) to 6.2 us (six) with the checks in Python; one token through
+// a dense product 12.2 -> 8.2 us with the rounding of its row.
 //
 // bind(addresses, current_device, current_stream) hands over the loaded library's functions and
 // torch's two queries; each function below takes what the call of _lib.py of its name takes,
@@ -160,14 +160,20 @@ T* as(void* p) { return static_cast<T*>(p); }
 
 // The library's call, with Python's lock released: a launch waits where the GPU's queue is full,
 // and other threads (or a host function of the queue that needs the lock) have to go on. Releasing
-// and taking it again costs under 0.1 us a call.
+// and taking it again costs under 0.1 us a call. Taking it ends a daemon thread's stack where
+// the interpreter is on its way out, so that must not happen in a destructor.
 template <typename F, typename... A>
 int unlocked(F call, A... a) {
-  struct Lock {
-    PyThreadState* const state = PyEval_SaveThread();
-    ~Lock() { PyEval_RestoreThread(state); }
-  } lock;
-  return call(a...);
+  PyThreadState* const state = PyEval_SaveThread();
+  int st;
+  try {
+    st = call(a...);
+  } catch (...) {
+    PyEval_RestoreThread(state);
+    throw;
+  }
+  PyEval_RestoreThread(state);
+  return st;
 }
 
 // Runs a call's body; C++ exceptions (a tensor without storage, for one) become Python's.

@@ -96,3 +96,33 @@ def test_two_threads_on_streams_of_their_own():
     assert not errors
     for (_, _, _, c), ref in zip(jobs, want):
         assert torch.equal(c, ref)
+
+
+def test_a_daemon_thread_waits_in_a_call_while_python_ends():
+    """The thread's call returns after the interpreter has begun to go; the process ends as usual."""
+    import os
+    import subprocess
+    import sys
+    say("int daemon thread")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import ctypes, sys, threading, time, torch
+from redundant_expert_balancing_amd import _lib as L, int8
+fast = L._int()
+x = torch.zeros(64, dtype=torch.bfloat16, device="cuda")
+q, s = int8.buffers(1, 64)
+torch.cuda.synchronize()
+good = [ctypes.cast(getattr(L.lib(), "moonep_int_" + n), ctypes.c_void_p).value for n in L._INT_CALLS]
+sleep = ctypes.cast(ctypes.CDLL(None).nanosleep, ctypes.c_void_p).value
+fast.bind((sleep, *good[1:]), torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+wait = L.Shape(0, 0, 500_000_000, 0, 0, 64, 64, L.INFER, L.BF16)
+threading.Thread(target=lambda: fast.quantize(wait, 0, 64, x, q, s, None), daemon=True).start()
+time.sleep(0.1)
+class Last:
+    def __del__(self, sleep=time.sleep):
+        sleep(1.0)                       # past the end of the call
+sys.modules["last"] = Last()
+print("at the end", flush=True)
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0 and "at the end" in done.stdout, done.stderr
